@@ -192,7 +192,7 @@ def prepare(case, seed):
         if own:
             from expert_routed_grouped_amd import moe
             s["router"] = moe.moe_pack_router(s["w_router"])
-            s["ws"] = moe.moe_decode_layer_mx4_workspace(T, k, E, El, H, I)
+            s["ws"] = moe.moe_decode_layer_mx4_workspace(T, k, El, H, I)
             s["pgu"], s["pd"] = moe.moe_pack_mx4(*s["wgu"]), moe.moe_pack_mx4(*s["wd"])
         return s
     s["x"] = x.bfloat16()
