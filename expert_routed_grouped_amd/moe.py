@@ -7,6 +7,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -17,6 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP8, MOE_F32_ROUTER_PACKED = 0, 1, 2, 3, 4
+MOE_MXFP4 = 5
 MOE_FFN_GATHER, MOE_FFN_ZERO_Y, MOE_FFN_ONLY_GATE_UP, MOE_FFN_ONLY_DOWN = 1, 2, 4, 8
 MOE_FFN_PACKED_WEIGHTS = 16
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SHAPE", -3: "MOE_ERR_DTYPE", -4: "MOE_ERR_WORKSPACE",
@@ -27,9 +29,12 @@ EXPORTS = ("moe_version", "moe_status_str", "moe_route", "moe_permute", "moe_per
            "moe_ffn_workspace_size", "moe_grouped_ffn", "moe_combine", "moe_quantize_mx", "moe_ffn_mx_workspace_size",
            "moe_grouped_ffn_mx", "moe_shared_workspace_size", "moe_shared_expert", "moe_route_dispatch_workspace_size",
            "moe_route_dispatch", "moe_pack_weights", "moe_pack_router", "moe_grouped_ffn_noalloc",
-           "moe_decode_layer_workspace_size", "moe_decode_layer", "moe_workspace_size")
+           "moe_decode_layer_workspace_size", "moe_decode_layer", "moe_workspace_size", "moe_quantize_mx4",
+           "moe_dequantize_mx", "moe_mx4_packed_scale_bytes", "moe_pack_mx4", "moe_ffn_mx4_workspace_size",
+           "moe_grouped_ffn_mx4")
 MOE_OP_PERMUTE, MOE_OP_GROUPED_FFN, MOE_OP_GROUPED_FFN_F32, MOE_OP_GROUPED_FFN_MX = 0, 1, 2, 3
 MOE_OP_ROUTE_DISPATCH, MOE_OP_DECODE_LAYER, MOE_OP_SHARED_EXPERT, MOE_OP_SHARED_EXPERT_F32 = 4, 5, 6, 7
+MOE_OP_GROUPED_FFN_MX4 = 8
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -93,6 +98,19 @@ def lib():
         L.moe_pack_weights.argtypes = [P, I, I, I, I, P, P]
         L.moe_pack_router.restype = I
         L.moe_pack_router.argtypes = [P, I, I, I, P, P]
+        L64 = ctypes.c_int64
+        L.moe_quantize_mx4.restype = I
+        L.moe_quantize_mx4.argtypes = [P, I, L64, I, P, P, P]
+        L.moe_dequantize_mx.restype = I
+        L.moe_dequantize_mx.argtypes = [P, P, I, L64, I, P, I, P]
+        L.moe_mx4_packed_scale_bytes.restype = Z
+        L.moe_mx4_packed_scale_bytes.argtypes = [L64, I]
+        L.moe_pack_mx4.restype = I
+        L.moe_pack_mx4.argtypes = [P, P, L64, I, P, P, P]
+        L.moe_ffn_mx4_workspace_size.restype = Z
+        L.moe_ffn_mx4_workspace_size.argtypes = [I, I, I, I, I, I]
+        L.moe_grouped_ffn_mx4.restype = I
+        L.moe_grouped_ffn_mx4.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, P, P, P, P, P, I, P, Z, P]
         _lib = L
     return _lib
 
@@ -402,3 +420,140 @@ def moe_decode_layer(x: torch.Tensor, w_router: torch.Tensor, bias: Optional[tor
 def decode_layer_error_word(workspace: torch.Tensor) -> int:
     """The diagnostic word of a moe_decode_layer workspace (nonzero: a wait in the kernel gave up)."""
     return int(workspace[16:20].view(torch.int32).item())
+
+
+# ---- MXFP4 (include/moe.h, the *_mx4 calls) ----
+# The C ABI cannot see buffer sizes, so the shapes, types and devices of every tensor are checked here.
+def _need(t: torch.Tensor, name: str, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _on(t: torch.Tensor):
+    """The device of a GPU tensor as the current one, so that the call runs there on its current stream."""
+    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+
+
+def _out_dtype(dtype) -> int:
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported output dtype {dtype}")
+    return MOE_F32 if dtype == torch.float32 else MOE_BF16
+
+
+def moe_quantize_mx4(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                     stream=None):
+    """MXFP4 quantisation of a [rows, K] fp32/bf16 tensor -> (codes uint8 [rows, K/2], scales uint8 [rows, K/32])."""
+    rows, K = x.shape
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    with _on(x):
+        if codes is None:
+            codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+        _need(codes, "codes", torch.uint8, (rows, K // 2), x.device)
+        _need(scales, "scales", torch.uint8, (rows, K // 32), x.device)
+        _check("moe_quantize_mx4", lib().moe_quantize_mx4(_ptr(x), _dtype(x), rows, K, _ptr(codes), _ptr(scales),
+                                                          _stream(stream)))
+    return codes, scales
+
+
+def moe_dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None,
+                      dtype=torch.float32, stream=None) -> torch.Tensor:
+    """The values of MXFP4 codes [rows, K/2] or MXFP8 codes [rows, K] with scales [rows, K/32] (which of the two
+    follows from the widths) -> [rows, K] of ``dtype`` (fp32 or bf16)."""
+    rows, K = codes.shape[0], scales.shape[1] * 32
+    if codes.shape[1] not in (K, K // 2):
+        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are no MXFP4 or MXFP8 pair")
+    fp4 = codes.shape[1] == K // 2
+    with _on(codes):
+        if out is None:
+            out = torch.empty((rows, K), dtype=dtype, device=codes.device)
+        odt = _out_dtype(out.dtype)
+        _need(codes, "codes", torch.uint8, (rows, K // 2 if fp4 else K), codes.device)
+        _need(scales, "scales", torch.uint8, (rows, K // 32), codes.device)
+        _need(out, "out", out.dtype, (rows, K), codes.device)
+        _check("moe_dequantize_mx", lib().moe_dequantize_mx(_ptr(codes), _ptr(scales), MOE_MXFP4 if fp4 else MOE_MXFP8,
+                                                            rows, K, _ptr(out), odt, _stream(stream)))
+    return out
+
+
+def moe_pack_mx4(codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """MXFP4 weights [E, N, K/2] (or [N, K/2]) with scales [E, N, K/32] in the layout of moe_pack_mx4:
+    (codes uint8 [E, N/16, K/128, 1024], scales uint8 [E, N/16, ceil(K/512), 256]); without E for 2-D weights."""
+    if codes.dim() not in (2, 3) or scales.dim() != codes.dim():
+        raise ValueError("codes and scales must both be [E, N, ...] or [N, ...]")
+    lead, N, K = codes.shape[:-2], codes.shape[-2], codes.shape[-1] * 2
+    _need(codes, "codes", torch.uint8, (*lead, N, K // 2), codes.device)
+    _need(scales, "scales", torch.uint8, (*lead, N, K // 32), codes.device)
+    if N % 16 != 0 or K % 128 != 0:
+        raise MoEError("moe_pack_mx4", -2, "N must be a multiple of 16 and K of 128")
+    with _on(codes):
+        pc = torch.empty((*lead, N // 16, K // 128, 1024), dtype=torch.uint8, device=codes.device)
+        ps = torch.empty((*lead, N // 16, (K + 511) // 512, 256), dtype=torch.uint8, device=codes.device)
+        rows = (lead[0] if lead else 1) * N
+        _check("moe_pack_mx4", lib().moe_pack_mx4(_ptr(codes), _ptr(scales), rows, K, _ptr(pc), _ptr(ps),
+                                                  _stream(stream)))
+    return pc, ps
+
+
+def _mx4_weights(wgu, wd):
+    """Sizes (E_loc, H, I) of packed gate/up and down weights, each a (codes, scales) pair of moe_pack_mx4."""
+    (gc, gs), (dc, ds) = wgu, wd
+    if gc.dim() != 4 or dc.dim() != 4 or gc.shape[1] % 2 != 0:
+        raise ValueError("weights must be the (codes, scales) pairs of moe_pack_mx4, with experts in front")
+    El, H, I = gc.shape[0], gc.shape[2] * 128, gc.shape[1] * 8
+    dev = gc.device
+    _need(gc, "w_gate_up codes", torch.uint8, (El, 2 * I // 16, H // 128, 1024), dev)
+    _need(gs, "w_gate_up scales", torch.uint8, (El, 2 * I // 16, (H + 511) // 512, 256), dev)
+    _need(dc, "w_down codes", torch.uint8, (El, H // 16, I // 128, 1024), dev)
+    _need(ds, "w_down scales", torch.uint8, (El, H // 16, (I + 511) // 512, 256), dev)
+    return El, H, I
+
+
+def moe_ffn_mx4_workspace_size(T: int, k: int, E_loc: int, H: int, I: int, y_dtype: int = MOE_F32) -> int:
+    return int(lib().moe_ffn_mx4_workspace_size(T, k, E_loc, H, I, y_dtype))
+
+
+def moe_ffn_mx4_workspace(T: int, k: int, E_loc: int, H: int, I: int, dtype=torch.bfloat16,
+                          device="cuda") -> torch.Tensor:
+    """A workspace for moe_grouped_ffn_mx4 with output of ``dtype``."""
+    return torch.empty(moe_ffn_mx4_workspace_size(T, k, E_loc, H, I, _out_dtype(dtype)), dtype=torch.uint8,
+                       device=device)
+
+
+def moe_grouped_ffn_mx4(a_codes: torch.Tensor, a_scales: torch.Tensor, offsets: torch.Tensor, row_token: torch.Tensor,
+                        row_w: torch.Tensor, token_row: torch.Tensor, wgu, wd, y: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """SwiGLU expert FFN with MXFP4 weights and the gate-weighted sum to token order -> y [T, H] of ``dtype``
+    (overwritten).  Activations MXFP8 or MXFP4 (from the width of ``a_codes``); ``wgu`` and ``wd`` are the
+    (codes, scales) pairs of moe_pack_mx4; the maps are those of moe_permute."""
+    El, H, I = _mx4_weights(wgu, wd)
+    T, k = token_row.shape
+    dev = a_codes.device
+    fp4 = a_codes.shape[1] == H // 2
+    if row_token.numel() < T * min(k, El) or row_w.numel() < T * min(k, El):
+        raise ValueError(f"row_token and row_w must hold T * min(k, E_loc) = {T * min(k, El)} entries")
+    with _on(a_codes):
+        if y is None:
+            y = torch.empty((T, H), dtype=dtype, device=dev)
+        ydt = _out_dtype(y.dtype)
+        _need(a_codes, "a_codes", torch.uint8, (T, H // 2 if fp4 else H), dev)
+        _need(a_scales, "a_scales", torch.uint8, (T, H // 32), dev)
+        _need(offsets, "offsets", torch.int32, (El + 1,), dev)
+        _need(row_token, "row_token", torch.int32, row_token.shape, dev)
+        _need(row_w, "row_w", torch.float32, row_w.shape, dev)
+        _need(token_row, "token_row", torch.int32, (T, k), dev)
+        _need(wgu[0], "w_gate_up codes", torch.uint8, wgu[0].shape, dev)
+        _need(y, "y", y.dtype, (T, H), dev)
+        if workspace is None:
+            workspace = torch.empty(moe_ffn_mx4_workspace_size(T, k, El, H, I, ydt), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+        _check("moe_grouped_ffn_mx4", lib().moe_grouped_ffn_mx4(
+            _ptr(a_codes), _ptr(a_scales), MOE_MXFP4 if fp4 else MOE_MXFP8, _ptr(offsets), _ptr(row_token),
+            _ptr(row_w), _ptr(token_row), El, T, k, H, I, _ptr(wgu[0]), _ptr(wgu[1]), _ptr(wd[0]), _ptr(wd[1]),
+            _ptr(y), ydt, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return y

@@ -48,7 +48,9 @@
  *    fp32 per-output-channel scales), MOE_MXFP8 (OCP microscaling: E4M3 codes,
  *    uint8, plus one E8M0 scale byte 2^(s-127) per 32 consecutive values along
  *    the contraction axis, in a separate uint8 array [rows, K/32]; used by
- *    moe_quantize_mx and moe_grouped_ffn_mx).
+ *    moe_quantize_mx and moe_grouped_ffn_mx), MOE_MXFP4 (E2M1 codes, two per
+ *    byte with the even index in the low half, and the same E8M0 scales; used by
+ *    the *_mx4 calls).
  *  - Sizes: T >= 0 tokens, hidden H, E experts with 1 <= k <= min(E, 32),
  *    E <= 1024, intermediate I.  Local experts are [e_begin, e_end) with
  *    E_loc = e_end - e_begin >= 1; R_cap = T * min(k, E_loc) bounds the number
@@ -71,6 +73,7 @@ extern "C" {
 #define MOE_FP8_E4M3 2
 #define MOE_MXFP8 3
 #define MOE_F32_ROUTER_PACKED 4 /* router weight as written by moe_pack_router (moe_route_dispatch only) */
+#define MOE_MXFP4 5             /* OCP microscaling: E2M1 codes, two per byte, one E8M0 scale byte per 32 values */
 
 /* status codes */
 #define MOE_OK 0
@@ -99,6 +102,7 @@ extern "C" {
 #define MOE_OP_DECODE_LAYER 5     /* moe_decode_layer */
 #define MOE_OP_SHARED_EXPERT 6    /* moe_shared_expert with bf16 activations (I = I_s, E_loc and k unused) */
 #define MOE_OP_SHARED_EXPERT_F32 7 /* moe_shared_expert with fp32 activations */
+#define MOE_OP_GROUPED_FFN_MX4 8   /* moe_grouped_ffn_mx4 with fp32 output (enough for bf16 output too) */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int moe_version(void);
@@ -340,6 +344,99 @@ int moe_grouped_ffn_mx(const uint8_t *a_codes, const uint8_t *a_scales, const in
                        const uint8_t *wgu_codes, const uint8_t *wgu_scales, const uint8_t *wd_codes,
                        const uint8_t *wd_scales, float *y, float *y_perm, void *workspace,
                        size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
+ * moe_quantize_mx4 - MXFP4 quantisation of a row-major matrix along its rows.
+ *
+ * Defined by: "Hosting Qwen on Blackwell", section "Quantization" (4-bit microscaled formats beside the
+ * deployed MXFP8); the block rule is that of moe_quantize_mx for the E2M1 format (magnitudes 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6).
+ *
+ * For every row r and block b (values v = x[r, 32b .. 32b+31]):
+ *   amax = max |v|;  s = amax == 0 ? 0 : clamp(floor(log2 amax) - 2 + 127, 0, 254)
+ *   scales[r, b] = s;  code of v_i = E2M1 nearest to v_i / 2^(s-127), ties to the even code, magnitudes
+ *   above 6 saturate to 6, sign bit kept;  codes[r, (32b+i)/2] holds it in its low half for even i.
+ *   A block that holds a NaN or an infinity gets s = 255 (the E8M0 NaN) and zero codes: all of it reads
+ *   as NaN, in moe_dequantize_mx and in the products.
+ * x: rows x K, MOE_F32 or MOE_BF16, 16-byte aligned; codes [rows, K/2] uint8, 4-byte aligned; scales
+ * [rows, K/32] uint8.  K a multiple of 32, rows >= 0, rows * K < 2^40.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+int moe_quantize_mx4(const void *x, int x_dtype, int64_t rows, int K, uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * moe_dequantize_mx - the values that MXFP4 or MXFP8 codes stand for.
+ *
+ *   out[r, i] = value(codes[r], i) * 2^(scales[r, i/32] - 127); NaN where the scale is 255.
+ * mx_dtype: MOE_MXFP4 (codes [rows, K/2], 4-byte aligned) or MOE_MXFP8 (codes [rows, K], 8-byte aligned);
+ * out [rows, K] MOE_F32 (exact) or MOE_BF16 (exact except E4M3 results below 2^-133, which round to
+ * nearest even), 16-byte aligned.  A product past the largest fp32 value is infinite.  K a multiple of 32,
+ * rows >= 0, rows * K < 2^40.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+int moe_dequantize_mx(const uint8_t *codes, const uint8_t *scales, int mx_dtype, int64_t rows, int K, void *out,
+                      int out_dtype, void *stream);
+
+/* Bytes of packed scales moe_pack_mx4 writes for rows x K (rows a multiple of 16, K of 128; else 0). */
+size_t moe_mx4_packed_scale_bytes(int64_t rows, int K);
+
+/*
+ * moe_pack_mx4 - MXFP4 weights in the order the matrix cores take them.
+ *
+ * Same values, another order in memory, once when the weights are loaded; moe_grouped_ffn_mx4 and
+ * moe_decode_layer_mx4 read only this layout.  codes [rows, K/2] and scales [rows, K/32] row-major (rows
+ * count over all experts, E * N).  Rows go in groups of 16, group g = row / 16, n = row % 16:
+ *   codes: group g is K/128 blocks of 1024 bytes; the 16 bytes of k = 128c + 32q .. 128c + 32q + 31 are at
+ *     g * 8K + c * 1024 + (16q + n) * 16   (the same number of bytes as codes);
+ *   scales: group g is ceil(K/512) blocks of 256 bytes; the scale of that piece is at
+ *     (g * ceil(K/512) + c / 4) * 256 + (16q + n) * 4 + c % 4, and 0 where 128c >= K
+ *     (moe_mx4_packed_scale_bytes(rows, K) in all).
+ * One lane then owns one row and 32 of 128 k, and a wave reads 1 KB of codes and 256 bytes of scales
+ * contiguously.  rows a multiple of 16, K of 128; codes and both outputs 16-byte aligned; no two buffers may
+ * overlap.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (also for overlapping buffers), MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+int moe_pack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int K, uint8_t *packed_codes,
+                 uint8_t *packed_scales, void *stream);
+
+/*
+ * Bytes of workspace moe_grouped_ffn_mx4 needs (the intermediate and, for more than a few tokens, one row of
+ * y_dtype per assignment).  0 for sizes or types it does not take.
+ */
+size_t moe_ffn_mx4_workspace_size(int T, int k, int E_loc, int H, int I, int y_dtype);
+
+/*
+ * moe_grouped_ffn_mx4 - the SwiGLU expert FFN with MXFP4 weights, and the weighted sum to token order.
+ *
+ * Defined by: the passages of moe_grouped_ffn, with the 4-bit microscaled format of the "Quantization"
+ * section of "Hosting Qwen on Blackwell" for the weights.
+ *
+ * For each local expert i and each of its rows r in [offsets[i], offsets[i+1]), t = row_token[r]:
+ *   G, U  = w_gate_up[i, 0..I-1, :] . a_t,  w_gate_up[i, I..2I-1, :] . a_t
+ *   h_r   = silu(G) * U in fp32, quantised per row in blocks of 32 along I to a_dtype with the rule of
+ *           moe_quantize_mx4 / moe_quantize_mx (a block with a NaN or infinity reads as NaN)
+ *   o_r   = w_down[i] . h_r
+ *   y[t, :] = sum over the rows r of token t of row_w[r] * o_r, accumulated in fp32 and rounded once to
+ *             y_dtype.  The order of the sum is fixed by the routing, so the result is the same from run to
+ *             run; with MOE_BF16 output and more than 64 tokens each term is rounded to bf16 first.
+ * y [T, H] is overwritten; a token without a local row gets zeros.  The products run on the block-scaled
+ * matrix cores with fp32 sums.  With MOE_MXFP4 activations every product and its bits enter the sum; with
+ * MOE_MXFP8 the matrix cores align each group of eight neighbouring products to the largest of them and drop
+ * what lies more than 13 binary places below its leading one (about 1e-4 of a 4096-long sum of normal values,
+ * against the 3% steps of the E4M3 codes themselves).
+ *
+ * a: MOE_MXFP8 (codes [T, H]) or MOE_MXFP4 (codes [T, H/2]), scales [T, H/32], e.g. from moe_quantize_mx /
+ * moe_quantize_mx4.  offsets [E_loc+1], row_token, row_w [T * min(k, E_loc)] and token_row [T, k] as
+ * moe_permute writes them for the same T, k and local experts.  Weights as moe_pack_mx4 writes them:
+ * w_gate_up [E_loc, 2I, H] (rows 0..I-1 gate, I..2I-1 up), w_down [E_loc, H, I].  H and I multiples of 128,
+ * E_loc <= 1024, k <= 32; T * H, T * min(k, E_loc) * I below 2^31 and H * I below 2^30.  Pointers 16-byte
+ * aligned (a_scales 4-byte); workspace at least moe_ffn_mx4_workspace_size bytes, 256-byte aligned, any
+ * contents.  Calls that overlap in time must not share a workspace or y.  T == 0 enqueues nothing.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_WORKSPACE, MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+int moe_grouped_ffn_mx4(const uint8_t *a_codes, const uint8_t *a_scales, int a_dtype, const int32_t *offsets,
+                        const int32_t *row_token, const float *row_w, const int32_t *token_row, int E_loc, int T, int k,
+                        int H, int I, const uint8_t *wgu_codes, const uint8_t *wgu_scales, const uint8_t *wd_codes,
+                        const uint8_t *wd_scales, void *y, int y_dtype, void *workspace, size_t workspace_bytes,
+                        void *stream);
 
 /*
  * moe_combine - gate-weighted gather-sum of per-row outputs back to token order.
