@@ -14,7 +14,7 @@ struct Mx4Params {
   TileParams tp;               // offsets, row_token, row_w, El, H, I, R_cap, T; a / w / out: codes (out: rows for down)
   const uint8_t *a_scales;     // [rows, K/32]
   const uint8_t *w_scales;     // packed
-  uint8_t *out_scales;         // gate/up: h scales [R_cap, I/32]
+  uint8_t *out_scales;         // gate/up: h scales
 };
 
 constexpr int SM = 16;  // rows per tile
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void ffn_mx4_simple_kernel(Mx4Params p) {
   const int r = r0 + min(n, rows - 1);
   const size_t src = DOWN ? (size_t)r : (size_t)p.tp.row_token[r];
   const uint8_t *arow = (const uint8_t *)p.tp.a + src * mx4::code_bytes<FA>(K);
-  const uint8_t *srow = p.a_scales + src * (K / 32);
+  const uint8_t *srow = p.a_scales + src * (DOWN ? mx4::h_scale_stride(K) : (size_t)(K / 32));
   size_t group[4];
 #pragma unroll
   for (int g = 0; g < 4; g++)
@@ -43,7 +43,8 @@ __global__ __launch_bounds__(256) void ffn_mx4_simple_kernel(Mx4Params p) {
   for (int g = 0; g < 4; g++) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < K / 128; s++) {
     const v8i_t a = mx4::act_frag<FA>(arow, s, q);
-    const uint32_t sa = mx4::act_scale(srow, s, q);
+    const uint32_t sa = DOWN ? *(const uint32_t *)(srow + (size_t)(s >> 2) * 16 + 4 * q) >> (8 * (s & 3))
+                             : mx4::act_scale(srow, s, q);
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       const u32x4_t w = *(const u32x4_t *)((const uint8_t *)p.tp.w + group[g] * mx4::group_codes(K) +
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(256) void ffn_mx4_simple_kernel(Mx4Params p) {
 #pragma unroll
       for (int i = 0; i < 4; i++) v[g][i] = silu_fast(acc[g][i]) * acc[2 + g][i];
     mx4::store_h_block<FA>(v, on, (uint8_t *)p.tp.out + (size_t)r * mx4::code_bytes<FA>(p.tp.I),
-                           p.out_scales + (size_t)r * (p.tp.I / 32), c0, q);
+                           p.out_scales + (size_t)r * mx4::h_scale_stride(p.tp.I), c0, q);
   } else if (on) {
     const float w = p.tp.row_w[r];
 #pragma unroll
@@ -93,9 +94,9 @@ __global__ __launch_bounds__(256) void sum_rows_kernel(const void *__restrict__ 
   }
 }
 
-// Workspace: h codes [R_cap, I] (a byte each, half of it used by E2M1), h scales [R_cap, I/32], rows [R_cap, H].
+// Workspace: h codes [R_cap, I] (a byte each, half of it used by E2M1), h scales, rows [R_cap, H].
 size_t h_bytes(int R_cap, int I) { return align_up((size_t)R_cap * I, 256); }
-size_t hs_bytes(int R_cap, int I) { return align_up((size_t)R_cap * (I / 32), 256); }
+size_t hs_bytes(int R_cap, int I) { return align_up((size_t)R_cap * mx4::h_scale_stride(I), 256); }
 
 template <int FA, bool BF16>
 hipError_t launch(const FfnMx4Args &a, hipStream_t s) {
@@ -146,6 +147,10 @@ size_t ffn_mx4_ws_bytes(int R_cap, int H, int I, int y_bf16) {
 
 hipError_t launch_ffn_mx4(const FfnMx4Args &a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
+  if (a.T <= kMx4StreamMaxT) {
+    uint8_t *h = (uint8_t *)a.ws;
+    return launch_ffn_mx4_stream(a, h, h + h_bytes(a.R_cap, a.I), s);
+  }
   if (a.a_fp4) return a.y_bf16 ? launch<mx4::FP4, true>(a, s) : launch<mx4::FP4, false>(a, s);
   return a.y_bf16 ? launch<mx4::FP8, true>(a, s) : launch<mx4::FP8, false>(a, s);
 }

@@ -44,10 +44,10 @@ __device__ __forceinline__ v8i_t piece8(const u32x4_t &lo, const u32x4_t &hi) {
   return v8i_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
-// acc += weights (16 rows) x activations (16 tokens) over 128 k; byte J of sw and byte 0 of sa scale.
-template <int FA, int J>
+// acc += weights (16 rows) x activations (16 tokens) over 128 k; byte J of sw and byte JA of sa scale.
+template <int FA, int J, int JA = 0>
 __device__ __forceinline__ f32x4_t mfma(const v8i_t &w, const v8i_t &a, const f32x4_t &acc, uint32_t sw, uint32_t sa) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc, FP4, FA, J, (int)sw, 0, (int)sa);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc, FP4, FA, J, (int)sw, JA, (int)sa);
 }
 
 // One 128-k step of an activation row-major operand: row points at this lane's row.
@@ -64,6 +64,12 @@ __device__ __forceinline__ v8i_t act_frag(const uint8_t *row, int step, int q) {
 __device__ __forceinline__ uint32_t act_scale(const uint8_t *srow, int step, int q) {
   return *(const uint32_t *)(srow + 4 * (size_t)step) >> (8 * q);
 }
+
+// Scales of the intermediate h (workspace): per row ceil(I/512) pieces of 16 bytes; lane quarter q takes the dword
+// at 4 q of a piece, whose byte j is the scale of step j, as for the packed weights.
+__host__ __device__ __forceinline__ size_t h_scale_stride(int I) { return (size_t)((I + 511) / 512) * 16; }
+// Place of block b (columns 32b ..) in its row.
+__device__ __forceinline__ int h_scale_pos(int b) { return (b & ~15) + (b & 3) * 4 + ((b >> 2) & 3); }
 
 // Scale byte of a block from the bit pattern of its largest magnitude (the maximum over bit patterns
 // orders NaN above infinity above every finite value).  EMAX: exponent of the format's largest power of
@@ -93,7 +99,7 @@ __device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d
 
 // Quantise and store this lane's part of one 32-column block of the intermediate of one token:
 // v[g][r] is column 16 g + 4 q + r.  The four lanes (n, 0..3) of a token hold the block.  Every lane of the
-// wave takes part; ``on`` says whether the token exists.  hrow / srow: the token's code row and scale row.
+// wave takes part; ``on`` says whether the token exists.  hrow / srow: the token's code row and its scales.
 template <int FA>
 __device__ __forceinline__ void store_h_block(const float (&v)[2][4], bool on, uint8_t *hrow, uint8_t *srow, int col0,
                                               int q) {
@@ -116,7 +122,7 @@ __device__ __forceinline__ void store_h_block(const float (&v)[2][4], bool on, u
     if constexpr (FA == FP8) *(uint32_t *)(hrow + col) = s == 255 ? 0u : e4m3_quad(u[0], u[1], u[2], u[3]);
     else *(uint16_t *)(hrow + col / 2) = s == 255 ? (uint16_t)0 : (uint16_t)e2m1_quad(u[0], u[1], u[2], u[3]);
   }
-  if (q == 0) srow[col0 / 32] = (uint8_t)s;
+  if (q == 0) srow[h_scale_pos(col0 / 32)] = (uint8_t)s;
 }
 
 // Four neighbouring output values of one row, fp32 or rounded to bf16 (nearest even).
@@ -154,3 +160,8 @@ struct FfnMx4Args {
 };
 size_t ffn_mx4_ws_bytes(int R_cap, int H, int I, int y_bf16);
 hipError_t launch_ffn_mx4(const FfnMx4Args &a, hipStream_t s);
+// Weight-streaming path for few rows per expert (ffn_mx4_stream.hip), T <= kMx4StreamMaxT: h and its scales into
+// ``h`` / ``hs``, then the down half, which also sums to token order; launch_down_sum_mx4 is that half alone.
+constexpr int kMx4StreamMaxT = 64;
+hipError_t launch_ffn_mx4_stream(const FfnMx4Args &a, uint8_t *h, uint8_t *hs, hipStream_t s);
+hipError_t launch_down_sum_mx4(const FfnMx4Args &a, const uint8_t *h, const uint8_t *hs, hipStream_t s);

@@ -172,6 +172,9 @@ SHAPES = [
     (300, 4, 3, 384, 128, 0, 2, 0.0),
     (1100, 2, 1, 256, 384, 0, 2, 3.0),     # one expert with over 1024 rows
     (700, 40, 2, 128, 256, 3, 37, 0.0),    # odd expert range, few rows each
+    (64, 33, 32, 128, 128, 0, 33, 0.0),    # the most rows a small batch can have
+    (64, 1024, 2, 128, 128, 0, 1024, 0.0), # the most experts
+    (2, 64, 8, 128, 512, 0, 64, 0.0),
 ]
 
 
