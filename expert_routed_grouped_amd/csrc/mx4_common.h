@@ -37,10 +37,12 @@ constexpr int kBlk = 1024, kSblk = 256;
 __host__ __device__ __forceinline__ size_t group_codes(int K) { return (size_t)(K / 128) * kBlk; }
 __host__ __device__ __forceinline__ size_t group_scales(int K) { return (size_t)((K + 511) / 512) * kSblk; }
 
-__device__ __forceinline__ v8i_t piece4(const u32x4_t &p) {
+// By value: a component read through a reference would become a load without type information, and the compiler
+// then waits for every load into LDS in flight before it.
+__device__ __forceinline__ v8i_t piece4(const u32x4_t p) {
   return v8i_t{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
 }
-__device__ __forceinline__ v8i_t piece8(const u32x4_t &lo, const u32x4_t &hi) {
+__device__ __forceinline__ v8i_t piece8(const u32x4_t lo, const u32x4_t hi) {
   return v8i_t{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
@@ -158,7 +160,7 @@ struct FfnMx4Args {
   int y_bf16;
   void *ws;
 };
-size_t ffn_mx4_ws_bytes(int R_cap, int H, int I, int y_bf16);
+size_t ffn_mx4_ws_bytes(int T, int R_cap, int H, int I, int y_bf16);
 hipError_t launch_ffn_mx4(const FfnMx4Args &a, hipStream_t s);
 // Weight-streaming path for few rows per expert (ffn_mx4_stream.hip), T <= kMx4StreamMaxT: h and its scales into
 // ``h`` / ``hs``, then the down half, which also sums to token order; launch_down_sum_mx4 is that half alone.
