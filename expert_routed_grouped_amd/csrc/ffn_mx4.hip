@@ -53,22 +53,26 @@ struct Lay {
 
 struct Src {
   __amdgpu_buffer_rsrc_t ra, rw, rsa, rsw;  // activations, this expert's weights, and their scales
-  uint32_t aoff[4], woff[2];                // this lane's bytes of its wave's pieces at step 0
+  uint32_t off[6];                          // this lane's bytes of its wave's pieces at step 0, activations first
 };
 
-template <int FA, int BM, int SLOTI>
-__device__ __forceinline__ void load_step(const Src &src, int st, int wave, char *lds) {
+// Loads U0 .. U1 - 1 of the NL that this wave issues for step st into ring slot SLOTI (fewer activation pieces than
+// waves: some are fetched twice).
+template <int FA, int BM, int SLOTI, int U0, int U1>
+__device__ __forceinline__ void load_pieces(const Src &src, int st, int wave, char *lds) {
   using L = Lay<FA, BM>;
   const uint32_t sa = (uint32_t)st * L::AROW, sw = (uint32_t)st * mx4::kBlk;
 #pragma unroll
-  for (int u = 0; u < L::NA; u++)  // fewer pieces than waves: some are fetched twice
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        src.ra, (lds_void *)(lds + SLOTI * L::SLOT + (wave + NWV * u) % (L::A_BYTES / 1024) * 1024), 16, src.aoff[u], sa, 0,
-        0);
-#pragma unroll
-  for (int u = 0; u < 2; u++)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        src.rw, (lds_void *)(lds + SLOTI * L::SLOT + L::A_BYTES + (wave + NWV * u) * 1024), 16, src.woff[u], sw, 0, 0);
+  for (int u = U0; u < U1; u++) {
+    if (u < L::NA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          src.ra, (lds_void *)(lds + SLOTI * L::SLOT + (wave + NWV * u) % (L::A_BYTES / 1024) * 1024), 16, src.off[u],
+          sa, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          src.rw, (lds_void *)(lds + SLOTI * L::SLOT + L::A_BYTES + (wave + NWV * (u - L::NA)) * 1024), 16, src.off[u],
+          sw, 0, 0);
+  }
 }
 
 // MODE 0: gate/up + SwiGLU -> h.  MODE 1: down -> gated rows.  NB: 16-row blocks of this wave.
@@ -102,7 +106,7 @@ __device__ __forceinline__ void body(const Mx4Params &mp, const Src &src, int K,
   scales(wsn, asn, 0);
   asm volatile("" ::: "memory");
   [&]<int... D>(std::integer_sequence<int, D...>) __attribute__((always_inline)) {
-    (load_step<FA, BM, D>(src, min(D, nstep - 1), wave, lds), ...);
+    (load_pieces<FA, BM, D, 0, L::NL>(src, min(D, nstep - 1), wave, lds), ...);
   }(std::make_integer_sequence<int, L::RD - 1>{});
   // step kt = IDX modulo PER: ring slot and scale byte are compile-time constants
   constexpr int PER = L::RD % 4 == 0 ? L::RD : L::RD % 2 == 0 ? 2 * L::RD : 4 * L::RD;
@@ -130,14 +134,19 @@ __device__ __forceinline__ void body(const Mx4Params &mp, const Src &src, int K,
 #pragma unroll
     for (int g = 0; g < 4; g++) w[g] = mx4::piece4(*(const u32x4_t *)(lds + wbase + (S * L::SLOT + g * 1024)));
     a[0] = act(0);
-    load_step<FA, BM, SN>(src, min(kt + L::RD - 1, nstep - 1), wave, lds);
-#pragma unroll
-    for (int i = 0; i < NB; i++) {
-      if (i + 1 < NB) a[(i + 1) & 1] = act(i + 1);
-      __builtin_amdgcn_sched_barrier(0);  // the next operand is on its way while this one is multiplied
+    const int stn = min(kt + L::RD - 1, nstep - 1);
+    // block i: fetch the next operand and a share of the coming step, then multiply
+    auto block = [&](auto I) __attribute__((always_inline)) {
+      constexpr int i = decltype(I)::value;
+      if constexpr (i + 1 < NB) a[(i + 1) & 1] = act(i + 1);
+      load_pieces<FA, BM, SN, L::NL * i / NB, L::NL *(i + 1) / NB>(src, stn, wave, lds);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int g = 0; g < 4; g++) acc[i][g] = mx4::mfma<FA, j, j>(w[g], a[i & 1], acc[i][g], ws[g], as[i]);
-    }
+    };
+    [&]<int... I>(std::integer_sequence<int, I...>) __attribute__((always_inline)) {
+      (block(std::integral_constant<int, I>{}), ...);
+    }(std::make_integer_sequence<int, NB>{});
   };
   for (int kt = 0; kt < nstep; kt += PER)
     [&]<int... IDX>(std::integer_sequence<int, IDX...>) __attribute__((always_inline)) {
@@ -214,11 +223,11 @@ __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
 #pragma unroll
   for (int u = 0; u < L::NA; u++) {
     const int b = (wave + NWV * u) % (L::A_BYTES / 1024);
-    src.aoff[u] = FA == mx4::FP8 ? a_row(b * 8 + (lane & 7)) * arb + (uint32_t)(lane >> 3) * 16u
+    src.off[u] = FA == mx4::FP8 ? a_row(b * 8 + (lane & 7)) * arb + (uint32_t)(lane >> 3) * 16u
                                  : a_row(b * 16 + n) * arb + (uint32_t)q * 16u;
   }
 #pragma unroll
-  for (int u = 0; u < 2; u++) src.woff[u] = w_group(wave + NWV * u) * gc + (uint32_t)lane * 16u;
+  for (int u = 0; u < 2; u++) src.off[L::NA + u] = w_group(wave + NWV * u) * gc + (uint32_t)lane * 16u;
   const int arow0 = wm * half, rbase = r0 + arow0;
   uint32_t wgrp[4], sao[8];
 #pragma unroll
