@@ -64,7 +64,7 @@ int moe_pack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int 
 
 size_t moe_ffn_mx4_workspace_size(int T, int k, int E_loc, int H, int I, int y_dtype) {
   if (!ffn_sizes_ok(T, k, E_loc, H, I) || (y_dtype != MOE_F32 && y_dtype != MOE_BF16)) return 0;
-  return ffn_mx4_ws_bytes(T, T * (k < E_loc ? k : E_loc), H, I, y_dtype == MOE_BF16);
+  return ffn_mx4_ws_bytes(T, T * (k < E_loc ? k : E_loc), E_loc, H, I, y_dtype == MOE_BF16);
 }
 
 int moe_grouped_ffn_mx4(const uint8_t *a_codes, const uint8_t *a_scales, int a_dtype, const int32_t *offsets,

@@ -12,13 +12,15 @@
 // Both operands go from memory to LDS by buffer loads (no registers, no address arithmetic in the loop) into a
 // ring of RD slots, RD - 1 steps ahead; each slot holds them in the order in which the operand reads are
 // contiguous, 1 KB pieces that one wave's load fills: packed weight blocks as they are, eight rows x 128 bytes
-// of E4M3 rows, 16 rows x 64 bytes of E2M1 rows.  Scales go straight to registers, one dword per lane and 16 rows
-// for four steps, a byte of it per step.  Every wave issues the same loads every step (past the last step they
-// fetch it again into slots nobody reads), so the wait at the top of a step is a fixed count; one barrier per
-// step.
+// of E4M3 rows, 16 rows x 64 bytes of E2M1 rows.  The scales of four steps (16 bytes a row) follow the same way, one
+// load per wave every four steps, into two slots of their own (loaded straight into registers by the lanes that
+// use them, four times the requests, they cost a third of the loop's time).  Every wave issues the same loads every
+// step, so the wait at the top of a step is a fixed count; one barrier per step.
 //
-// BM is 256, or 64 where an expert has few rows (the tile is then bound by the weights' bytes: a smaller
-// activation slot leaves room for a deeper ring).
+// One workgroup per compute unit works through a list of tiles (written by the launch before), because a tile's
+// own latencies -- finding it, its rows' tokens, the first loads, the stores -- were 14 us of the 43 to 54 us a gate/up
+// tile took: the next tile's description and tokens are fetched while a tile is computed, and its last RD - 1 steps
+// fetch the next tile's first ones.
 #include "mx4_common.h"
 
 #include <utility>
@@ -28,13 +30,15 @@ namespace {
 using ffn::TileParams;
 using mx4::v8i_t;
 
-constexpr int BN = 256, NTHR = 512, NWV = NTHR / 64;
+constexpr int BN = 256, NTHR = 512, NWV = NTHR / 64, NCU = 256;
 
 struct Mx4Params {
   TileParams tp;               // offsets, row_token, row_w, El, H, I, R_cap, T; a / w / out: codes (out: rows for down)
   const uint8_t *a_scales;     // lane order, mx4::h_scale_stride(K) bytes a row
   const uint8_t *w_scales;     // packed
   uint8_t *out_scales;         // gate/up: h scales
+  const int4 *tiles;           // {expert, N tile, first row, rows | rows of a wave << 16}
+  const int *ntiles;
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -42,123 +46,148 @@ constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw buffer, 32-bit data format
 
 template <int FA, int BM>
 struct Lay {
+  static constexpr int MAXNB = BM / 32;                      // 16-row blocks of a wave
   static constexpr int AROW = FA == mx4::FP8 ? 128 : 64;     // activation bytes of a row and step
-  static constexpr int A_BYTES = BM * AROW, W_BYTES = BN * 64;
+  static constexpr int A_BYTES = BM * AROW, W_BYTES = BN * 64, PIECES = A_BYTES / 1024;
   static constexpr int SLOT = A_BYTES + W_BYTES;
-  static constexpr int RD = BM == 64 ? 6 : FA == mx4::FP8 ? 3 : 4;  // slots of the ring
-  static constexpr int NA = (A_BYTES / 1024 + NWV - 1) / NWV, NL = NA + W_BYTES / 1024 / NWV;  // loads per wave and step
-  static constexpr int BYTES = RD * SLOT;
-  static_assert(BYTES <= 160 * 1024 && RD >= 3, "fits the LDS of one CU");
+  static constexpr int SSLOT = BM * 16 + BN / 16 * 256;      // scales of four steps
+  static constexpr int FIT = (163840 - 2 * SSLOT) / SLOT, RD = FIT < 6 ? FIT : 6;  // slots of the ring
+  static constexpr int SA = BM / 64;                         // waves that fetch activation scales; the next four fetch weight scales
+  static constexpr int NA = (PIECES + NWV - 1) / NWV, NL = NA + W_BYTES / 1024 / NWV;  // loads per wave and step
+  static_assert(RD >= 3, "two steps ahead");
 };
 
-struct Src {
-  __amdgpu_buffer_rsrc_t ra, rw, rsa, rsw;  // activations, this expert's weights, and their scales
-  uint32_t off[6];                          // this lane's bytes of its wave's pieces at step 0, activations first
+// A tile as one wave sees it.
+template <int FA, int BM>
+struct Tile {
+  __amdgpu_buffer_rsrc_t rw, rs;                // its expert's weights; the scales this wave fetches
+  uint32_t off[Lay<FA, BM>::NL];                // this lane's bytes of its wave's pieces at step 0, activations first
+  uint32_t soff;                                // and of its scales
+  int col0, rbase, mvalid, arow0, nb;
 };
 
-// Loads U0 .. U1 - 1 of the NL that this wave issues for step st into ring slot SLOTI (fewer activation pieces than
-// waves: some are fetched twice).
-template <int FA, int BM, int SLOTI, int U0, int U1>
-__device__ __forceinline__ void load_pieces(const Src &src, int st, int wave, char *lds) {
+// 16 bytes per lane from memory to 1 KB of LDS.
+__device__ __forceinline__ void dma(const __amdgpu_buffer_rsrc_t &r, char *to, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, voff, soff, 0, 0);
+}
+
+// Loads U0 .. U1 - 1 of the NL that this wave issues for step st of a tile into a ring slot (fewer activation
+// pieces than waves: some are fetched twice).
+template <int FA, int BM, int U0, int U1>
+__device__ __forceinline__ void load_pieces(const __amdgpu_buffer_rsrc_t &ra, const __amdgpu_buffer_rsrc_t &rw,
+                                            const uint32_t (&off)[Lay<FA, BM>::NL], int st, int wave, char *slot) {
   using L = Lay<FA, BM>;
   const uint32_t sa = (uint32_t)st * L::AROW, sw = (uint32_t)st * mx4::kBlk;
 #pragma unroll
   for (int u = U0; u < U1; u++) {
-    if (u < L::NA)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          src.ra, (lds_void *)(lds + SLOTI * L::SLOT + (wave + NWV * u) % (L::A_BYTES / 1024) * 1024), 16, src.off[u],
-          sa, 0, 0);
-    else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          src.rw, (lds_void *)(lds + SLOTI * L::SLOT + L::A_BYTES + (wave + NWV * (u - L::NA)) * 1024), 16, src.off[u],
-          sw, 0, 0);
+    if (u < L::NA) dma(ra, slot + (wave + NWV * u) % L::PIECES * 1024, off[u], sa);
+    else dma(rw, slot + L::A_BYTES + (wave + NWV * (u - L::NA)) * 1024, off[u], sw);
   }
 }
 
-// MODE 0: gate/up + SwiGLU -> h.  MODE 1: down -> gated rows.  NB: 16-row blocks of this wave.
-template <int MODE, int FA, bool BF16, int BM, int NB>
-__device__ __forceinline__ void body(const Mx4Params &mp, const Src &src, int K, int nt, int rbase, int mvalid, int wave,
-                                     int lane, int arow0, int wn, const uint32_t (&wgrp)[4], const uint32_t (&sao)[8],
-                                     char *lds) {
+// One tile: the K loop and the epilogue.  MODE 0: gate/up + SwiGLU -> h.  MODE 1: down -> gated rows.  NB: 16-row
+// blocks of this wave.  ready() makes ``nxt`` usable; it is called once, before the first load for it.
+template <int MODE, int FA, bool BF16, int BM, int NB, typename READY>
+__device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_buffer_rsrc_t &ra,
+                                          const Tile<FA, BM> &t, const Tile<FA, BM> &nxt, READY ready, int K, int wave,
+                                          int lane, int &slot, int &sslot, char *lds) {
   using L = Lay<FA, BM>;
   const TileParams &p = mp.tp;
-  const int n = lane & 15, q = lane >> 4;
+  const int n = lane & 15, q = lane >> 4, wn = wave & 3;
   const int nstep = K / 128, nch = (nstep + 3) / 4;
+  const int nst = max(nstep, L::RD - 1);  // a shorter tile idles, so that loads reach only one tile ahead
   f32x4_t acc[NB][4];
 #pragma unroll
   for (int i = 0; i < NB; i++)
 #pragma unroll
     for (int g = 0; g < 4; g++) acc[i][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const uint32_t gs = (uint32_t)mx4::group_scales(K);
-  uint32_t ws[4], as[NB], wsn[4], asn[NB];
-  auto scales = [&](uint32_t(&w)[4], uint32_t(&a)[NB], int c) __attribute__((always_inline)) {
+  float gate[NB];
+  if constexpr (MODE == 1) {
 #pragma unroll
-    for (int g = 0; g < 4; g++)
-      w[g] = __builtin_amdgcn_raw_buffer_load_b32(src.rsw, lane * 4, (int)(wgrp[g] * gs + (uint32_t)c * mx4::kSblk), 0);
-#pragma unroll
-    for (int i = 0; i < NB; i++) a[i] = __builtin_amdgcn_raw_buffer_load_b32(src.rsa, (int)sao[i], c * 16, 0);
-  };
+    for (int i = 0; i < NB; i++) gate[i] = p.row_w[t.rbase + min(16 * i + n, max(t.mvalid, 1) - 1)];
+  }
   // LDS bytes of this lane's operands inside a slot
   const uint32_t wbase = L::A_BYTES + (uint32_t)wn * 4096u + lane * 16u;
   const uint32_t abase = FA == mx4::FP8
-                             ? (uint32_t)(arow0 >> 3) * 1024u + (uint32_t)(n >> 3) * 1024u + q * 128u + (n & 7) * 16u
-                             : (uint32_t)(arow0 >> 4) * 1024u + lane * 16u;
-  scales(wsn, asn, 0);
-  asm volatile("" ::: "memory");
-  [&]<int... D>(std::integer_sequence<int, D...>) __attribute__((always_inline)) {
-    (load_pieces<FA, BM, D, 0, L::NL>(src, min(D, nstep - 1), wave, lds), ...);
-  }(std::make_integer_sequence<int, L::RD - 1>{});
-  // step kt = IDX modulo PER: ring slot and scale byte are compile-time constants
-  constexpr int PER = L::RD % 4 == 0 ? L::RD : L::RD % 2 == 0 ? 2 * L::RD : 4 * L::RD;
-  auto step = [&](auto IC, int kt) __attribute__((always_inline)) {
-    constexpr int IDX = decltype(IC)::value, j = IDX % 4, S = IDX % L::RD, SN = (IDX + L::RD - 1) % L::RD;
-    if (kt >= nstep) return;
+                             ? (uint32_t)(t.arow0 >> 3) * 1024u + (uint32_t)(n >> 3) * 1024u + q * 128u + (n & 7) * 16u
+                             : (uint32_t)(t.arow0 >> 4) * 1024u + lane * 16u;
+  uint32_t ws[4], as[NB];
+  auto step = [&](auto JC, int kt) __attribute__((always_inline)) {
+    constexpr int j = decltype(JC)::value;
+    if (kt >= nst) return;
+    // everything this step reads was issued RD - 1 steps ago or earlier (the scales of a whole piece, four); newer
+    // are the pieces of RD - 2 steps.  After a tile whose last piece is short its successor's first scales are
+    // younger than that.
+    if (j == 0 && kt == 0 && (nstep & 3) != 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L::NL *(L::RD - 2)) : "memory");
     asm volatile("s_barrier" ::: "memory");
     if constexpr (j == 0) {
+      const int c = kt >> 2;
+      if (c == max(nch - 2, 0)) ready();
+      if (c < nch) {
+        const char *sp = lds + L::RD * L::SLOT + sslot * L::SSLOT;
 #pragma unroll
-      for (int g = 0; g < 4; g++) ws[g] = wsn[g];
+        for (int g = 0; g < 4; g++) ws[g] = *(const uint32_t *)(sp + BM * 16 + (wn * 4 + g) * 256 + lane * 4);
 #pragma unroll
-      for (int i = 0; i < NB; i++) as[i] = asn[i];
-      scales(wsn, asn, min((kt >> 2) + 1, nch - 1));
-      asm volatile("" ::: "memory");
+        for (int i = 0; i < NB; i++) as[i] = *(const uint32_t *)(sp + (t.arow0 + 16 * i + n) * 16 + q * 4);
+        sslot ^= 1;
+        const bool same = c + 1 < nch;
+        dma(same ? t.rs : nxt.rs, lds + L::RD * L::SLOT + sslot * L::SSLOT + wave * 1024 - (wave >= L::SA + 4 ? 4096 : 0),
+            same ? t.soff : nxt.soff, (same ? c + 1 : 0) * (wave < L::SA ? 16 : mx4::kSblk));
+      }
     }
+    const int sn = slot == 0 ? L::RD - 1 : slot - 1;  // the slot read in the step before
+    char *const ldn = lds + sn * L::SLOT;
+    const uint32_t so = (uint32_t)slot * L::SLOT;
+    const uint32_t ab = abase + so, wb = wbase + so;
+    const int st = kt + L::RD - 1;
     auto act = [&](int i) __attribute__((always_inline)) {
       if constexpr (FA == mx4::FP8)
-        return mx4::piece8(*(const u32x4_t *)(lds + abase + (S * L::SLOT + i * 2048)),
-                           *(const u32x4_t *)(lds + abase + (S * L::SLOT + i * 2048 + 512)));
+        return mx4::piece8(*(const u32x4_t *)(lds + ab + i * 2048), *(const u32x4_t *)(lds + ab + (i * 2048 + 512)));
       else
-        return mx4::piece4(*(const u32x4_t *)(lds + abase + (S * L::SLOT + i * 1024)));
+        return mx4::piece4(*(const u32x4_t *)(lds + ab + i * 1024));
     };
-    v8i_t w[4], a[2];
+    // fetch step fs: of this tile, or of the next one (selected without a branch, which would cut the block apart)
+    const bool here = st < nst;
+    const int fs = here ? st : min(st - nst, nstep - 1);
+    const __amdgpu_buffer_rsrc_t rw = here ? t.rw : nxt.rw;
+    uint32_t off[L::NL];
 #pragma unroll
-    for (int g = 0; g < 4; g++) w[g] = mx4::piece4(*(const u32x4_t *)(lds + wbase + (S * L::SLOT + g * 1024)));
-    a[0] = act(0);
-    const int stn = min(kt + L::RD - 1, nstep - 1);
-    // block i: fetch the next operand and a share of the coming step, then multiply
-    auto block = [&](auto I) __attribute__((always_inline)) {
-      constexpr int i = decltype(I)::value;
-      if constexpr (i + 1 < NB) a[(i + 1) & 1] = act(i + 1);
-      load_pieces<FA, BM, SN, L::NL * i / NB, L::NL *(i + 1) / NB>(src, stn, wave, lds);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int u = 0; u < L::NL; u++) off[u] = here ? t.off[u] : nxt.off[u];
+    if (kt < nstep) {
+      v8i_t w[4], a[2];
 #pragma unroll
-      for (int g = 0; g < 4; g++) acc[i][g] = mx4::mfma<FA, j, j>(w[g], a[i & 1], acc[i][g], ws[g], as[i]);
-    };
-    [&]<int... I>(std::integer_sequence<int, I...>) __attribute__((always_inline)) {
-      (block(std::integral_constant<int, I>{}), ...);
-    }(std::make_integer_sequence<int, NB>{});
+      for (int g = 0; g < 4; g++) w[g] = mx4::piece4(*(const u32x4_t *)(lds + wb + g * 1024));
+      a[0] = act(0);
+      // block i: fetch the next operand and a share of the step to come, then multiply
+      auto block = [&](auto I) __attribute__((always_inline)) {
+        constexpr int i = decltype(I)::value;
+        if constexpr (i + 1 < NB) a[(i + 1) & 1] = act(i + 1);
+        load_pieces<FA, BM, L::NL * i / NB, L::NL *(i + 1) / NB>(ra, rw, off, fs, wave, ldn);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int g = 0; g < 4; g++) acc[i][g] = mx4::mfma<FA, j, j>(w[g], a[i & 1], acc[i][g], ws[g], as[i]);
+      };
+      [&]<int... I>(std::integer_sequence<int, I...>) __attribute__((always_inline)) {
+        (block(std::integral_constant<int, I>{}), ...);
+      }(std::make_integer_sequence<int, NB>{});
+    } else {
+      load_pieces<FA, BM, 0, L::NL>(ra, rw, off, fs, wave, ldn);
+    }
+    slot = slot + 1 == L::RD ? 0 : slot + 1;
   };
-  for (int kt = 0; kt < nstep; kt += PER)
-    [&]<int... IDX>(std::integer_sequence<int, IDX...>) __attribute__((always_inline)) {
-      (step(std::integral_constant<int, IDX>{}, kt + IDX), ...);
-    }(std::make_integer_sequence<int, PER>{});
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
-  // acc[i][g][r]: tile row arow0 + 16 i + n, weight row 16 g + 4 q + r of this wave's 64
+  for (int kt = 0; kt < nst; kt += 4) {
+    step(std::integral_constant<int, 0>{}, kt);
+    step(std::integral_constant<int, 1>{}, kt + 1);
+    step(std::integral_constant<int, 2>{}, kt + 2);
+    step(std::integral_constant<int, 3>{}, kt + 3);
+  }
+  // acc[i][g][r]: row rbase + 16 i + n, weight row 16 g + 4 q + r of this wave's 64
 #pragma unroll
   for (int i = 0; i < NB; i++) {
     const int m = 16 * i + n;
-    const bool on = m < mvalid;
-    const size_t row = (size_t)(rbase + m);
+    const bool on = m < t.mvalid;
+    const size_t row = (size_t)(t.rbase + m);
     if constexpr (MODE == 0) {
       float v[2][4];
 #pragma unroll
@@ -166,13 +195,12 @@ __device__ __forceinline__ void body(const Mx4Params &mp, const Src &src, int K,
 #pragma unroll
         for (int r = 0; r < 4; r++) v[g][r] = silu_fast(acc[i][g][r]) * acc[i][2 + g][r];
       mx4::store_h_block<FA>(v, on, (uint8_t *)p.out + row * mx4::code_bytes<FA>(p.I),
-                             mp.out_scales + row * mx4::h_scale_stride(p.I), nt * 128 + wn * 32, q);
+                             mp.out_scales + row * mx4::h_scale_stride(p.I), t.col0, q);
     } else if (on) {
-      const float w = p.row_w[row];
 #pragma unroll
       for (int g = 0; g < 4; g++) {
-        const int col = nt * BN + wn * 64 + 16 * g + 4 * q;
-        if (col < p.H) mx4::store4<BF16>(p.out, row * p.H + col, acc[i][g] * w);
+        const int col = t.col0 + 16 * g + 4 * q;
+        if (col < p.H) mx4::store4<BF16>(p.out, row * p.H + col, acc[i][g] * gate[i]);
       }
     }
   }
@@ -181,85 +209,146 @@ __device__ __forceinline__ void body(const Mx4Params &mp, const Src &src, int K,
 template <int MODE, int FA, bool BF16, int BM>
 __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
   using L = Lay<FA, BM>;
-  __shared__ __attribute__((aligned(1024))) char lds[L::BYTES];
+  __shared__ __attribute__((aligned(1024))) char lds[L::RD * L::SLOT + 2 * L::SSLOT];
   const TileParams &p = mp.tp;
   const int K = MODE == 0 ? p.H : p.I, Nw = MODE == 0 ? 2 * p.I : p.H;
-  const int NT = MODE == 0 ? p.I / 128 : (p.H + BN - 1) / BN;
-  int e, nt, mt, mtiles;
-  if (!ffn::locate_tile<BM>(p, NT, e, nt, mt, mtiles)) return;
-  e = __builtin_amdgcn_readfirstlane(e);  // the same in every lane: keep them scalar
-  nt = __builtin_amdgcn_readfirstlane(nt);
-  mt = __builtin_amdgcn_readfirstlane(mt);
-  mtiles = __builtin_amdgcn_readfirstlane(mtiles);
-  const int beg = p.offsets[e], cnt = p.offsets[e + 1] - beg;
-  const int trows = __builtin_amdgcn_readfirstlane(min(BM, (((cnt + mtiles - 1) / mtiles) + 31) & ~31));
-  const int r0 = beg + mt * trows;
-  const int rows = min(trows, min(beg + cnt, p.R_cap) - r0);
-  if (rows <= 0) return;
-  const int half = trows >> 1;
+  const int nstep = K / 128;
+  // Workgroups go round-robin over the 8 XCDs: XCD x takes the x-th eighth of the list, its workgroups in
+  // turn, so that the tiles of one expert, which share operands, meet in one L2.
+  const int total = *mp.ntiles, per = gridDim.x >> 3, xcd = blockIdx.x & 7;
+  const int qt = total >> 3, rem = total & 7;
+  const int end = xcd * qt + min(xcd, rem) + qt + (xcd < rem ? 1 : 0);
+  int at = xcd * qt + min(xcd, rem) + (blockIdx.x >> 3);
+  if (at >= end) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3, n = lane & 15, q = lane >> 4;
-  const int mvalid = min(rows - wm * half, half);
-
   const uint32_t arb = (uint32_t)mx4::code_bytes<FA>(K), ass = (uint32_t)mx4::h_scale_stride(K);
-  const uint32_t gc = (uint32_t)mx4::group_codes(K);
-  auto a_row = [&](int row) -> uint32_t {  // source row of tile row ``row`` (rows past the end repeat the last)
-    const int r = r0 + min(row, rows - 1);
-    return MODE == 0 ? min((uint32_t)p.row_token[r], (uint32_t)p.T - 1u) : (uint32_t)r;
-  };
-  auto w_group = [&](int i) -> uint32_t {  // weight group of LDS piece i
-    if constexpr (MODE == 0) return (uint32_t)(nt * 8 + (i >> 2) * 2 + (i & 1) + ((i >> 1) & 1) * (p.I / 16));
-    else return (uint32_t)min(nt * 16 + i, p.H / 16 - 1);
-  };
-  Src src;
+  const uint32_t gc = (uint32_t)mx4::group_codes(K), gs = (uint32_t)mx4::group_scales(K);
   const uint32_t arows = MODE == 0 ? (uint32_t)p.T : (uint32_t)p.R_cap;
-  const size_t wexp = (size_t)e * (Nw / 16);
-  src.ra = __builtin_amdgcn_make_buffer_rsrc((void *)p.a, (short)0, (int)(arows * arb), kRsrcWord3);
-  src.rsa = __builtin_amdgcn_make_buffer_rsrc((void *)mp.a_scales, (short)0, (int)(arows * ass), kRsrcWord3);
-  src.rw = __builtin_amdgcn_make_buffer_rsrc((void *)((const char *)p.w + wexp * gc), (short)0, (int)(Nw / 16 * gc),
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)p.a, (short)0, (int)(arows * arb), kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rsa =
+      __builtin_amdgcn_make_buffer_rsrc((void *)mp.a_scales, (short)0, (int)(arows * ass), kRsrcWord3);
+
+  // A tile's description; the activation offsets hold the source rows of this lane's pieces and scales (rows past
+  // the tile's end repeat its last) until place() turns them into bytes, so that nothing waits for them here.
+  auto describe = [&](Tile<FA, BM> &t, int i) __attribute__((always_inline)) {
+    const int4 d = mp.tiles[i];
+    const int e = __builtin_amdgcn_readfirstlane(d.x), nt = __builtin_amdgcn_readfirstlane(d.y);
+    const int r0 = __builtin_amdgcn_readfirstlane(d.z), rp = __builtin_amdgcn_readfirstlane(d.w);
+    const int rows = rp & 0xffff, part = rp >> 16;
+    const size_t wexp = (size_t)e * (Nw / 16);
+    t.rw = __builtin_amdgcn_make_buffer_rsrc((void *)((const char *)p.w + wexp * gc), (short)0, (int)(Nw / 16 * gc),
                                              kRsrcWord3);
-  src.rsw = __builtin_amdgcn_make_buffer_rsrc((void *)(mp.w_scales + wexp * mx4::group_scales(K)), (short)0,
-                                              (int)(Nw / 16 * mx4::group_scales(K)), kRsrcWord3);
+    if (wave < L::SA) t.rs = rsa;
+    else t.rs = __builtin_amdgcn_make_buffer_rsrc((void *)(mp.w_scales + wexp * gs), (short)0, (int)(Nw / 16 * gs), kRsrcWord3);
+    auto group = [&](int i) -> uint32_t {  // weight group of LDS piece i
+      if constexpr (MODE == 0) return (uint32_t)(nt * 8 + (i >> 2) * 2 + (i & 1) + ((i >> 1) & 1) * (p.I / 16));
+      else return (uint32_t)min(nt * 16 + i, p.H / 16 - 1);
+    };
 #pragma unroll
-  for (int u = 0; u < L::NA; u++) {
-    const int b = (wave + NWV * u) % (L::A_BYTES / 1024);
-    src.off[u] = FA == mx4::FP8 ? a_row(b * 8 + (lane & 7)) * arb + (uint32_t)(lane >> 3) * 16u
-                                 : a_row(b * 16 + n) * arb + (uint32_t)q * 16u;
-  }
+    for (int u = 0; u < 2; u++) t.off[L::NA + u] = group(wave + NWV * u) * gc + (uint32_t)lane * 16u;
+    t.col0 = MODE == 0 ? nt * 128 + wn * 32 : nt * BN + wn * 64;
+    t.arow0 = wm * part;
+    t.rbase = r0 + t.arow0;
+    t.mvalid = min(rows - t.arow0, part);
+    t.nb = min(part >> 4, (max(t.mvalid, 1) + 15) >> 4);
+    auto src = [&](int row) -> uint32_t {
+      const int r = r0 + min(row, rows - 1);
+      return MODE == 0 ? (uint32_t)p.row_token[r] : (uint32_t)r;
+    };
 #pragma unroll
-  for (int u = 0; u < 2; u++) src.off[L::NA + u] = w_group(wave + NWV * u) * gc + (uint32_t)lane * 16u;
-  const int arow0 = wm * half, rbase = r0 + arow0;
-  uint32_t wgrp[4], sao[8];
-#pragma unroll
-  for (int g = 0; g < 4; g++) wgrp[g] = __builtin_amdgcn_readfirstlane(w_group(wn * 4 + g));
-#pragma unroll
-  for (int i = 0; i < BM / 32; i++) sao[i] = a_row(arow0 + 16 * i + n) * ass + 4u * q;
-  const int nb = __builtin_amdgcn_readfirstlane(min(half >> 4, (max(mvalid, 1) + 15) >> 4));
-#define MX4_BODY(NB) body<MODE, FA, BF16, BM, NB>(mp, src, K, nt, rbase, mvalid, wave, lane, arow0, wn, wgrp, sao, lds)
-  if constexpr (BM == 64) {
-    if (nb == 1) MX4_BODY(1);
-    else MX4_BODY(2);
-  } else {
-    switch (nb) {
-      case 1: MX4_BODY(1); break;
-      case 2: MX4_BODY(2); break;
-      case 3:
-      case 4: MX4_BODY(4); break;
-      case 5:
-      case 6: MX4_BODY(6); break;
-      default: MX4_BODY(8); break;
+    for (int u = 0; u < L::NA; u++) {
+      const int b = (wave + NWV * u) % L::PIECES;
+      t.off[u] = src(FA == mx4::FP8 ? b * 8 + (lane & 7) : b * 16 + n);
     }
-  }
+    t.soff = wave < L::SA ? src(wave * 64 + lane) : group(((wave - L::SA) & 3) * 4 + q) * gs + (uint32_t)n * 16u;
+  };
+  auto place = [&](Tile<FA, BM> &t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < L::NA; u++)
+      t.off[u] = min(t.off[u], arows - 1) * arb + (uint32_t)(FA == mx4::FP8 ? lane >> 3 : q) * 16u;
+    if (wave < L::SA) t.soff = min(t.soff, arows - 1) * ass;
+  };
+
+  Tile<FA, BM> cur, nxt;
+  describe(cur, at);
+  place(cur);
+  dma(cur.rs, lds + L::RD * L::SLOT + wave * 1024 - (wave >= L::SA + 4 ? 4096 : 0), cur.soff, 0);
+#pragma unroll
+  for (int d = 0; d < L::RD - 1; d++) 
+    load_pieces<FA, BM, 0, L::NL>(ra, cur.rw, cur.off, min(d, nstep - 1), wave, lds + d * L::SLOT);
+  int slot = 0, sslot = 0;
+  for (;;) {
+    const bool more = at + per < end;
+    at = more ? at + per : at;  // after the last tile: its own first steps again, which nobody reads
+    describe(nxt, at);
+    auto ready = [&]() __attribute__((always_inline)) { place(nxt); };
+#define MX4_BODY(NB) tile_body<MODE, FA, BF16, BM, NB>(mp, ra, cur, nxt, ready, K, wave, lane, slot, sslot, lds)
+    // the waves of a tile may take different cases: each issues the same loads and meets the same barriers
+    if constexpr (BM == 64) {
+      if (cur.nb == 1) MX4_BODY(1);
+      else MX4_BODY(2);
+    } else {
+      if (cur.nb <= 2) MX4_BODY(2);
+      else if (cur.nb <= 4) MX4_BODY(4);
+      else if (L::MAXNB > 6 && cur.nb > 6) MX4_BODY(L::MAXNB);
+      else MX4_BODY(6);
+    }
 #undef MX4_BODY
+    if (!more) break;
+    cur = nxt;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
 }
 
-// Activation scales [T, K/32] into lane order: dword q of piece c of a row has the scales 16c + 4j + q, j = 0 .. 3
-// (0 past the end of the row).
-__global__ __launch_bounds__(256) void lane_scales_kernel(const uint8_t *__restrict__ s, int T, int K,
-                                                          uint32_t *__restrict__ out) {
-  const int kb = K / 32, dw = (K + 511) / 512 * 4;
-  const long long total = (long long)T * dw;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
+// The tile list: expert by expert, then N tile by N tile, then M tile by M tile.  One workgroup; smem: El + 1 ints.
+template <int BM>
+__device__ void list_tiles(const TileParams &p, int NT, int cap, int4 *out, int *count, int *smem) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  auto rows_of = [&](int e) { return e < p.El ? min(p.offsets[e + 1], p.R_cap) - max(p.offsets[e], 0) : 0; };
+  if (wave == 0) {
+    int n0 = 0;
+    for (int b = 0; b < p.El; b += 64) {
+      const int c = rows_of(b + lane), t = c > 0 ? (c + BM - 1) / BM : 0;
+      const int incl = ffn::wave_incl_scan_i(t, lane);
+      if (b + lane < p.El) smem[b + lane] = n0 + incl - t;
+      n0 += __shfl(incl, 63, 64);
+    }
+    if (lane == 0) {
+      smem[p.El] = n0;
+      *count = min(n0 * NT, cap);
+    }
+  }
+  __syncthreads();
+  for (int e = wave; e < p.El; e += blockDim.x >> 6) {
+    const int c = rows_of(e), m = smem[e + 1] - smem[e], base = smem[e] * NT;
+    if (m == 0) continue;
+    const int trows = min(BM, ((c + m - 1) / m + 31) & ~31);  // m * trows >= c; a last tile may have no rows left
+    for (int i = lane; i < m * NT; i += 64) {
+      const int nt = i / m, mt = i - nt * m;
+      const int rows = max(min(trows, c - mt * trows), 0);
+      if (base + i < cap) out[base + i] = make_int4(e, nt, max(p.offsets[e], 0) + mt * trows, rows | (trows / 2) << 16);
+    }
+  }
+  __syncthreads();
+}
+
+// What the tile kernels need first.  Workgroup 0: the tile lists of both halves.  The others: activation scales
+// [T, K/32] into lane order: dword q of piece c of a row has the scales 16c + 4j + q, j = 0 .. 3 (0 past the end of
+// the row).
+template <int BM>
+__global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int cap, int4 *gtiles, int4 *dtiles, int *counts,
+                                                      const uint8_t *__restrict__ s, uint32_t *__restrict__ out) {
+  if (blockIdx.x == 0) {
+    __shared__ int smem[1024 + 1];
+    list_tiles<BM>(p, p.I / 128, cap * (p.I / 128), gtiles, counts, smem);
+    const int nt = (p.H + BN - 1) / BN;
+    list_tiles<BM>(p, nt, cap * nt, dtiles, counts + 1, smem);
+    return;
+  }
+  const int K = p.H, kb = K / 32, dw = (K + 511) / 512 * 4;
+  const long long total = (long long)p.T * dw, stride = (long long)(gridDim.x - 1) * blockDim.x;
+  for (long long i = (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x; i < total; i += stride) {
     const long long t = i / dw;
     const int d = (int)(i - t * dw), c = d >> 2, q = d & 3;
     uint32_t w = 0;
@@ -295,21 +384,39 @@ __global__ __launch_bounds__(256) void sum_rows_kernel(const void *__restrict__ 
   }
 }
 
-// Workspace: h codes [R_cap, I] (a byte each, half of it used by E2M1), h scales, and for the tile kernel the
-// activation scales in lane order and the rows [R_cap, H].
+// Workspace: h codes [R_cap, I] (a byte each, half of it used by E2M1), h scales, and for the tile kernels the
+// activation scales in lane order, the tile lists and the rows [R_cap, H].
 size_t h_bytes(int R_cap, int I) { return align_up((size_t)R_cap * I, 256); }
 size_t hs_bytes(int R_cap, int I) { return align_up((size_t)R_cap * mx4::h_scale_stride(I), 256); }
 size_t as_bytes(int T, int H) { return align_up((size_t)T * mx4::h_scale_stride(H), 256); }
+// M tiles at most: one per started BM rows of each expert.
+int max_mtiles(int T, int R_cap, int El, int BM) {
+  const long long a = ((long long)R_cap + (long long)El * (BM - 1)) / BM, b = (long long)El * ceil_div_i(T, BM);
+  return (int)(a < b ? a : b);
+}
+// Rows of a tile: 64 while an expert has at most 64 rows on average, else 192 or 256, whichever pads an expert of
+// average size to fewer rows.
+int tile_rows(int R_cap, int El) {
+  const int avg = ceil_div_i(R_cap, El);
+  if (avg <= 64) return 64;
+  auto padded = [&](int BM) {
+    const int m = ceil_div_i(avg, BM);
+    return m * ((ceil_div_i(avg, m) + 31) & ~31);
+  };
+  return padded(256) < padded(192) ? 256 : 192;
+}
+size_t list_bytes(int T, int R_cap, int El, int H, int I) {
+  const int m = max_mtiles(T, R_cap, El, tile_rows(R_cap, El));
+  return 256 + align_up((size_t)m * (I / 128 + ceil_div_i(H, BN)) * sizeof(int4), 256);
+}
 
 template <int FA, bool BF16, int BM>
 hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
   uint8_t *h = (uint8_t *)a.ws, *hs = h + h_bytes(a.R_cap, a.I), *as = hs + hs_bytes(a.R_cap, a.I);
-  uint8_t *rows = as + as_bytes(a.T, a.H);
-  const long long dwords = (long long)a.T * (mx4::h_scale_stride(a.H) / 4);
-  hipLaunchKernelGGL(lane_scales_kernel, dim3((unsigned)(dwords < (1 << 20) ? (dwords + 255) / 256 : 4096)), dim3(256), 0,
-                     s, a.a_s, a.T, a.H, (uint32_t *)as);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+  uint8_t *list = as + as_bytes(a.T, a.H), *rows = list + list_bytes(a.T, a.R_cap, a.El, a.H, a.I);
+  const int mt = max_mtiles(a.T, a.R_cap, a.El, BM), ntg = a.I / 128, ntd = ceil_div_i(a.H, BN);
+  int *counts = (int *)list;
+  int4 *gtiles = (int4 *)(list + 256), *dtiles = gtiles + (size_t)mt * ntg;
   Mx4Params p{};
   p.tp.offsets = a.offsets;
   p.tp.row_token = a.row_token;
@@ -319,9 +426,11 @@ hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
   p.tp.I = a.I;
   p.tp.R_cap = a.R_cap;
   p.tp.T = a.T;
-  const long long mt1 = ((long long)a.R_cap + (long long)a.El * (BM - 1)) / BM;
-  const long long mt2 = (long long)a.El * ceil_div_i(a.T, BM);
-  const int mt = (int)(mt1 < mt2 ? mt1 : mt2);
+  const long long dwords = (long long)a.T * (mx4::h_scale_stride(a.H) / 4);
+  hipLaunchKernelGGL(prepare_kernel<BM>, dim3(1 + (unsigned)(dwords < (1 << 20) ? (dwords + 255) / 256 : 4096)), dim3(256),
+                     0, s, p.tp, mt, gtiles, dtiles, counts, a.a_s, (uint32_t *)as);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
   Mx4Params g = p;
   g.tp.a = a.a;
   g.a_scales = as;
@@ -329,7 +438,9 @@ hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
   g.w_scales = a.wgu_s;
   g.tp.out = h;
   g.out_scales = hs;
-  hipLaunchKernelGGL((ffn_mx4_kernel<0, FA, false, BM>), dim3(mt * (a.I / 128)), dim3(NTHR), 0, s, g);
+  g.tiles = gtiles;
+  g.ntiles = counts;
+  hipLaunchKernelGGL((ffn_mx4_kernel<0, FA, false, BM>), dim3(NCU), dim3(NTHR), 0, s, g);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
   Mx4Params d = p;
@@ -338,7 +449,9 @@ hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
   d.tp.w = a.wd;
   d.w_scales = a.wd_s;
   d.tp.out = rows;
-  hipLaunchKernelGGL((ffn_mx4_kernel<1, FA, BF16, BM>), dim3(mt * ceil_div_i(a.H, BN)), dim3(NTHR), 0, s, d);
+  d.tiles = dtiles;
+  d.ntiles = counts + 1;
+  hipLaunchKernelGGL((ffn_mx4_kernel<1, FA, BF16, BM>), dim3(NCU), dim3(NTHR), 0, s, d);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(sum_rows_kernel<BF16>, dim3(a.T < 16384 ? a.T : 16384), dim3(256), 0, s, rows, a.token_row, a.T,
@@ -348,15 +461,19 @@ hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
 
 template <int FA, bool BF16>
 hipError_t launch(const FfnMx4Args &a, hipStream_t s) {
-  if ((long long)a.R_cap <= 64LL * a.El) return launch_tiles<FA, BF16, 64>(a, s);
-  return launch_tiles<FA, BF16, 256>(a, s);
+  switch (tile_rows(a.R_cap, a.El)) {
+    case 64: return launch_tiles<FA, BF16, 64>(a, s);
+    case 192: return launch_tiles<FA, BF16, 192>(a, s);
+    default: return launch_tiles<FA, BF16, 256>(a, s);
+  }
 }
 
 }  // namespace
 
-size_t ffn_mx4_ws_bytes(int T, int R_cap, int H, int I, int y_bf16) {
+size_t ffn_mx4_ws_bytes(int T, int R_cap, int El, int H, int I, int y_bf16) {
   size_t b = h_bytes(R_cap, I) + hs_bytes(R_cap, I);
-  if (T > kMx4StreamMaxT) b += as_bytes(T, H) + align_up((size_t)R_cap * H * (y_bf16 ? 2 : 4), 256);
+  if (T > kMx4StreamMaxT)
+    b += as_bytes(T, H) + list_bytes(T, R_cap, El, H, I) + align_up((size_t)R_cap * H * (y_bf16 ? 2 : 4), 256);
   return b;
 }
 

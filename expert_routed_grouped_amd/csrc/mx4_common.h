@@ -160,7 +160,7 @@ struct FfnMx4Args {
   int y_bf16;
   void *ws;
 };
-size_t ffn_mx4_ws_bytes(int T, int R_cap, int H, int I, int y_bf16);
+size_t ffn_mx4_ws_bytes(int T, int R_cap, int El, int H, int I, int y_bf16);
 hipError_t launch_ffn_mx4(const FfnMx4Args &a, hipStream_t s);
 // Weight-streaming path for few rows per expert (ffn_mx4_stream.hip), T <= kMx4StreamMaxT: h and its scales into
 // ``h`` / ``hs``, then the down half, which also sums to token order; launch_down_sum_mx4 is that half alone.
