@@ -196,12 +196,10 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
         for (int r = 0; r < 4; r++) v[g][r] = silu_fast(acc[i][g][r]) * acc[i][2 + g][r];
       mx4::store_h_block<FA>(v, on, (uint8_t *)p.out + row * mx4::code_bytes<FA>(p.I),
                              mp.out_scales + row * mx4::h_scale_stride(p.I), t.col0, q);
-    } else if (on) {
+    } else if (t.col0 < p.H) {  // H is a multiple of 128: a wave's 64 columns are all there or none
 #pragma unroll
-      for (int g = 0; g < 4; g++) {
-        const int col = t.col0 + 16 * g + 4 * q;
-        if (col < p.H) mx4::store4<BF16>(p.out, row * p.H + col, acc[i][g] * gate[i]);
-      }
+      for (int g = 0; g < 4; g += 2)
+        mx4::store_pair<BF16>(p.out, row * p.H + t.col0 + 16 * g, q, acc[i][g] * gate[i], acc[i][g + 1] * gate[i], on);
     }
   }
 }

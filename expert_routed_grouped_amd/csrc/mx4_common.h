@@ -134,6 +134,29 @@ __device__ __forceinline__ void store4(void *base, size_t index, const f32x4_t &
   else *(f32x4_t *)((float *)base + index) = v;
 }
 
+// Two neighbouring 16-column groups of one row, a and b (this lane: columns 4q .. 4q+3 of each): bf16 values are
+// exchanged between lane quarters first (row-pair swap), so that a lane stores 16 contiguous bytes and the four
+// lanes of a row 64, twice what they would without (32-byte pieces took 130 us for 6000 tokens' rows).
+// ``base``: the row at the first column of a.  The whole wave takes part; ``on``: this lane's row exists.
+template <bool BF16>
+__device__ __forceinline__ void store_pair(void *base, size_t index, int q, const f32x4_t &a, const f32x4_t &b, bool on) {
+  if constexpr (BF16) {
+    u32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const auto s = __builtin_amdgcn_permlane16_swap(pack_bf16x2(a[2 * i], a[2 * i + 1]),
+                                                      pack_bf16x2(b[2 * i], b[2 * i + 1]), false, false);
+      v[i] = s[0];
+      v[2 + i] = s[1];
+    }
+    // quarter 0: a 0-7, 1: b 0-7, 2: a 8-15, 3: b 8-15
+    if (on) *(u32x4_t *)((uint16_t *)base + index + (q & 1) * 16 + (q >> 1) * 8) = v;
+  } else if (on) {
+    *(f32x4_t *)((float *)base + index + 4 * q) = a;
+    *(f32x4_t *)((float *)base + index + 16 + 4 * q) = b;
+  }
+}
+
 }  // namespace mx4
 
 // ---------------------------------------------------------------------------
