@@ -78,6 +78,7 @@ size_t moe_workspace_size(int op, int T, int k, int E_loc, int H, int I) {
     case MOE_OP_DECODE_LAYER: return moe_decode_layer_workspace_size(T, k, E_loc, I);
     case MOE_OP_SHARED_EXPERT: return moe_shared_workspace_size(T, I, MOE_BF16);
     case MOE_OP_SHARED_EXPERT_F32: return moe_shared_workspace_size(T, I, MOE_F32);
+    case MOE_OP_DECODE_LAYER_MX4: return moe_decode_layer_mx4_workspace_size(T, k, E_loc, H, I);
     case MOE_OP_GROUPED_FFN_MX4: return moe_ffn_mx4_workspace_size(T, k, E_loc, H, I, MOE_F32);
     default: return 0;
   }

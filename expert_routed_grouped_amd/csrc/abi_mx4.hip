@@ -106,4 +106,48 @@ int moe_grouped_ffn_mx4(const uint8_t *a_codes, const uint8_t *a_scales, int a_d
   return hip_status(launch_ffn_mx4(fa, (hipStream_t)stream));
 }
 
+size_t moe_decode_layer_mx4_workspace_size(int T, int k, int E_loc, int H, int I) {
+  if (T < 0 || T > kMx4StreamMaxT || E_loc > kDecodeMx4MaxE || H > kDecodeMx4MaxH || !ffn_sizes_ok(T, k, E_loc, H, I)) return 0;
+  return decode_layer_mx4_ws_bytes(T, k, E_loc, H, I);
+}
+
+int moe_decode_layer_mx4(const void *x, const float *w_router_packed, const float *bias, int T, int H, int E, int k,
+                         int e_begin, int e_end, int I, const uint8_t *wgu_codes, const uint8_t *wgu_scales,
+                         const uint8_t *wd_codes, const uint8_t *wd_scales, int32_t *topk_ids, float *topk_w, void *y,
+                         int y_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+  if (T < 0 || T > kMx4StreamMaxT || E < 1 || E > kDecodeMx4MaxE || k < 1 || k > E || e_begin < 0 || e_end <= e_begin ||
+      e_end > E || H > kDecodeMx4MaxH || !ffn_sizes_ok(T, k, e_end - e_begin, H, I))
+    return MOE_ERR_SHAPE;
+  if (y_dtype != MOE_F32 && y_dtype != MOE_BF16) return MOE_ERR_DTYPE;
+  if (T == 0) return MOE_OK;
+  if (!x || !w_router_packed || !wgu_codes || !wgu_scales || !wd_codes || !wd_scales || !topk_ids || !topk_w || !y)
+    return MOE_ERR_NULL;
+  const int El = e_end - e_begin;
+  if (!workspace || workspace_bytes < moe_decode_layer_mx4_workspace_size(T, k, El, H, I)) return MOE_ERR_WORKSPACE;
+  if (!aligned(x, 16) || !aligned(w_router_packed, 16) || !aligned(wgu_codes, 16) || !aligned(wgu_scales, 16) ||
+      !aligned(wd_codes, 16) || !aligned(wd_scales, 16) || !aligned(y, 16) || !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  DecodeMx4Args a{};
+  a.x = x;
+  a.wr = w_router_packed;
+  a.bias = bias;
+  a.T = T;
+  a.H = H;
+  a.E = E;
+  a.k = k;
+  a.lo = e_begin;
+  a.El = El;
+  a.I = I;
+  a.wgu = wgu_codes;
+  a.wgu_s = wgu_scales;
+  a.wd = wd_codes;
+  a.wd_s = wd_scales;
+  a.ids = topk_ids;
+  a.gates = topk_w;
+  a.y = y;
+  a.y_bf16 = y_dtype == MOE_BF16;
+  a.ws = workspace;
+  return hip_status(launch_decode_layer_mx4(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -190,3 +190,22 @@ hipError_t launch_ffn_mx4(const FfnMx4Args &a, hipStream_t s);
 constexpr int kMx4StreamMaxT = 64;
 hipError_t launch_ffn_mx4_stream(const FfnMx4Args &a, uint8_t *h, uint8_t *hs, hipStream_t s);
 hipError_t launch_down_sum_mx4(const FfnMx4Args &a, const uint8_t *h, const uint8_t *hs, hipStream_t s);
+
+// The whole layer of a few tokens (decode_mx4.hip): T <= kMx4StreamMaxT.  Its workspace starts with control words that
+// are zero before the call and after it (the error word, uint32 number 4, excepted).
+constexpr int kDecodeMx4MaxH = 8192, kDecodeMx4MaxE = 256;
+struct DecodeMx4Args {
+  const void *x;               // [T, H] bf16
+  const float *wr;             // router weight, fp32 packed [H/4, E, 4]
+  const float *bias;           // [E] or NULL
+  int T, H, E, k, lo, El, I;
+  const uint8_t *wgu, *wgu_s;  // packed codes and scales of [El, 2I, H]
+  const uint8_t *wd, *wd_s;    // packed codes and scales of [El, H, I]
+  int32_t *ids;                // [T, k]
+  float *gates;                // [T, k]
+  void *y;                     // [T, H], overwritten
+  int y_bf16;
+  void *ws;
+};
+size_t decode_layer_mx4_ws_bytes(int T, int k, int El, int H, int I);
+hipError_t launch_decode_layer_mx4(const DecodeMx4Args &a, hipStream_t s);

@@ -31,10 +31,10 @@ EXPORTS = ("moe_version", "moe_status_str", "moe_route", "moe_permute", "moe_per
            "moe_route_dispatch", "moe_pack_weights", "moe_pack_router", "moe_grouped_ffn_noalloc",
            "moe_decode_layer_workspace_size", "moe_decode_layer", "moe_workspace_size", "moe_quantize_mx4",
            "moe_dequantize_mx", "moe_mx4_packed_scale_bytes", "moe_pack_mx4", "moe_ffn_mx4_workspace_size",
-           "moe_grouped_ffn_mx4")
+           "moe_grouped_ffn_mx4", "moe_decode_layer_mx4_workspace_size", "moe_decode_layer_mx4")
 MOE_OP_PERMUTE, MOE_OP_GROUPED_FFN, MOE_OP_GROUPED_FFN_F32, MOE_OP_GROUPED_FFN_MX = 0, 1, 2, 3
 MOE_OP_ROUTE_DISPATCH, MOE_OP_DECODE_LAYER, MOE_OP_SHARED_EXPERT, MOE_OP_SHARED_EXPERT_F32 = 4, 5, 6, 7
-MOE_OP_GROUPED_FFN_MX4 = 8
+MOE_OP_GROUPED_FFN_MX4, MOE_OP_DECODE_LAYER_MX4 = 8, 9
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -111,6 +111,10 @@ def lib():
         L.moe_ffn_mx4_workspace_size.argtypes = [I, I, I, I, I, I]
         L.moe_grouped_ffn_mx4.restype = I
         L.moe_grouped_ffn_mx4.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, P, P, P, P, P, I, P, Z, P]
+        L.moe_decode_layer_mx4_workspace_size.restype = Z
+        L.moe_decode_layer_mx4_workspace_size.argtypes = [I, I, I, I, I]
+        L.moe_decode_layer_mx4.restype = I
+        L.moe_decode_layer_mx4.argtypes = [P, P, P, I, I, I, I, I, I, I, P, P, P, P, P, P, P, I, P, Z, P]
         _lib = L
     return _lib
 
@@ -557,3 +561,48 @@ def moe_grouped_ffn_mx4(a_codes: torch.Tensor, a_scales: torch.Tensor, offsets: 
             _ptr(row_w), _ptr(token_row), El, T, k, H, I, _ptr(wgu[0]), _ptr(wgu[1]), _ptr(wd[0]), _ptr(wd[1]),
             _ptr(y), ydt, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
     return y
+
+
+def moe_decode_layer_mx4_workspace(T: int, k: int, E_loc: int, H: int, I: int, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for moe_decode_layer_mx4 (its control words must start at zero)."""
+    return torch.zeros(int(lib().moe_decode_layer_mx4_workspace_size(T, k, E_loc, H, I)), dtype=torch.uint8,
+                       device=device)
+
+
+def moe_decode_layer_mx4(x: torch.Tensor, w_router_packed: torch.Tensor, bias: Optional[torch.Tensor], k: int,
+                         e_begin: int, e_end: int, wgu, wd, workspace: torch.Tensor,
+                         topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                         y: Optional[torch.Tensor] = None, dtype=torch.bfloat16, stream=None):
+    """The whole MoE layer of up to 64 tokens with MXFP4 experts -> (y [T, H] of ``dtype``, topk_ids, topk_w).
+    ``w_router_packed`` is the fp32 [H/4, E, 4] tensor of moe_pack_router, ``wgu`` and ``wd`` the (codes, scales)
+    pairs of moe_pack_mx4 for the experts [e_begin, e_end), ``workspace`` starts zeroed
+    (moe_decode_layer_mx4_workspace; decode_layer_error_word reads its diagnostic)."""
+    El, H, I = _mx4_weights(wgu, wd)
+    T, dev = x.shape[0], x.device
+    if w_router_packed.dim() != 3:
+        raise ValueError("w_router_packed must be the [H/4, E, 4] tensor of moe_pack_router")
+    E = w_router_packed.shape[1]
+    if El != e_end - e_begin:
+        raise ValueError(f"weights hold {El} experts, [{e_begin}, {e_end}) has {e_end - e_begin}")
+    with _on(x):
+        if topk_ids is None:
+            topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if topk_w is None:
+            topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        if y is None:
+            y = torch.empty((T, H), dtype=dtype, device=dev)
+        ydt = _out_dtype(y.dtype)
+        _need(x, "x", torch.bfloat16, (T, H), dev)
+        _need(w_router_packed, "w_router_packed", torch.float32, (H // 4, E, 4), dev)
+        if bias is not None:
+            _need(bias, "bias", torch.float32, (E,), dev)
+        _need(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+        _need(topk_w, "topk_w", torch.float32, (T, k), dev)
+        _need(wgu[0], "w_gate_up codes", torch.uint8, wgu[0].shape, dev)
+        _need(y, "y", y.dtype, (T, H), dev)
+        _need(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        _check("moe_decode_layer_mx4", lib().moe_decode_layer_mx4(
+            _ptr(x), _ptr(w_router_packed), _ptr(bias), T, H, E, k, e_begin, e_end, I, _ptr(wgu[0]), _ptr(wgu[1]),
+            _ptr(wd[0]), _ptr(wd[1]), _ptr(topk_ids), _ptr(topk_w), _ptr(y), ydt, _ptr(workspace), workspace.numel(),
+            _stream(stream)))
+    return y, topk_ids, topk_w

@@ -103,6 +103,7 @@ extern "C" {
 #define MOE_OP_SHARED_EXPERT 6    /* moe_shared_expert with bf16 activations (I = I_s, E_loc and k unused) */
 #define MOE_OP_SHARED_EXPERT_F32 7 /* moe_shared_expert with fp32 activations */
 #define MOE_OP_GROUPED_FFN_MX4 8   /* moe_grouped_ffn_mx4 with fp32 output (enough for bf16 output too) */
+#define MOE_OP_DECODE_LAYER_MX4 9  /* moe_decode_layer_mx4 */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int moe_version(void);
@@ -437,6 +438,36 @@ int moe_grouped_ffn_mx4(const uint8_t *a_codes, const uint8_t *a_scales, int a_d
                         int H, int I, const uint8_t *wgu_codes, const uint8_t *wgu_scales, const uint8_t *wd_codes,
                         const uint8_t *wd_scales, void *y, int y_dtype, void *workspace, size_t workspace_bytes,
                         void *stream);
+
+/* Bytes of workspace moe_decode_layer_mx4 needs (0 for sizes it does not take). */
+size_t moe_decode_layer_mx4_workspace_size(int T, int k, int E_loc, int H, int I);
+
+/*
+ * moe_decode_layer_mx4 - the whole MoE layer of a few tokens with MXFP4 experts, in two launches.
+ *
+ * Defined by: "Hosting Qwen on Blackwell", section "Expert parallelism" (for decoding the MoE kernels are
+ * merged), with the steps of moe_route, moe_permute, moe_quantize_mx and moe_grouped_ffn_mx4.
+ *
+ * Results: topk_ids, topk_w [T, k] exactly as moe_route (bit for bit); y [T, H] of y_dtype overwritten with
+ *   y[t, :] = sum over the local assignments (t, j) of topk_w[t, j] * FFN_{topk_ids[t, j]}(x[t, :])
+ * where the FFN is that of moe_grouped_ffn_mx4 with x and h as MXFP8 and the sum, in fp32, is rounded once.
+ * The order of the sum is fixed by the routing.  A block of 32 values of x that holds a NaN or an infinity
+ * reads as NaN in the experts' products, so that y of that token is NaN; other tokens are not affected.
+ *
+ * x [T, H] bf16; w_router_packed [H/4, E, 4] fp32 as moe_pack_router writes it; bias [E] or NULL; weights of
+ * the local experts [e_begin, e_end) as moe_pack_mx4 writes them.  0 <= T <= 64, E <= 256, 1 <= k <= min(E,
+ * 32), H and I multiples of 128, H <= 8192.  Pointers 16-byte aligned.  T == 0 enqueues nothing.
+ * The workspace (moe_decode_layer_mx4_workspace_size bytes, 256-byte aligned) must be all zero before its first
+ * call (zero it once when allocating); every call leaves its control words zero again, and it serves calls of
+ * any smaller or equal sizes.  Calls that overlap in time must not share a workspace (two captured graphs that
+ * may run at once need one each).  Its uint32 word 4 (byte 16) is a diagnostic: nonzero if a wait inside the
+ * kernel gave up (never expected; the results of that call are then invalid); the library does not clear it.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_WORKSPACE, MOE_ERR_ALIGN, MOE_ERR_HIP.
+ */
+int moe_decode_layer_mx4(const void *x, const float *w_router_packed, const float *bias, int T, int H, int E, int k,
+                         int e_begin, int e_end, int I, const uint8_t *wgu_codes, const uint8_t *wgu_scales,
+                         const uint8_t *wd_codes, const uint8_t *wd_scales, int32_t *topk_ids, float *topk_w, void *y,
+                         int y_dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * moe_combine - gate-weighted gather-sum of per-row outputs back to token order.

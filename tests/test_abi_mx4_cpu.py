@@ -97,6 +97,36 @@ def test_ffn_workspace_size():
     assert moe.moe_workspace_size(moe.MOE_OP_GROUPED_FFN_MX4, 100, 8, 128, 4096, 1536) == f(100, 8, 128, 4096, 1536)
 
 
+def layer(**kw):
+    a = dict(x=A, wr=A, b=None, T=4, H=256, E=16, k=2, lo=0, hi=16, I=128, gc=A, gs=A, dc=A, ds=A, ids=A, w=A, y=A, yd=1,
+             ws=A, wsb=1 << 30)
+    a.update(kw)
+    return moe.lib().moe_decode_layer_mx4(a["x"], a["wr"], a["b"], a["T"], a["H"], a["E"], a["k"], a["lo"], a["hi"], a["I"],
+                                          a["gc"], a["gs"], a["dc"], a["ds"], a["ids"], a["w"], a["y"], a["yd"], a["ws"],
+                                          a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), -2), (dict(T=65), -2), (dict(E=257, hi=257), -2), (dict(k=0), -2), (dict(k=17), -2),
+    (dict(E=64, k=33, hi=64), -2), (dict(lo=-1), -2), (dict(lo=3, hi=3), -2), (dict(hi=17), -2), (dict(H=200), -2),
+    (dict(H=8320), -2), (dict(I=96), -2), (dict(yd=2), -3), (dict(x=None), -1), (dict(wr=None), -1), (dict(gc=None), -1),
+    (dict(gs=None), -1), (dict(dc=None), -1), (dict(ds=None), -1), (dict(ids=None), -1), (dict(w=None), -1),
+    (dict(y=None), -1), (dict(ws=None), -4), (dict(wsb=5000), -4), (dict(x=off(A, 8)), -6), (dict(wr=off(A, 8)), -6),
+    (dict(ds=off(A, 8)), -6), (dict(y=off(A, 4)), -6), (dict(ws=off(A, 64)), -6), (dict(T=0, x=None, ws=None), 0),
+])
+def test_layer_validation(kw, code):
+    assert layer(**kw) == code
+
+
+def test_layer_workspace_size():
+    f = moe.lib().moe_decode_layer_mx4_workspace_size
+    assert f(8, 8, 128, 4096, 1536) >= 256 + 8 * 4096 + 64 * (1536 + 48)
+    assert f(65, 8, 128, 4096, 1536) == 0 and f(8, 8, 257, 4096, 1536) == 0 and f(8, 8, 128, 8320, 1536) == 0
+    assert f(8, 8, 128, 4100, 1536) == 0
+    assert all(f(t, 8, 128, 4096, 1536) <= f(t + 1, 8, 128, 4096, 1536) for t in range(64 - 1))
+    assert moe.moe_workspace_size(moe.MOE_OP_DECODE_LAYER_MX4, 8, 8, 128, 4096, 1536) == f(8, 8, 128, 4096, 1536)
+
+
 def test_binding_refuses_host_and_misshapen_tensors():
     u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
     with pytest.raises(ValueError):
@@ -124,4 +154,15 @@ def test_binding_refuses_host_and_misshapen_tensors():
                 dict(wgu=(u8(2, 15, 2, 1024), u8(2, 15, 1, 256))), dict(y=torch.zeros((3, 128)))):
         with pytest.raises(ValueError) as err:
             moe.moe_grouped_ffn_mx4(**{**ok, **bad})
+        assert "on the GPU" not in str(err.value)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    ok = dict(x=bf(3, 256), w_router_packed=torch.zeros(64, 8, 4), bias=None, k=2, e_begin=0, e_end=2, wgu=wgu, wd=wd,
+              workspace=u8(100000))
+    with pytest.raises(ValueError, match="GPU"):
+        moe.moe_decode_layer_mx4(**ok)
+    for bad in (dict(x=bf(3, 128)), dict(x=torch.zeros(3, 256)), dict(w_router_packed=torch.zeros(8, 256)),
+                dict(w_router_packed=torch.zeros(32, 8, 4)), dict(e_end=3), dict(bias=torch.zeros(7)),
+                dict(topk_ids=i32(3, 3)), dict(y=bf(2, 256)), dict(workspace=torch.zeros(1000))):
+        with pytest.raises(ValueError) as err:
+            moe.moe_decode_layer_mx4(**{**ok, **bad})
         assert "on the GPU" not in str(err.value)

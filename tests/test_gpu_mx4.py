@@ -285,3 +285,168 @@ def test_grouped_ffn_empty_batch():
     assert y.shape == (0, 256)
     c, sc = moe.moe_quantize_mx4(e(0, 64, dt=torch.bfloat16))
     assert c.shape == (0, 32) and moe.moe_dequantize_mx(c, sc).shape == (0, 64)
+
+
+# ------------------------------------------------------------------ the few-token layer
+def check_clean(ws):
+    ctl = ws[:256].view(torch.int32).cpu()
+    assert int(ctl[4]) == 0, "a wait inside the kernel gave up"
+    assert not ctl[:4].any(), "control words not reset"
+
+
+def layer_setup(T, E, k, H, I, lo, hi, seed, even=True, bias=False):
+    s = setup(T, E, k, H, I, lo, hi, seed, even=even)
+    g = gen(seed + 1)
+    s["wr"] = (torch.randn((E, H), device=DEV, generator=g) * 0.05).bfloat16()
+    s["bias"] = torch.randn(E, device=DEV, generator=g) if bias else None
+    s["router"] = moe.moe_pack_router(s["wr"])
+    return s
+
+
+def run_layer(s, k, lo, hi, ws, dtype=torch.bfloat16, **kw):
+    return moe.moe_decode_layer_mx4(s["x"], s["router"], s["bias"], k, lo, hi, s["wgu"], s["wd"], ws, dtype=dtype, **kw)
+
+
+LAYERS = [
+    # T, E, k, H, I, lo, hi, bias
+    (1, 8, 2, 256, 128, 0, 8, False),
+    (1, 128, 8, 1024, 512, 0, 128, True),
+    (2, 64, 1, 128, 128, 0, 64, False),     # one step of the contraction
+    (5, 65, 8, 640, 384, 0, 65, True),      # experts past a multiple of 64, K not a multiple of 512
+    (17, 16, 4, 384, 256, 3, 11, False),    # local experts, more rows than a tile
+    (33, 200, 6, 512, 128, 0, 200, False),
+    (64, 8, 8, 256, 256, 0, 8, True),       # every token on every expert
+    (64, 256, 8, 384, 128, 64, 128, False),
+    (64, 40, 32, 128, 128, 0, 40, False),   # the most rows
+    (3, 1, 1, 128, 128, 0, 1, False),       # one expert
+    (4, 16, 2, 8192, 128, 0, 16, False),    # the widest
+]
+
+
+@pytest.mark.parametrize("shape", LAYERS, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_decode_layer(shape, dtype):
+    """Routing bit for bit as moe_route; y inside the interval; the workspace's control words zero again; the
+    same call again gives the same bits."""
+    T, E, k, H, I, lo, hi, bias = shape
+    s = layer_setup(T, E, k, H, I, lo, hi, seed=T * E + H, bias=bias)
+    ids, w = moe.moe_route(s["x"], s["wr"], s["bias"], k)
+    ws = moe.moe_decode_layer_mx4_workspace(T, k, hi - lo, H, I)
+    y, ids2, w2 = run_layer(s, k, lo, hi, ws, dtype)
+    check_clean(ws)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    xv, _ = R.quantize(s["x"], "mxfp8")
+    mid, rad = R.layer(xv, ids, w, lo, hi - lo, lambda e: s["gv"][e], lambda e: s["dv"][e], "mxfp8", dtype,
+                       rows_rounded=False)
+    R.check_interval(y, mid, rad, str(shape))
+    y2, _, _ = run_layer(s, k, lo, hi, ws, dtype)
+    check_clean(ws)
+    assert torch.equal(y, y2)
+
+
+def test_decode_layer_full_width():
+    T, E, k, H, I = 6, 32, 8, 4096, 1536
+    s = layer_setup(T, E, k, H, I, 0, E, seed=3)
+    ws = moe.moe_decode_layer_mx4_workspace(T, k, E, H, I)
+    y, ids, w = run_layer(s, k, 0, E, ws)
+    ids1, w1 = moe.moe_route(s["x"], s["wr"], s["bias"], k)
+    assert torch.equal(ids, ids1) and torch.equal(w, w1)
+    xv, _ = R.quantize(s["x"], "mxfp8")
+    mid, rad = R.layer(xv, ids, w, 0, E, lambda e: s["gv"][e], lambda e: s["dv"][e], "mxfp8", torch.bfloat16, False)
+    R.check_interval(y, mid, rad, "full width")
+
+
+def test_decode_layer_routing_ties_and_zero_router():
+    """Equal logits go to the lower index, also across 64-expert items; a zero router picks the first k."""
+    s = layer_setup(7, 130, 5, 256, 128, 0, 130, seed=4)
+    s["wr"][70] = s["wr"][3]
+    s["wr"][129] = s["wr"][3]
+    for wr in (s["wr"], torch.zeros_like(s["wr"])):
+        s["wr"], s["router"] = wr, moe.moe_pack_router(wr)
+        ws = moe.moe_decode_layer_mx4_workspace(7, 5, 130, 256, 128)
+        _, ids, w = run_layer(s, 5, 0, 130, ws)
+        ids1, w1 = moe.moe_route(s["x"], wr, None, 5)
+        assert torch.equal(ids, ids1) and torch.equal(w, w1)
+    assert torch.equal(ids.cpu(), torch.arange(5, dtype=torch.int32).repeat(7, 1))
+
+
+def test_decode_layer_one_workspace_many_sizes():
+    """One workspace of the largest size serves smaller calls in any order."""
+    big = dict(E=24, k=4, H=512, I=256)
+    ws = moe.moe_decode_layer_mx4_workspace(64, 4, 24, 512, 256)
+    for T in (64, 1, 30, 2, 64):
+        s = layer_setup(T, **big, lo=0, hi=24, seed=T)
+        y, ids, w = run_layer(s, 4, 0, 24, ws)
+        check_clean(ws)
+        fresh, _, _ = run_layer(s, 4, 0, 24, moe.moe_decode_layer_mx4_workspace(T, 4, 24, 512, 256))
+        assert torch.equal(y, fresh)
+
+
+def test_decode_layer_no_local_rows_and_bad_token():
+    s = layer_setup(9, 16, 2, 256, 128, 0, 4, seed=5)
+    ws = moe.moe_decode_layer_mx4_workspace(9, 2, 4, 256, 128)
+    s["bias"] = torch.zeros(16, device=DEV)
+    s["bias"][8:] = 1e4  # every token on experts that are not local
+    y = torch.full((9, 256), math.nan, dtype=torch.bfloat16, device=DEV)
+    run_layer(s, 2, 0, 4, ws, y=y)
+    check_clean(ws)
+    assert not y.any()
+    s["bias"] = torch.zeros(16, device=DEV)
+    s["bias"][:4] = 1e4  # every token local
+    y0, ids0, _ = run_layer(s, 2, 0, 4, ws)
+    s["x"][4, 100] = math.inf
+    y1, ids1, _ = run_layer(s, 2, 0, 4, ws)
+    check_clean(ws)
+    keep = torch.arange(9, device=DEV) != 4
+    assert y1[4].isnan().all() and torch.equal(y1[keep], y0[keep]) and torch.equal(ids1[keep], ids0[keep])
+
+
+def test_decode_layer_agrees_with_the_composed_calls():
+    """moe_route, moe_permute, moe_quantize_mx and moe_grouped_ffn_mx4 one after another: same routing and
+    the same products in the same order, so the same y bit for bit."""
+    s = layer_setup(20, 48, 6, 1024, 512, 8, 40, seed=6, even=False)
+    ws = moe.moe_decode_layer_mx4_workspace(20, 6, 32, 1024, 512)
+    y, ids, w = run_layer(s, 6, 8, 40, ws)
+    ids1, w1 = moe.moe_route(s["x"], s["wr"], s["bias"], 6)
+    assert torch.equal(ids, ids1) and torch.equal(w, w1)
+    s["ids"], s["gates"] = ids1, w1
+    y1, _ = run_ffn(s, 48, 8, 40, "mxfp8", torch.bfloat16)
+    assert torch.equal(y, y1)
+
+
+def test_decode_layer_graph_streams_and_empty():
+    """Captured and replayed with new inputs between eager calls on another workspace; two streams at once with a
+    workspace each; T = 0."""
+    T, E, k, H, I = 12, 32, 4, 512, 256
+    s = layer_setup(T, E, k, H, I, 0, E, seed=7)
+    ws, ws2 = (moe.moe_decode_layer_mx4_workspace(T, k, E, H, I) for _ in range(2))
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+    ids = torch.empty((T, k), dtype=torch.int32, device=DEV)
+    w = torch.empty((T, k), dtype=torch.float32, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    run_layer(s, k, 0, E, ws, topk_ids=ids, topk_w=w, y=y, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run_layer(s, k, 0, E, ws, topk_ids=ids, topk_w=w, y=y)
+    g = gen(8)
+    for _ in range(4):
+        s["x"].copy_(R.even_rows((T, H), g, DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = (y.clone(), ids.clone(), w.clone())
+        want = run_layer(s, k, 0, E, ws2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):  # both streams busy at once
+        a = run_layer(s, k, 0, E, ws)
+        with torch.cuda.stream(side):
+            b = run_layer(s, k, 0, E, ws2)
+    torch.cuda.synchronize()
+    check_clean(ws)
+    check_clean(ws2)
+    assert torch.equal(a[0], want[0]) and torch.equal(b[0], want[0])
+    s["x"] = s["x"][:0]
+    assert run_layer(s, k, 0, E, ws)[0].shape == (0, H)
