@@ -1,20 +1,21 @@
 // The whole MoE layer of a few tokens with MXFP4 experts in two launches (moe_decode_layer_mx4).
 //
 // Launch 1 routes, groups and computes the intermediate h; launch 2 is the down half of mx4_stream.h, which also
-// sums to token order.  In launch 1 the resident workgroups draw tickets.  The first T * ceil(E / 64) tickets are
-// routing items (token t, 64 experts): the row of x is widened into LDS (the item of the first experts also
-// quantises it to MXFP8 for the experts' products) and one wave computes 64 logits, one lane each, with the
-// library's fp32 chain over ascending h.  The last item to finish takes the top k of every token, groups the
-// assignments by expert, lists the experts' tiles and raises a flag.  A workgroup whose ticket is past the routing
-// items waits for the flag (its wait is for workgroups that drew earlier tickets, so they run; it is bounded
-// all the same) and then takes its share of the gate/up tiles.
+// sums to token order (and zeroes the control words).  In launch 1 the resident workgroups draw tickets.  The
+// first T * ceil(E / 64) tickets are routing items (token t, 64 experts): the row of x is widened into LDS (the item
+// of the first experts also quantises it to MXFP8 for the experts' products), one wave computes 64 logits, one
+// lane each, with the library's fp32 chain over ascending h, and counts itself done.  A workgroup whose ticket is
+// past the routing items waits for that count (for workgroups that drew earlier tickets, so they run; the wait is
+// bounded all the same).  Then every workgroup takes the top k of every token and groups the assignments for
+// itself, in LDS, rather than wait for one that does it and hands it out (a hand-over between workgroups on
+// different XCDs costs about 5 us), the one with the first free ticket writes it down, and all share the gate/up
+// tiles.
 //
 // What bounds it: at one token the chain, H dependent additions whose order is the routing contract (about 3 ns
-// each), then the weights' bytes.  Against instruction issue the chain has the packed fp32 router (no unpacking), its
-// x operand broadcast inside rows of 16 lanes by the FMA itself (DPP), so 16 steps cost 16 FMAs, four loads and
-// one LDS read; and the matrix is touched by the idle waves beforehand, so that the loads find it in L2.
+// each), then the weights' bytes.  Against instruction issue the chain has the packed fp32 router (no unpacking)
+// and its x operand broadcast inside rows of 16 lanes by the FMA itself (DPP), so 16 steps cost 16 FMAs, four loads
+// and one LDS read: 16 us of 4096 steps.  (Touching the matrix beforehand with the idle waves made it slower, 23 us.)
 #include "mx4_stream.h"
-#include "permute_dev.h"
 #include "route_dev.h"
 
 #include <mutex>
@@ -22,30 +23,31 @@
 namespace {
 
 constexpr int NTHR = mx4s::NTHR, NW = mx4s::NW;
-constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the routed flag before giving up (seconds)
+constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the count before giving up (seconds)
 
 // control words
-enum : int { kTicket = 0, kDone = 1, kRouted = 2, kExit = 3, kError = 4, kTiles = 5, kCtlBytes = 256 };
+enum : int { kTicket = 0, kDone = 1, kError = 4, kCtlBytes = 256 };
 
 struct Params {
   const uint16_t *x;   // [T, H] bf16
   const float *wr;     // [H/4, E, 4] fp32
   const float *bias;   // [E] or NULL
-  int T, H, E, k, lo, El, I, nbits, R_cap, n_route;
+  int T, H, E, k, lo, El, I, R_cap, n_route;
   int32_t *ids;
   float *gates;
   uint32_t *ctl;
   float *logits;       // [T, 64 EC]
   uint8_t *xq, *xs;    // x as MXFP8
-  int32_t *counts, *offsets, *row_token, *token_row;
+  int32_t *offsets, *row_token;
   float *row_w;
-  int2 *tiles;         // {first row, expert | rows << 16}
   const uint8_t *wgu, *wgu_s;
   uint8_t *h, *hs;
 };
 
-__device__ __forceinline__ uint32_t ld_agent(const uint32_t *p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// What a routing item hands to other workgroups is stored at agent scope, i.e. through to memory, so that nothing
+// has to be written back before it counts itself done.
+__device__ __forceinline__ void st_agent(uint32_t *p, uint32_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // acc += x[h] w[h] for 16 steps in order: lane l holds x[h0 + l % 16], w[i] the weights of steps 4i .. 4i+3.  The FMA
@@ -66,21 +68,13 @@ __device__ __forceinline__ float chain16(float acc, float xv, const f32x4_t (&w)
 __device__ __forceinline__ void route_item(const Params &p, int t, int c, int EP, float *xf) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int H = p.H;
-  uint32_t touch = 0;
-  if (wave > 0) {  // the chain's 1 KB lines, one access per 128 bytes
-    const char *base = (const char *)p.wr + (size_t)c * 1024;
-    const int width = min(p.E - 64 * c, 64) * 16;  // bytes of a 4-wide h group in this item's slice
-    const int per = (width + 127) / 128, n = H / 4 * per;
-    for (int i = threadIdx.x - 64; i < n; i += NTHR - 64)
-      touch |= *(const volatile uint32_t *)(base + (size_t)(i / per) * p.E * 16 + min((i % per) * 128, width - 4));
-  }
   for (int v = threadIdx.x; v < H / 8; v += NTHR) {
     const u32x4_t r = *((const u32x4_t *)(p.x + (size_t)t * H) + v);
     const float f[8] = {bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y),
                         bf16_lo(r.z), bf16_hi(r.z), bf16_lo(r.w), bf16_hi(r.w)};
     *(f32x4_t *)(xf + 8 * v) = f32x4_t{f[0], f[1], f[2], f[3]};
     *(f32x4_t *)(xf + 8 * v + 4) = f32x4_t{f[4], f[5], f[6], f[7]};
-    if (c == 0) {  // H is a multiple of 128: the four lanes of a block loop together
+    if (c == 0) {  // H is a multiple of 128: 16 neighbouring lanes loop together
       uint32_t m = 0;
 #pragma unroll
       for (int j = 0; j < 8; j++) m = max(m, mx4::abs_bits(f[j]));
@@ -91,8 +85,14 @@ __device__ __forceinline__ void route_item(const Params &p, int t, int c, int EP
 #pragma unroll
       for (int j = 0; j < 8; j++) u[j] = ldexpf(f[j], 127 - (int)s);
       const uint32_t lo = mx4::e4m3_quad(u[0], u[1], u[2], u[3]), hi = mx4::e4m3_quad(u[4], u[5], u[6], u[7]);
-      *(uint2 *)(p.xq + (size_t)t * H + 8 * v) = s == 255 ? make_uint2(0, 0) : make_uint2(lo, hi);
-      if ((v & 3) == 0) p.xs[(size_t)t * (H / 32) + (v >> 2)] = (uint8_t)s;
+      uint32_t *xq = (uint32_t *)(p.xq + (size_t)t * H + 8 * v);
+      st_agent(xq, s == 255 ? 0u : lo);
+      st_agent(xq + 1, s == 255 ? 0u : hi);
+      // the scale bytes of four blocks (16 lanes) as one dword
+      uint32_t w = s << (8 * ((v >> 2) & 3));
+      w |= (uint32_t)__shfl_xor((int)w, 4, 64);
+      w |= (uint32_t)__shfl_xor((int)w, 8, 64);
+      if ((v & 15) == 0) st_agent((uint32_t *)(p.xs + (size_t)t * (H / 32) + (v >> 2)), w);
     }
   }
   __syncthreads();
@@ -126,37 +126,84 @@ __device__ __forceinline__ void route_item(const Params &p, int t, int c, int EP
         acc = chain16(acc, xv[j], w[j]);
       }
     }
-    if (e < p.E) p.logits[(size_t)t * EP + e] = p.bias ? acc + p.bias[e] : acc;
+    if (e < p.E) st_agent((uint32_t *)p.logits + (size_t)t * EP + e, __float_as_uint(p.bias ? acc + p.bias[e] : acc));
   }
-  asm volatile("" ::"v"(touch));  // keeps the warm-up loads
 }
 
-// After every logit: top k and gates, the grouping, the tile list, the flag.
+// LDS after the partial sums (which the widened row of x shares): the grouping.  With at most 64 tokens, each on
+// distinct experts, an expert's rows are a 64-bit set of tokens: its count is the set's, a row's place in the
+// expert's group (token order) the number of lower members.
+struct Groups {
+  unsigned long long *set;  // [El]
+  int2 *sel;                // [T, k] {local expert or -1, gate}
+  int2 *tiles;              // {first row, expert | rows << 16}
+  int *first;               // [El] first row of an expert
+  int *token;               // [R_cap] token of a row
+  __device__ Groups(const Params &p, char *at) {
+    set = (unsigned long long *)at;
+    sel = (int2 *)(set + p.El);
+    tiles = sel + p.T * p.k;
+    first = (int *)(tiles + p.El + p.R_cap / mx4s::TM);
+    token = first + p.El;
+  }
+};
+constexpr size_t kGroupBytes = kDecodeMx4MaxE * 20 + kMx4StreamMaxT * 32 * 12 + kMx4StreamMaxT * 32 / mx4s::TM * 8;
+
+// Top k and gates, the grouping and the tile list; ``write``: also to memory.  Returns the number of tiles.
 template <int EC>
-__device__ __forceinline__ void group_all(const Params &p, int *smem) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int t = wave; t < p.T; t += NW)
-    rt::topk_token<EC>(p.logits + (size_t)t * 64 * EC, p.E, p.k, lane, p.ids + (size_t)t * p.k, p.gates + (size_t)t * p.k);
+__device__ __forceinline__ int group_all(const Params &p, const Groups &g, bool write, int *s_n) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), N = p.T * p.k;
+  for (int e = threadIdx.x; e < p.El; e += NTHR) g.set[e] = 0;
   __syncthreads();
-  perm::permute_block<NW>(p.ids, p.gates, p.T * p.k, p.k, p.lo, p.El, p.nbits, p.R_cap, p.counts, p.offsets,
-                          p.row_token, p.row_w, p.token_row, smem);
+  for (int t = wave; t < p.T; t += NW) {
+    int e;
+    float w;
+    rt::topk_lane<EC>(p.logits + (size_t)t * 64 * EC, p.E, p.k, lane, e, w);
+    if (lane < p.k) {
+      if (write) {
+        p.ids[(size_t)t * p.k + lane] = e;
+        p.gates[(size_t)t * p.k + lane] = w;
+      }
+      const int l = (unsigned)(e - p.lo) < (unsigned)p.El ? e - p.lo : -1;
+      if (l >= 0) atomicOr(g.set + l, 1ull << t);
+      g.sel[t * p.k + lane] = make_int2(l, __float_as_int(w));
+    }
+  }
   __syncthreads();
   if (wave == 0) {
-    int n0 = 0;
+    int n0 = 0, t0 = 0;
     for (int b = 0; b < p.El; b += 64) {
-      const int e = b + lane;
-      const int beg = e < p.El ? p.offsets[e] : 0, cnt = e < p.El ? p.offsets[e + 1] - beg : 0;
-      const int t = (cnt + mx4s::TM - 1) / mx4s::TM;
-      const int incl = ffn::wave_incl_scan_i(t, lane), at = n0 + incl - t;
+      const int e = b + lane, cnt = e < p.El ? __popcll(g.set[e]) : 0, t = (cnt + mx4s::TM - 1) / mx4s::TM;
+      const int ci = ffn::wave_incl_scan_i(cnt, lane), ti = ffn::wave_incl_scan_i(t, lane);
+      const int beg = n0 + ci - cnt;
+      if (e < p.El) {
+        g.first[e] = beg;
+        if (write) p.offsets[e] = beg;
+      }
       for (int i = 0; i < t; i++)
-        p.tiles[at + i] = make_int2(beg + i * mx4s::TM, e | min(mx4s::TM, cnt - i * mx4s::TM) << 16);
-      n0 += __shfl(incl, 63, 64);
+        g.tiles[t0 + ti - t + i] = make_int2(beg + i * mx4s::TM, e | min(mx4s::TM, cnt - i * mx4s::TM) << 16);
+      n0 += __shfl(ci, 63, 64);
+      t0 += __shfl(ti, 63, 64);
     }
-    if (lane == 0) p.ctl[kTiles] = (uint32_t)n0;
+    if (lane == 0) {
+      if (write) p.offsets[p.El] = n0;
+      *s_n = t0;
+    }
   }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
   __syncthreads();
-  if (threadIdx.x == 0) __hip_atomic_store(p.ctl + kRouted, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+  for (int a = threadIdx.x; a < N; a += NTHR) {
+    const int2 d = g.sel[a];
+    const int t = a / p.k;
+    if (d.x < 0) continue;
+    const int r = g.first[d.x] + __popcll(g.set[d.x] & ((1ull << t) - 1));
+    g.token[r] = t;
+    if (write) {
+      p.row_token[r] = t;
+      p.row_w[r] = __int_as_float(d.y);
+    }
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(*s_n);
 }
 
 template <int EC>
@@ -172,45 +219,35 @@ __global__ __launch_bounds__(NTHR, 2) void decode_route_gate_up_kernel(Params p)
     __syncthreads();  // everyone has the item before thread 0 may draw the next one
     if (item >= p.n_route) break;
     route_item(p, item / EC, item % EC, 64 * EC, lds);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");  // logits and x codes before the count
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's stores have reached memory
     __syncthreads();
-    if (threadIdx.x == 0) s_item = atomicAdd(p.ctl + kDone, 1u) == (uint32_t)p.n_route - 1u;
-    __syncthreads();
-    if (__builtin_amdgcn_readfirstlane(s_item)) {
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      group_all<EC>(p, (int *)lds);
-    }
+    if (threadIdx.x == 0) __hip_atomic_fetch_add(p.ctl + kDone, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // Closes thread 0's part before the next ticket.  Without it the compiler joins the two conditionals across the
+    // loop's back edge, and the other lanes of its wave go round the loop without it, for ever on the old ticket.
     __syncthreads();
   }
   if (threadIdx.x == 0) {
     int ok = 0;
-    for (uint32_t i = 0; i < kSpinLimit; i++) {
-      if (ld_agent(p.ctl + kRouted) != 0) {
-        ok = 1;
-        break;
-      }
-      __builtin_amdgcn_s_sleep(2);
+    for (uint32_t i = 0; i < kSpinLimit && !ok; i++) {
+      ok = __hip_atomic_load(p.ctl + kDone, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= (uint32_t)p.n_route;
+      if (!ok) __builtin_amdgcn_s_sleep(1);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");  // this CU's L1 and this XCD's L2 let go of older copies
     if (!ok) atomicOr(p.ctl + kError, 1u);
-    s_item = ok ? (int)ld_agent(p.ctl + kTiles) : 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");  // this CU's L1 and this XCD's L2 let go of older copies
   }
   __syncthreads();
-  const int nt = __builtin_amdgcn_readfirstlane(s_item), fid = item - p.n_route;
+  const int fid = item - p.n_route;
+  const Groups g(p, (char *)(lds + mx4s::RED_FLOATS));
+  const int nt = group_all<EC>(p, g, fid == 0, &s_item);
   const int ncb = p.I / 32, S = mx4s::split_for(nt * ncb, p.H), per = NW / S, nb = (ncb + per - 1) / per;
   for (int i = fid; i < nt * nb; i += gridDim.x) {
     const int ti = i / nb;
-    const int2 d = p.tiles[ti];
+    const int2 d = g.tiles[ti];
     const int r0 = __builtin_amdgcn_readfirstlane(d.x), er = __builtin_amdgcn_readfirstlane(d.y);
     const int cb = (i - ti * nb) * per + wave / S;
     mx4s::gate_up_tile<mx4::FP8>(mx4s::Half{p.xq, p.xs, p.wgu, p.wgu_s}, p.H, p.I, er & 0xffff, cb * 32, r0,
-                                 cb < ncb ? er >> 16 : 0, S, wave & (S - 1), [&](int r) { return (size_t)p.row_token[r]; },
+                                 cb < ncb ? er >> 16 : 0, S, wave & (S - 1), [&](int r) { return (size_t)g.token[r]; },
                                  p.h, p.hs, lds);
-  }
-  __syncthreads();
-  if (threadIdx.x == 0 && atomicAdd(p.ctl + kExit, 1u) == gridDim.x - 1u) {
-    // every other workgroup has left: zero the control words for the next call (not the error word)
-    for (int i = 0; i < kError; i++) __hip_atomic_store(p.ctl + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 
@@ -232,10 +269,9 @@ int resident_blocks(K kernel, size_t shm) {
   return cache[dev];
 }
 
-// LDS of launch 1: the widened row of x, the grouping's scratch or the partial sums, whichever is largest
-// (the same for every call, so that the resident count is too).
-constexpr size_t kLds = sizeof(float) * (kDecodeMx4MaxH > mx4s::RED_FLOATS ? kDecodeMx4MaxH : mx4s::RED_FLOATS);
-static_assert(kLds >= sizeof(int) * (NW + 1) * kDecodeMx4MaxE, "the grouping's scratch fits");
+// LDS of launch 1, the same for every call, so that the resident count is too.
+static_assert(kDecodeMx4MaxH <= mx4s::RED_FLOATS, "the widened row of x fits where the partial sums go");
+constexpr size_t kLds = sizeof(float) * mx4s::RED_FLOATS + kGroupBytes;
 
 template <int EC>
 hipError_t launch(const Params &p, hipStream_t s) {
@@ -250,7 +286,7 @@ hipError_t launch(const Params &p, hipStream_t s) {
 
 // Workspace pieces after the control words, each 256-byte aligned.
 struct Layout {
-  size_t logits, xq, xs, counts, offsets, row_token, token_row, row_w, tiles, h, hs, end;
+  size_t logits, xq, xs, offsets, row_token, row_w, h, hs, end;
   Layout(int T, int k, int El, int H, int I) {
     const size_t R = (size_t)T * (k < El ? k : El);
     size_t at = kCtlBytes;
@@ -262,12 +298,9 @@ struct Layout {
     logits = take((size_t)T * kDecodeMx4MaxE * 4);
     xq = take((size_t)T * H);
     xs = take((size_t)T * (H / 32));
-    counts = take((size_t)El * 4);
     offsets = take((size_t)(El + 1) * 4);
     row_token = take(R * 4);
-    token_row = take((size_t)T * k * 4);
     row_w = take(R * 4);
-    tiles = take((El + R / mx4s::TM) * sizeof(int2));
     h = take(R * I);
     hs = take(R * mx4::h_scale_stride(I));
     end = at;
@@ -293,7 +326,6 @@ hipError_t launch_decode_layer_mx4(const DecodeMx4Args &a, hipStream_t s) {
   p.lo = a.lo;
   p.El = a.El;
   p.I = a.I;
-  while ((1 << p.nbits) < a.El) p.nbits++;
   p.R_cap = a.T * (a.k < a.El ? a.k : a.El);
   p.n_route = a.T * EC;
   p.ids = a.ids;
@@ -302,12 +334,9 @@ hipError_t launch_decode_layer_mx4(const DecodeMx4Args &a, hipStream_t s) {
   p.logits = (float *)(ws + l.logits);
   p.xq = (uint8_t *)(ws + l.xq);
   p.xs = (uint8_t *)(ws + l.xs);
-  p.counts = (int32_t *)(ws + l.counts);
   p.offsets = (int32_t *)(ws + l.offsets);
   p.row_token = (int32_t *)(ws + l.row_token);
-  p.token_row = (int32_t *)(ws + l.token_row);
   p.row_w = (float *)(ws + l.row_w);
-  p.tiles = (int2 *)(ws + l.tiles);
   p.wgu = a.wgu;
   p.wgu_s = a.wgu_s;
   p.h = (uint8_t *)(ws + l.h);
@@ -327,5 +356,7 @@ hipError_t launch_decode_layer_mx4(const DecodeMx4Args &a, hipStream_t s) {
   d.wd_s = a.wd_s;
   d.y = a.y;
   d.y_bf16 = a.y_bf16;
+  d.zero = p.ctl;
+  d.n_zero = kDone + 1;
   return launch_down_sum_mx4(d, p.h, p.hs, s);
 }

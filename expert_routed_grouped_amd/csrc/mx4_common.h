@@ -182,6 +182,8 @@ struct FfnMx4Args {
   void *y;                     // [T, H], overwritten
   int y_bf16;
   void *ws;
+  uint32_t *zero;              // launch_down_sum_mx4 only: n_zero words that it zeroes, or NULL
+  int n_zero;
 };
 size_t ffn_mx4_ws_bytes(int T, int R_cap, int El, int H, int I, int y_bf16);
 hipError_t launch_ffn_mx4(const FfnMx4Args &a, hipStream_t s);

@@ -140,6 +140,8 @@ struct DownArgs {
   int El, T, R_cap, H, I;
   Half p;                  // h rows and the down weights
   void *y;                 // [T, H], overwritten
+  uint32_t *zero;          // n_zero words to zero for the next call, or NULL
+  int n_zero;
 };
 
 // LDS of the down half: sums [NW][T][16], one staged operand piece per wave, tile list {first row, expert | rows
@@ -164,6 +166,7 @@ __global__ __launch_bounds__(NTHR) void down_sum_kernel(DownArgs a) {
   int2 *tiles = (int2 *)((char *)(lds + NW * a.T * 16) + NW * stage_bytes<FA>());
   int2 *rowinfo = tiles + cap;  // {token, gate bits}
   float *tot = lds + wave * a.T * 16;
+  if (blockIdx.x == 0 && (int)threadIdx.x < a.n_zero) a.zero[threadIdx.x] = 0;
   for (int i = lane; i < a.T * 4; i += 64) *(f32x4_t *)(tot + 4 * i) = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int i = threadIdx.x; i < a.R_cap; i += NTHR) rowinfo[i] = make_int2(a.row_token[i], __float_as_int(a.row_w[i]));
   if (wave == 0) {

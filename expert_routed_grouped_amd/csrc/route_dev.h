@@ -277,10 +277,10 @@ __device__ __forceinline__ void route_tokens(const void *__restrict__ x, const v
   }
 }
 
-// Top-k + gates of one token from its logits in LDS (wave-wide; every lane of the
-// wave takes part).  Lanes own experts lane + 64q.
+// Top-k + gates of one token from its logits (wave-wide; every lane of the wave takes part): lane
+// j < k gets the j-th expert and its gate.  Lanes own experts lane + 64q.
 template <int EC>
-__device__ __forceinline__ void topk_token(const float *lgt, int E, int k, int lane, int32_t *ids_t, float *gates_t) {
+__device__ __forceinline__ void topk_lane(const float *lgt, int E, int k, int lane, int &my_e, float &gate) {
   uint64_t key[EC];
 #pragma unroll
   for (int q = 0; q < EC; q++) {
@@ -288,7 +288,7 @@ __device__ __forceinline__ void topk_token(const float *lgt, int E, int k, int l
     key[q] = eq < E ? (((uint64_t)ord_key(lgt[eq]) << 32) | (uint32_t)~(uint32_t)eq) : 0ull;
   }
   float my_v = 0.0f, m = 0.0f;
-  int my_e = 0;
+  my_e = 0;
   for (int j = 0; j < k; j++) {
     uint64_t best = key[0];
 #pragma unroll
@@ -304,9 +304,18 @@ __device__ __forceinline__ void topk_token(const float *lgt, int E, int k, int l
   }
   float u = lane < k ? expf(my_v - m) : 0.0f;
   float sum = wave_sum_f32(u);
+  gate = u / sum;
+}
+
+// The same, written to ids_t[0 .. k) and gates_t[0 .. k).
+template <int EC>
+__device__ __forceinline__ void topk_token(const float *lgt, int E, int k, int lane, int32_t *ids_t, float *gates_t) {
+  int e;
+  float g;
+  topk_lane<EC>(lgt, E, k, lane, e, g);
   if (lane < k) {
-    ids_t[lane] = my_e;
-    gates_t[lane] = u / sum;
+    ids_t[lane] = e;
+    gates_t[lane] = g;
   }
 }
 
