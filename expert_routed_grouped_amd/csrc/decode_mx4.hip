@@ -8,7 +8,7 @@
 // past the routing items waits for that count (for workgroups that drew earlier tickets, so they run; the wait is
 // bounded all the same).  Then every workgroup takes the top k of every token and groups the assignments for
 // itself, in LDS, rather than wait for one that does it and hands it out (a hand-over between workgroups on
-// different XCDs costs about 5 us), the one with the first free ticket writes it down, and all share the gate/up
+// different XCDs costs about 5 us), the one with the first free ticket writes down what launch 2 needs, and all share the gate/up
 // tiles.
 //
 // What bounds it: at one token the chain, H dependent additions whose order is the routing contract (about 3 ns
@@ -38,7 +38,9 @@ struct Params {
   uint32_t *ctl;
   float *logits;       // [T, 64 EC]
   uint8_t *xq, *xs;    // x as MXFP8
-  int32_t *offsets, *row_token;
+  int2 *dtiles;        // the down half's tiles {first row, expert | rows << 16}
+  int *ndtiles;
+  int32_t *row_token;
   float *row_w;
   const uint8_t *wgu, *wgu_s;
   uint8_t *h, *hs;
@@ -151,14 +153,18 @@ constexpr size_t kGroupBytes = kDecodeMx4MaxE * 20 + kMx4StreamMaxT * 32 * 12 + 
 
 // Top k and gates, the grouping and the tile list; ``write``: also to memory.  Returns the number of tiles.
 template <int EC>
-__device__ __forceinline__ int group_all(const Params &p, const Groups &g, bool write, int *s_n) {
+__device__ __forceinline__ int group_all(const Params &p, const Groups &g, bool write, int *s_n, float *scratch) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), N = p.T * p.k;
   for (int e = threadIdx.x; e < p.El; e += NTHR) g.set[e] = 0;
+  // the logits in one go, so that a wave's tokens do not wait for memory one after the other
+  const bool staged = p.T * 64 * EC <= mx4s::RED_FLOATS;
+  if (staged)
+    for (int i = threadIdx.x; i < p.T * 16 * EC; i += NTHR) *((f32x4_t *)scratch + i) = *((const f32x4_t *)p.logits + i);
   __syncthreads();
   for (int t = wave; t < p.T; t += NW) {
     int e;
     float w;
-    rt::topk_lane<EC>(p.logits + (size_t)t * 64 * EC, p.E, p.k, lane, e, w);
+    rt::topk_lane<EC>((staged ? scratch : p.logits) + (size_t)t * 64 * EC, p.E, p.k, lane, e, w);
     if (lane < p.k) {
       if (write) {
         p.ids[(size_t)t * p.k + lane] = e;
@@ -171,14 +177,17 @@ __device__ __forceinline__ int group_all(const Params &p, const Groups &g, bool 
   }
   __syncthreads();
   if (wave == 0) {
-    int n0 = 0, t0 = 0;
+    int n0 = 0, t0 = 0, d0 = 0;
     for (int b = 0; b < p.El; b += 64) {
       const int e = b + lane, cnt = e < p.El ? __popcll(g.set[e]) : 0, t = (cnt + mx4s::TM - 1) / mx4s::TM;
       const int ci = ffn::wave_incl_scan_i(cnt, lane), ti = ffn::wave_incl_scan_i(t, lane);
       const int beg = n0 + ci - cnt;
-      if (e < p.El) {
-        g.first[e] = beg;
-        if (write) p.offsets[e] = beg;
+      if (e < p.El) g.first[e] = beg;
+      if (write) {  // the down half's tiles
+        const int dt = (cnt + mx4s::TD - 1) / mx4s::TD, di = ffn::wave_incl_scan_i(dt, lane);
+        for (int i = 0; i < dt; i++)
+          p.dtiles[d0 + di - dt + i] = make_int2(beg + i * mx4s::TD, e | min(mx4s::TD, cnt - i * mx4s::TD) << 16);
+        d0 += __shfl(di, 63, 64);
       }
       for (int i = 0; i < t; i++)
         g.tiles[t0 + ti - t + i] = make_int2(beg + i * mx4s::TM, e | min(mx4s::TM, cnt - i * mx4s::TM) << 16);
@@ -186,7 +195,7 @@ __device__ __forceinline__ int group_all(const Params &p, const Groups &g, bool 
       t0 += __shfl(ti, 63, 64);
     }
     if (lane == 0) {
-      if (write) p.offsets[p.El] = n0;
+      if (write) *p.ndtiles = d0;
       *s_n = t0;
     }
   }
@@ -238,7 +247,7 @@ __global__ __launch_bounds__(NTHR, 2) void decode_route_gate_up_kernel(Params p)
   __syncthreads();
   const int fid = item - p.n_route;
   const Groups g(p, (char *)(lds + mx4s::RED_FLOATS));
-  const int nt = group_all<EC>(p, g, fid == 0, &s_item);
+  const int nt = group_all<EC>(p, g, fid == 0, &s_item, lds);
   const int ncb = p.I / 32, S = mx4s::split_for(nt * ncb, p.H), per = NW / S, nb = (ncb + per - 1) / per;
   for (int i = fid; i < nt * nb; i += gridDim.x) {
     const int ti = i / nb;
@@ -286,7 +295,7 @@ hipError_t launch(const Params &p, hipStream_t s) {
 
 // Workspace pieces after the control words, each 256-byte aligned.
 struct Layout {
-  size_t logits, xq, xs, offsets, row_token, row_w, h, hs, end;
+  size_t logits, xq, xs, dtiles, ndtiles, row_token, row_w, h, hs, end;
   Layout(int T, int k, int El, int H, int I) {
     const size_t R = (size_t)T * (k < El ? k : El);
     size_t at = kCtlBytes;
@@ -298,7 +307,8 @@ struct Layout {
     logits = take((size_t)T * kDecodeMx4MaxE * 4);
     xq = take((size_t)T * H);
     xs = take((size_t)T * (H / 32));
-    offsets = take((size_t)(El + 1) * 4);
+    dtiles = take((size_t)mx4s::max_tiles(T, El) * sizeof(int2));
+    ndtiles = take(sizeof(int));
     row_token = take(R * 4);
     row_w = take(R * 4);
     h = take(R * I);
@@ -334,7 +344,8 @@ hipError_t launch_decode_layer_mx4(const DecodeMx4Args &a, hipStream_t s) {
   p.logits = (float *)(ws + l.logits);
   p.xq = (uint8_t *)(ws + l.xq);
   p.xs = (uint8_t *)(ws + l.xs);
-  p.offsets = (int32_t *)(ws + l.offsets);
+  p.dtiles = (int2 *)(ws + l.dtiles);
+  p.ndtiles = (int *)(ws + l.ndtiles);
   p.row_token = (int32_t *)(ws + l.row_token);
   p.row_w = (float *)(ws + l.row_w);
   p.wgu = a.wgu;
@@ -344,7 +355,8 @@ hipError_t launch_decode_layer_mx4(const DecodeMx4Args &a, hipStream_t s) {
   const hipError_t err = EC == 1 ? launch<1>(p, s) : EC == 2 ? launch<2>(p, s) : launch<4>(p, s);
   if (err != hipSuccess) return err;
   FfnMx4Args d{};
-  d.offsets = p.offsets;
+  d.tiles = p.dtiles;
+  d.ntiles = p.ndtiles;
   d.row_token = p.row_token;
   d.row_w = p.row_w;
   d.El = a.El;

@@ -46,7 +46,8 @@ hipError_t launch(const FfnMx4Args &a, uint8_t *h, uint8_t *hs, hipStream_t s) {
 
 template <int FA, bool BF16>
 hipError_t launch_down(const FfnMx4Args &a, const uint8_t *h, const uint8_t *hs, hipStream_t s) {
-  mx4s::DownArgs d{a.offsets, a.row_token, a.row_w, a.El, a.T, a.R_cap, a.H, a.I, {h, hs, a.wd, a.wd_s}, a.y, a.zero, a.n_zero};
+  mx4s::DownArgs d{a.offsets, a.row_token, a.row_w, a.El, a.T, a.R_cap, a.H, a.I, {h, hs, a.wd, a.wd_s}, a.y, a.tiles, a.ntiles,
+                   a.zero, a.n_zero};
   hipLaunchKernelGGL((mx4s::down_sum_kernel<FA, BF16>), dim3(a.H / 16), dim3(mx4s::NTHR),
                      mx4s::down_lds_bytes<FA>(a.T, a.El, a.R_cap), s, d);
   return hipGetLastError();

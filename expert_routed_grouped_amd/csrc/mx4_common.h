@@ -182,7 +182,10 @@ struct FfnMx4Args {
   void *y;                     // [T, H], overwritten
   int y_bf16;
   void *ws;
-  uint32_t *zero;              // launch_down_sum_mx4 only: n_zero words that it zeroes, or NULL
+  // launch_down_sum_mx4 only
+  const int2 *tiles;           // its tiles {first row, expert | rows << 16}, or NULL: found from the offsets
+  const int *ntiles;
+  uint32_t *zero;              // n_zero words that it zeroes, or NULL
   int n_zero;
 };
 size_t ffn_mx4_ws_bytes(int T, int R_cap, int El, int H, int I, int y_bf16);

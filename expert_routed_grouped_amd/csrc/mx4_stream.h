@@ -140,6 +140,8 @@ struct DownArgs {
   int El, T, R_cap, H, I;
   Half p;                  // h rows and the down weights
   void *y;                 // [T, H], overwritten
+  const int2 *tiles;       // its tiles {first row, expert | rows << 16}, or NULL: found from the offsets
+  const int *ntiles;
   uint32_t *zero;          // n_zero words to zero for the next call, or NULL
   int n_zero;
 };
@@ -169,7 +171,11 @@ __global__ __launch_bounds__(NTHR) void down_sum_kernel(DownArgs a) {
   if (blockIdx.x == 0 && (int)threadIdx.x < a.n_zero) a.zero[threadIdx.x] = 0;
   for (int i = lane; i < a.T * 4; i += 64) *(f32x4_t *)(tot + 4 * i) = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int i = threadIdx.x; i < a.R_cap; i += NTHR) rowinfo[i] = make_int2(a.row_token[i], __float_as_int(a.row_w[i]));
-  if (wave == 0) {
+  if (a.tiles) {
+    const int nt = min(*a.ntiles, cap);
+    for (int i = threadIdx.x; i < nt; i += NTHR) tiles[i] = a.tiles[i];
+    if (threadIdx.x == 0) s_tiles = nt;
+  } else if (wave == 0) {
     int n0 = 0;
     for (int b = 0; b < a.El; b += 64) {
       const int e = b + lane;
