@@ -7,7 +7,6 @@ raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -427,40 +426,69 @@ def decode_layer_error_word(workspace: torch.Tensor) -> int:
 
 
 # ---- MXFP4 (include/moe.h, the *_mx4 calls) ----
-# The C ABI cannot see buffer sizes, so the shapes, types and devices of every tensor are checked here.
-def _need(t: torch.Tensor, name: str, dtype, shape, device):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+# The C ABI cannot see buffer sizes, so the shape, type and device of every tensor are checked here.  A call is short
+# next to what Python adds to it: one pass over each argument, raw addresses and streams.
+def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, device):
+    """Address of a contiguous GPU tensor of this type, shape and device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _on(t: torch.Tensor):
-    """The device of a GPU tensor as the current one, so that the call runs there on its current stream."""
-    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+class _On:
+    """``device`` as the current one (if it is not), so that a call runs there, on its current stream."""
+
+    def __init__(self, device: torch.device):
+        if device.type != "cuda":
+            raise ValueError("tensors passed to the MoE library must be on the GPU")
+        self.index = device.index
+        self.other = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.other = torch.cuda.device(self.index)
+            self.other.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
+
+    def stream(self, stream) -> int:
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.index)
+        if getattr(stream, "device", None) not in (None, torch.device("cuda", self.index)):
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{self.index}")
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _out_dtype(dtype) -> int:
-    if dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported output dtype {dtype}")
-    return MOE_F32 if dtype == torch.float32 else MOE_BF16
+    if dtype == torch.bfloat16:
+        return MOE_BF16
+    if dtype == torch.float32:
+        return MOE_F32
+    raise TypeError(f"unsupported output dtype {dtype}")
 
 
 def moe_quantize_mx4(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                      stream=None):
     """MXFP4 quantisation of a [rows, K] fp32/bf16 tensor -> (codes uint8 [rows, K/2], scales uint8 [rows, K/32])."""
     rows, K = x.shape
-    if x.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    with _on(x):
-        if codes is None:
-            codes = torch.empty((rows, K // 2), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
-        _need(codes, "codes", torch.uint8, (rows, K // 2), x.device)
-        _need(scales, "scales", torch.uint8, (rows, K // 32), x.device)
-        _check("moe_quantize_mx4", lib().moe_quantize_mx4(_ptr(x), _dtype(x), rows, K, _ptr(codes), _ptr(scales),
-                                                          _stream(stream)))
+    dt, dev, u8 = _out_dtype(x.dtype), x.device, torch.uint8
+    if codes is None:
+        codes = torch.empty((rows, K // 2), dtype=u8, device=dev)
+    if scales is None:
+        scales = torch.empty((rows, K // 32), dtype=u8, device=dev)
+    args = (_arg(x, "x", x.dtype, (rows, K), dev), dt, rows, K, _arg(codes, "codes", u8, (rows, K // 2), dev),
+            _arg(scales, "scales", u8, (rows, K // 32), dev))
+    with _On(dev) as on:
+        _check("moe_quantize_mx4", lib().moe_quantize_mx4(*args, on.stream(stream)))
     return codes, scales
 
 
@@ -468,19 +496,18 @@ def moe_dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, out: Optional[t
                       dtype=torch.float32, stream=None) -> torch.Tensor:
     """The values of MXFP4 codes [rows, K/2] or MXFP8 codes [rows, K] with scales [rows, K/32] (which of the two
     follows from the widths) -> [rows, K] of ``dtype`` (fp32 or bf16)."""
-    rows, K = codes.shape[0], scales.shape[1] * 32
+    rows, K, dev, u8 = codes.shape[0], scales.shape[1] * 32, codes.device, torch.uint8
     if codes.shape[1] not in (K, K // 2):
         raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} are no MXFP4 or MXFP8 pair")
     fp4 = codes.shape[1] == K // 2
-    with _on(codes):
-        if out is None:
-            out = torch.empty((rows, K), dtype=dtype, device=codes.device)
-        odt = _out_dtype(out.dtype)
-        _need(codes, "codes", torch.uint8, (rows, K // 2 if fp4 else K), codes.device)
-        _need(scales, "scales", torch.uint8, (rows, K // 32), codes.device)
-        _need(out, "out", out.dtype, (rows, K), codes.device)
-        _check("moe_dequantize_mx", lib().moe_dequantize_mx(_ptr(codes), _ptr(scales), MOE_MXFP4 if fp4 else MOE_MXFP8,
-                                                            rows, K, _ptr(out), odt, _stream(stream)))
+    if out is None:
+        _out_dtype(dtype)
+        out = torch.empty((rows, K), dtype=dtype, device=dev)
+    args = (_arg(codes, "codes", u8, (rows, K // 2 if fp4 else K), dev),
+            _arg(scales, "scales", u8, (rows, K // 32), dev), MOE_MXFP4 if fp4 else MOE_MXFP8, rows, K,
+            _arg(out, "out", out.dtype, (rows, K), dev), _out_dtype(out.dtype))
+    with _On(dev) as on:
+        _check("moe_dequantize_mx", lib().moe_dequantize_mx(*args, on.stream(stream)))
     return out
 
 
@@ -489,32 +516,31 @@ def moe_pack_mx4(codes: torch.Tensor, scales: torch.Tensor, stream=None):
     (codes uint8 [E, N/16, K/128, 1024], scales uint8 [E, N/16, ceil(K/512), 256]); without E for 2-D weights."""
     if codes.dim() not in (2, 3) or scales.dim() != codes.dim():
         raise ValueError("codes and scales must both be [E, N, ...] or [N, ...]")
-    lead, N, K = codes.shape[:-2], codes.shape[-2], codes.shape[-1] * 2
-    _need(codes, "codes", torch.uint8, (*lead, N, K // 2), codes.device)
-    _need(scales, "scales", torch.uint8, (*lead, N, K // 32), codes.device)
+    lead, N, K, dev, u8 = codes.shape[:-2], codes.shape[-2], codes.shape[-1] * 2, codes.device, torch.uint8
+    pcodes, pscales = (_arg(codes, "codes", u8, (*lead, N, K // 2), dev),
+                       _arg(scales, "scales", u8, (*lead, N, K // 32), dev))
     if N % 16 != 0 or K % 128 != 0:
         raise MoEError("moe_pack_mx4", -2, "N must be a multiple of 16 and K of 128")
-    with _on(codes):
-        pc = torch.empty((*lead, N // 16, K // 128, 1024), dtype=torch.uint8, device=codes.device)
-        ps = torch.empty((*lead, N // 16, (K + 511) // 512, 256), dtype=torch.uint8, device=codes.device)
-        rows = (lead[0] if lead else 1) * N
-        _check("moe_pack_mx4", lib().moe_pack_mx4(_ptr(codes), _ptr(scales), rows, K, _ptr(pc), _ptr(ps),
-                                                  _stream(stream)))
+    pc = torch.empty((*lead, N // 16, K // 128, 1024), dtype=u8, device=dev)
+    ps = torch.empty((*lead, N // 16, (K + 511) // 512, 256), dtype=u8, device=dev)
+    with _On(dev) as on:
+        _check("moe_pack_mx4", lib().moe_pack_mx4(pcodes, pscales, (lead[0] if lead else 1) * N, K, pc.data_ptr(),
+                                                  ps.data_ptr(), on.stream(stream)))
     return pc, ps
 
 
-def _mx4_weights(wgu, wd):
-    """Sizes (E_loc, H, I) of packed gate/up and down weights, each a (codes, scales) pair of moe_pack_mx4."""
+def _mx4_weights(wgu, wd, dev):
+    """Sizes (E_loc, H, I) and addresses of packed gate/up and down weights, each a (codes, scales) pair of
+    moe_pack_mx4."""
     (gc, gs), (dc, ds) = wgu, wd
     if gc.dim() != 4 or dc.dim() != 4 or gc.shape[1] % 2 != 0:
         raise ValueError("weights must be the (codes, scales) pairs of moe_pack_mx4, with experts in front")
-    El, H, I = gc.shape[0], gc.shape[2] * 128, gc.shape[1] * 8
-    dev = gc.device
-    _need(gc, "w_gate_up codes", torch.uint8, (El, 2 * I // 16, H // 128, 1024), dev)
-    _need(gs, "w_gate_up scales", torch.uint8, (El, 2 * I // 16, (H + 511) // 512, 256), dev)
-    _need(dc, "w_down codes", torch.uint8, (El, H // 16, I // 128, 1024), dev)
-    _need(ds, "w_down scales", torch.uint8, (El, H // 16, (I + 511) // 512, 256), dev)
-    return El, H, I
+    El, gI, hb, _ = gc.shape
+    H, I, u8 = hb * 128, gI * 8, torch.uint8
+    return El, H, I, (_arg(gc, "w_gate_up codes", u8, (El, gI, hb, 1024), dev),
+                      _arg(gs, "w_gate_up scales", u8, (El, gI, (H + 511) // 512, 256), dev),
+                      _arg(dc, "w_down codes", u8, (El, H // 16, I // 128, 1024), dev),
+                      _arg(ds, "w_down scales", u8, (El, H // 16, (I + 511) // 512, 256), dev))
 
 
 def moe_ffn_mx4_workspace_size(T: int, k: int, E_loc: int, H: int, I: int, y_dtype: int = MOE_F32) -> int:
@@ -534,32 +560,25 @@ def moe_grouped_ffn_mx4(a_codes: torch.Tensor, a_scales: torch.Tensor, offsets: 
     """SwiGLU expert FFN with MXFP4 weights and the gate-weighted sum to token order -> y [T, H] of ``dtype``
     (overwritten).  Activations MXFP8 or MXFP4 (from the width of ``a_codes``); ``wgu`` and ``wd`` are the
     (codes, scales) pairs of moe_pack_mx4; the maps are those of moe_permute."""
-    El, H, I = _mx4_weights(wgu, wd)
+    dev, u8, i32 = a_codes.device, torch.uint8, torch.int32
+    El, H, I, w = _mx4_weights(wgu, wd, dev)
     T, k = token_row.shape
-    dev = a_codes.device
     fp4 = a_codes.shape[1] == H // 2
     if row_token.numel() < T * min(k, El) or row_w.numel() < T * min(k, El):
         raise ValueError(f"row_token and row_w must hold T * min(k, E_loc) = {T * min(k, El)} entries")
-    with _on(a_codes):
-        if y is None:
-            y = torch.empty((T, H), dtype=dtype, device=dev)
-        ydt = _out_dtype(y.dtype)
-        _need(a_codes, "a_codes", torch.uint8, (T, H // 2 if fp4 else H), dev)
-        _need(a_scales, "a_scales", torch.uint8, (T, H // 32), dev)
-        _need(offsets, "offsets", torch.int32, (El + 1,), dev)
-        _need(row_token, "row_token", torch.int32, row_token.shape, dev)
-        _need(row_w, "row_w", torch.float32, row_w.shape, dev)
-        _need(token_row, "token_row", torch.int32, (T, k), dev)
-        _need(wgu[0], "w_gate_up codes", torch.uint8, wgu[0].shape, dev)
-        _need(y, "y", y.dtype, (T, H), dev)
-        if workspace is None:
-            workspace = torch.empty(moe_ffn_mx4_workspace_size(T, k, El, H, I, ydt), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev:
-            raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
-        _check("moe_grouped_ffn_mx4", lib().moe_grouped_ffn_mx4(
-            _ptr(a_codes), _ptr(a_scales), MOE_MXFP4 if fp4 else MOE_MXFP8, _ptr(offsets), _ptr(row_token),
-            _ptr(row_w), _ptr(token_row), El, T, k, H, I, _ptr(wgu[0]), _ptr(wgu[1]), _ptr(wd[0]), _ptr(wd[1]),
-            _ptr(y), ydt, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    if y is None:
+        _out_dtype(dtype)
+        y = torch.empty((T, H), dtype=dtype, device=dev)
+    ydt = _out_dtype(y.dtype)
+    if workspace is None:
+        workspace = torch.empty(moe_ffn_mx4_workspace_size(T, k, El, H, I, ydt), dtype=u8, device=dev)
+    args = (_arg(a_codes, "a_codes", u8, (T, H // 2 if fp4 else H), dev), _arg(a_scales, "a_scales", u8, (T, H // 32), dev),
+            MOE_MXFP4 if fp4 else MOE_MXFP8, _arg(offsets, "offsets", i32, (El + 1,), dev),
+            _arg(row_token, "row_token", i32, row_token.shape, dev), _arg(row_w, "row_w", torch.float32, row_w.shape, dev),
+            _arg(token_row, "token_row", i32, (T, k), dev), El, T, k, H, I, *w, _arg(y, "y", y.dtype, (T, H), dev), ydt,
+            _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.nbytes)
+    with _On(dev) as on:
+        _check("moe_grouped_ffn_mx4", lib().moe_grouped_ffn_mx4(*args, on.stream(stream)))
     return y
 
 
@@ -577,32 +596,26 @@ def moe_decode_layer_mx4(x: torch.Tensor, w_router_packed: torch.Tensor, bias: O
     ``w_router_packed`` is the fp32 [H/4, E, 4] tensor of moe_pack_router, ``wgu`` and ``wd`` the (codes, scales)
     pairs of moe_pack_mx4 for the experts [e_begin, e_end), ``workspace`` starts zeroed
     (moe_decode_layer_mx4_workspace; decode_layer_error_word reads its diagnostic)."""
-    El, H, I = _mx4_weights(wgu, wd)
-    T, dev = x.shape[0], x.device
+    dev, f32 = x.device, torch.float32
+    El, H, I, w = _mx4_weights(wgu, wd, dev)
+    T = x.shape[0]
     if w_router_packed.dim() != 3:
         raise ValueError("w_router_packed must be the [H/4, E, 4] tensor of moe_pack_router")
     E = w_router_packed.shape[1]
     if El != e_end - e_begin:
         raise ValueError(f"weights hold {El} experts, [{e_begin}, {e_end}) has {e_end - e_begin}")
-    with _on(x):
-        if topk_ids is None:
-            topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-        if topk_w is None:
-            topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
-        if y is None:
-            y = torch.empty((T, H), dtype=dtype, device=dev)
-        ydt = _out_dtype(y.dtype)
-        _need(x, "x", torch.bfloat16, (T, H), dev)
-        _need(w_router_packed, "w_router_packed", torch.float32, (H // 4, E, 4), dev)
-        if bias is not None:
-            _need(bias, "bias", torch.float32, (E,), dev)
-        _need(topk_ids, "topk_ids", torch.int32, (T, k), dev)
-        _need(topk_w, "topk_w", torch.float32, (T, k), dev)
-        _need(wgu[0], "w_gate_up codes", torch.uint8, wgu[0].shape, dev)
-        _need(y, "y", y.dtype, (T, H), dev)
-        _need(workspace, "workspace", torch.uint8, workspace.shape, dev)
-        _check("moe_decode_layer_mx4", lib().moe_decode_layer_mx4(
-            _ptr(x), _ptr(w_router_packed), _ptr(bias), T, H, E, k, e_begin, e_end, I, _ptr(wgu[0]), _ptr(wgu[1]),
-            _ptr(wd[0]), _ptr(wd[1]), _ptr(topk_ids), _ptr(topk_w), _ptr(y), ydt, _ptr(workspace), workspace.numel(),
-            _stream(stream)))
+    if topk_ids is None:
+        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if topk_w is None:
+        topk_w = torch.empty((T, k), dtype=f32, device=dev)
+    if y is None:
+        _out_dtype(dtype)
+        y = torch.empty((T, H), dtype=dtype, device=dev)
+    args = (_arg(x, "x", torch.bfloat16, (T, H), dev), _arg(w_router_packed, "w_router_packed", f32, (H // 4, E, 4), dev),
+            _arg(bias, "bias", f32, (E,), dev), T, H, E, k, e_begin, e_end, I, *w,
+            _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev), _arg(topk_w, "topk_w", f32, (T, k), dev),
+            _arg(y, "y", y.dtype, (T, H), dev), _out_dtype(y.dtype),
+            _arg(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.nbytes)
+    with _On(dev) as on:
+        _check("moe_decode_layer_mx4", lib().moe_decode_layer_mx4(*args, on.stream(stream)))
     return y, topk_ids, topk_w
