@@ -124,9 +124,89 @@ class LayerBuffers:
             self.side = (torch.cuda.Stream(device=device), torch.cuda.Event())
 
 
-def run_layer(dev: dict, bufs: LayerBuffers, stream=None) -> torch.Tensor:
+def convert_experts_mx4(dev: dict) -> dict:
+    """Add the routed experts of ``dev`` (bf16 or fp32 weights, row-major) in MXFP4, quantised and packed, as
+    ``dev["wgu_mx4"]`` and ``dev["wd_mx4"]``, and the packed router weight; run_layer with Mx4LayerBuffers reads
+    those.  Done once, like loading the weights; the originals may be dropped afterwards."""
+    if dev.get("packed"):
+        raise ValueError("convert the row-major weights, before pack_weights")
+    for src, dst in (("w_gate_up", "wgu_mx4"), ("w_down", "wd_mx4")):
+        w = dev[src]
+        if w.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{src} must be bf16 or fp32, got {w.dtype}")
+        El, N, K = w.shape
+        codes, scales = moe.moe_quantize_mx4(w.reshape(El * N, K))
+        dev[dst] = moe.moe_pack_mx4(codes.view(El, N, K // 2), scales.view(El, N, K // 32))
+    return pack_router(dev)
+
+
+class Mx4LayerBuffers:
+    """Device buffers of one layer shape with MXFP4 experts (convert_experts_mx4), reused across calls.
+
+    ``act``: format of the activations and the intermediate, "mxfp8" or "mxfp4"; ``dtype``: of y.  Up to 64
+    tokens with MXFP8 activations take the two-launch layer (moe_decode_layer_mx4), everything else the
+    separate calls.  A shared expert adds into y in fp32, so it needs ``dtype`` torch.float32."""
+
+    def __init__(self, cfg, device="cuda", act: str = "mxfp8", dtype=torch.bfloat16):
+        if act not in ("mxfp8", "mxfp4"):
+            raise ValueError(f"act must be mxfp8 or mxfp4, got {act}")
+        if cfg.I_s > 0 and dtype != torch.float32:
+            raise ValueError("a shared expert needs an fp32 y")
+        T, k, El, H, I = cfg.T, cfg.k, cfg.E_loc, cfg.H, cfg.I
+        d = dict(device=device)
+        self.cfg, self.act = cfg, act
+        self.topk_ids = torch.empty((T, k), dtype=torch.int32, **d)
+        self.topk_w = torch.empty((T, k), dtype=torch.float32, **d)
+        self.y = torch.empty((T, H), dtype=dtype, **d)
+        self.one_call = act == "mxfp8" and cfg.act == "bf16" and T <= 64 and cfg.E <= 256 and H <= 8192
+        if self.one_call:
+            self.workspace = moe.moe_decode_layer_mx4_workspace(T, k, El, H, I, device)
+        else:
+            R_cap = max(T * min(k, El), 1)
+            self.workspace = moe.moe_ffn_mx4_workspace(T, k, El, H, I, dtype, device)
+            self.perm = dict(counts=torch.empty(El, dtype=torch.int32, **d),
+                             offsets=torch.empty(El + 1, dtype=torch.int32, **d),
+                             row_token=torch.empty(R_cap, dtype=torch.int32, **d),
+                             row_w=torch.empty(R_cap, dtype=torch.float32, **d),
+                             token_row=torch.empty((T, k), dtype=torch.int32, **d),
+                             workspace=torch.empty(max(moe.moe_permute_workspace_size(T, k, El), 256),
+                                                   dtype=torch.uint8, **d))
+            self.codes = torch.empty((T, H if act == "mxfp8" else H // 2), dtype=torch.uint8, **d)
+            self.scales = torch.empty((T, H // 32), dtype=torch.uint8, **d)
+        self.shared_ws = None
+        if cfg.I_s > 0:
+            adt = moe.MOE_F32 if cfg.act == "f32" else moe.MOE_BF16
+            self.shared_ws = torch.empty(moe.moe_shared_workspace_size(T, cfg.I_s, adt), dtype=torch.uint8, **d)
+
+
+def _run_layer_mx4(dev: dict, bufs: Mx4LayerBuffers, stream) -> torch.Tensor:
+    cfg = bufs.cfg
+    if bufs.one_call:
+        wp = dev.get("w_router_packed")
+        if wp is None or not _router_pack_current(dev):
+            wp = pack_router(dev)["w_router_packed"]
+        moe.moe_decode_layer_mx4(dev["x"], wp, dev["bias"], cfg.k, cfg.lo, cfg.hi, dev["wgu_mx4"], dev["wd_mx4"],
+                                 bufs.workspace, bufs.topk_ids, bufs.topk_w, bufs.y, stream=stream)
+    else:
+        p = bufs.perm
+        moe.moe_route(dev["x"], dev["w_router"], dev["bias"], cfg.k, bufs.topk_ids, bufs.topk_w, stream=stream)
+        moe.moe_permute(bufs.topk_ids, bufs.topk_w, cfg.E, cfg.lo, cfg.hi, out=p, stream=stream)
+        quantize = moe.moe_quantize_mx if bufs.act == "mxfp8" else moe.moe_quantize_mx4
+        quantize(dev["x"], bufs.codes, bufs.scales, stream=stream)
+        moe.moe_grouped_ffn_mx4(bufs.codes, bufs.scales, p["offsets"], p["row_token"], p["row_w"], p["token_row"],
+                                dev["wgu_mx4"], dev["wd_mx4"], y=bufs.y, workspace=bufs.workspace, stream=stream)
+    if bufs.shared_ws is not None:
+        moe.moe_shared_expert(dev["x"], dev["ws_gate_up"], dev["ws_down"], bufs.y, dev.get("ss_gate_up"),
+                              dev.get("ss_down"), workspace=bufs.shared_ws, stream=stream)
+    return bufs.y
+
+
+def run_layer(dev: dict, bufs, stream=None) -> torch.Tensor:
     """route -> permute -> grouped FFN (-> combine) (-> shared expert), or for decode-sized batches
-    moe_decode_layer (-> shared expert).  Returns y [T,H] fp32."""
+    moe_decode_layer (-> shared expert).  Returns y [T,H] fp32.  With Mx4LayerBuffers the experts are those of
+    convert_experts_mx4 and y has the buffers' type."""
+    if isinstance(bufs, Mx4LayerBuffers):
+        return _run_layer_mx4(dev, bufs, stream)
     cfg = bufs.cfg
     p = bufs.perm
     packed = bool(dev.get("packed", False))

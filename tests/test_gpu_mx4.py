@@ -450,3 +450,60 @@ def test_decode_layer_graph_streams_and_empty():
     assert torch.equal(a[0], want[0]) and torch.equal(b[0], want[0])
     s["x"] = s["x"][:0]
     assert run_layer(s, k, 0, E, ws)[0].shape == (0, H)
+
+
+# ------------------------------------------------------------------ together, as a layer
+@pytest.mark.parametrize("T,act,wact", [(9, "mxfp8", "bf16"), (9, "mxfp4", "bf16"), (150, "mxfp8", "bf16"),
+                                        (150, "mxfp4", "f32")])
+@pytest.mark.parametrize("I_s", [0, 192])
+def test_layer(T, act, wact, I_s):
+    """convert_experts_mx4 and run_layer on a synthetic layer (an expert-parallel share, with and without a shared
+    expert), called twice, against 64 bits."""
+    from expert_routed_grouped_amd import layer as L
+    from expert_routed_grouped_amd import synth
+    cfg = synth.LayerConfig("mx4", T=T, H=512, E=24, k=4, I=256, act=wact, wdt=wact, e_begin=4, e_end=20, seed=77, w_std=0.06,
+                            I_s=I_s)
+    dev = L.to_device(synth.make_inputs(cfg))
+    if act == "mxfp8":  # activations whose sums are exact on the matrix cores
+        dev["x"] = R.even_rows((T, 512), gen(T), DEV).to(dev["x"].dtype)
+    L.convert_experts_mx4(dev)
+    bufs = L.Mx4LayerBuffers(cfg, act=act, dtype=torch.float32 if I_s else torch.bfloat16)
+    L.run_layer(dev, bufs)
+    first = bufs.y.clone()
+    y = L.run_layer(dev, bufs)
+    ids, w = moe.moe_route(dev["x"], dev["w_router"], None, 4)
+    assert torch.equal(ids, bufs.topk_ids)
+    xv, _ = R.quantize(dev["x"], act)
+    q = {n: R.quantize(dev[n], "mxfp4")[0] for n in ("w_gate_up", "w_down")}
+    mid, rad = R.layer(xv, ids, w, 4, 16, lambda e: q["w_gate_up"][e], lambda e: q["w_down"][e], act, y.dtype,
+                       rows_rounded=True)
+    if I_s:
+        # the shared expert: fp32 or bf16 products (exact for bf16, one rounding each for fp32) with fp32 sums in
+        # some order, h rounded to bf16 for bf16 models
+        x, gu, dn = dev["x"].double(), dev["ws_gate_up"].double(), dev["ws_down"].double()
+        a = x @ gu.T
+        mag = x.abs() @ gu.abs().T
+        G, U = a[:, :I_s], a[:, I_s:]
+        n = 2 * 512 * 2.0 ** -24
+        h = G * torch.sigmoid(G) * U
+        dh = U.abs() * 1.1 * n * mag[:, :I_s] + (G * torch.sigmoid(G)).abs() * n * mag[:, I_s:]
+        dh = dh + h.abs() * ((G.abs() + 5) * 2.0 ** -22 + (2.0 ** -8 if wact == "bf16" else 0))
+        mid = mid + h @ dn.T
+        rad = rad + dh @ dn.abs().T + 2 * I_s * 2.0 ** -24 * (h.abs() @ dn.abs().T) + (mid.abs() + rad) * 2.0 ** -22
+    else:
+        assert torch.equal(first, y)  # the shared expert's split sums are in no fixed order
+    R.check_interval(y, mid, rad, f"layer T={T} {act}")
+
+
+def test_layer_refusals():
+    from expert_routed_grouped_amd import layer as L
+    from expert_routed_grouped_amd import synth
+    cfg = synth.LayerConfig("mx4", T=4, H=256, E=4, k=2, I=128, seed=78, I_s=128)
+    with pytest.raises(ValueError):
+        L.Mx4LayerBuffers(cfg)  # a shared expert with a bf16 y
+    with pytest.raises(ValueError):
+        L.Mx4LayerBuffers(cfg.replace(I_s=0), act="bf16")
+    dev = L.to_device(synth.make_inputs(cfg.replace(I_s=0)))
+    L.pack_weights(dev)
+    with pytest.raises(ValueError):
+        L.convert_experts_mx4(dev)
