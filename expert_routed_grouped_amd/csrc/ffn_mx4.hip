@@ -299,54 +299,62 @@ __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
 }
 
-// The tile list: expert by expert, then N tile by N tile, then M tile by M tile.  One workgroup; smem: El + 1 ints.
+// The tile list: expert by expert, then N tile by N tile, then M tile by M tile.  Workgroup ``part`` of ``parts``
+// writes its share; each counts the M tiles of all experts for itself (a hand-over costs more than El loads do).  One
+// workgroup writing all of it, a wave an expert, took 27 us.  smem: El + 1 ints, the first M tile of each expert.
 template <int BM>
-__device__ void list_tiles(const TileParams &p, int NT, int cap, int4 *out, int *count, int *smem) {
+__device__ void list_tiles(const TileParams &p, int NT, int cap, int part, int parts, int4 *out, int *count, int *smem) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto rows_of = [&](int e) { return e < p.El ? min(p.offsets[e + 1], p.R_cap) - max(p.offsets[e], 0) : 0; };
+  auto rows_of = [&](int e) { return min(p.offsets[e + 1], p.R_cap) - max(p.offsets[e], 0); };
+  for (int e = threadIdx.x; e < p.El; e += blockDim.x) {
+    const int c = rows_of(e);
+    smem[e] = c > 0 ? (c + BM - 1) / BM : 0;
+  }
+  __syncthreads();
   if (wave == 0) {
     int n0 = 0;
     for (int b = 0; b < p.El; b += 64) {
-      const int c = rows_of(b + lane), t = c > 0 ? (c + BM - 1) / BM : 0;
+      const int t = b + lane < p.El ? smem[b + lane] : 0;
       const int incl = ffn::wave_incl_scan_i(t, lane);
       if (b + lane < p.El) smem[b + lane] = n0 + incl - t;
       n0 += __shfl(incl, 63, 64);
     }
-    if (lane == 0) {
-      smem[p.El] = n0;
-      *count = min(n0 * NT, cap);
-    }
+    if (lane == 0) smem[p.El] = n0;
   }
   __syncthreads();
-  for (int e = wave; e < p.El; e += blockDim.x >> 6) {
-    const int c = rows_of(e), m = smem[e + 1] - smem[e], base = smem[e] * NT;
-    if (m == 0) continue;
+  const int n = (int)min((long long)smem[p.El] * NT, (long long)cap);
+  if (part == 0 && threadIdx.x == 0) *count = n;
+  for (int i = part * blockDim.x + threadIdx.x; i < n; i += parts * blockDim.x) {
+    int e = 0;  // the last expert whose tiles start at or before i (an expert without tiles starts where the next does)
+    for (int hi = p.El; hi - e > 1;) {
+      const int mid = (e + hi) >> 1;
+      if (smem[mid] * NT <= i) e = mid;
+      else hi = mid;
+    }
+    const int c = rows_of(e), m = smem[e + 1] - smem[e], j = i - smem[e] * NT, nt = j / m, mt = j - nt * m;
     const int trows = min(BM, ((c + m - 1) / m + 31) & ~31);  // m * trows >= c; a last tile may have no rows left
-    for (int i = lane; i < m * NT; i += 64) {
-      const int nt = i / m, mt = i - nt * m;
-      const int rows = max(min(trows, c - mt * trows), 0);
-      if (base + i < cap) out[base + i] = make_int4(e, nt, max(p.offsets[e], 0) + mt * trows, rows | (trows / 2) << 16);
-    }
+    const int rows = max(min(trows, c - mt * trows), 0);
+    out[i] = make_int4(e, nt, max(p.offsets[e], 0) + mt * trows, rows | (trows / 2) << 16);
   }
-  __syncthreads();
 }
 
-// What the tile kernels need first.  Workgroup 0: the tile lists of both halves.  The others: activation scales
-// [T, K/32] into lane order: dword q of piece c of a row has the scales 16c + 4j + q, j = 0 .. 3 (0 past the end of
-// the row).
+// What the tile kernels need first.  The first 2 ``parts`` workgroups: the tile lists of both halves.  The others:
+// activation scales [T, K/32] into lane order: dword q of piece c of a row has the scales 16c + 4j + q, j = 0 .. 3 (0
+// past the end of the row).
 template <int BM>
-__global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int cap, int4 *gtiles, int4 *dtiles, int *counts,
-                                                      const uint8_t *__restrict__ s, uint32_t *__restrict__ out) {
-  if (blockIdx.x == 0) {
+__global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int parts, int gcap, int dcap, int4 *gtiles,
+                                                      int4 *dtiles, int *counts, const uint8_t *__restrict__ s,
+                                                      uint32_t *__restrict__ out) {
+  if ((int)blockIdx.x < 2 * parts) {
     __shared__ int smem[1024 + 1];
-    list_tiles<BM>(p, p.I / 128, cap * (p.I / 128), gtiles, counts, smem);
-    const int nt = (p.H + BN - 1) / BN;
-    list_tiles<BM>(p, nt, cap * nt, dtiles, counts + 1, smem);
+    const int part = blockIdx.x >> 1;
+    if (blockIdx.x & 1) list_tiles<BM>(p, (p.H + BN - 1) / BN, dcap, part, parts, dtiles, counts + 1, smem);
+    else list_tiles<BM>(p, p.I / 128, gcap, part, parts, gtiles, counts, smem);
     return;
   }
-  const int K = p.H, kb = K / 32, dw = (K + 511) / 512 * 4;
-  const long long total = (long long)p.T * dw, stride = (long long)(gridDim.x - 1) * blockDim.x;
-  for (long long i = (long long)(blockIdx.x - 1) * blockDim.x + threadIdx.x; i < total; i += stride) {
+  const int K = p.H, kb = K / 32, dw = (K + 511) / 512 * 4, b0 = blockIdx.x - 2 * parts;
+  const long long total = (long long)p.T * dw, stride = (long long)(gridDim.x - 2 * parts) * blockDim.x;
+  for (long long i = (long long)b0 * blockDim.x + threadIdx.x; i < total; i += stride) {
     const long long t = i / dw;
     const int d = (int)(i - t * dw), c = d >> 2, q = d & 3;
     uint32_t w = 0;
@@ -359,26 +367,50 @@ __global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int cap, int
   }
 }
 
-// y[t] = sum of t's rows in slot order; a slot without a row (or with one out of range) adds nothing.
+// y[t] = sum of t's rows in slot order; a slot without a row (or with one out of range) adds nothing.  A thread sums
+// eight columns, the loads of eight slots in flight.
+constexpr int SUM_THR = 256, SUM_COLS = 8;
 template <bool BF16>
-__global__ __launch_bounds__(256) void sum_rows_kernel(const void *__restrict__ rows, const int32_t *__restrict__ token_row,
-                                                       int T, int k, int R_cap, int H, void *__restrict__ y) {
+__global__ __launch_bounds__(SUM_THR) void sum_rows_kernel(const void *__restrict__ rows,
+                                                           const int32_t *__restrict__ token_row, int T, int k,
+                                                           int R_cap, int H, void *__restrict__ y) {
+  const int c = (blockIdx.y * SUM_THR + threadIdx.x) * SUM_COLS;
+  if (c >= H) return;  // H is a multiple of 128
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    for (int c = threadIdx.x * 4; c < H; c += blockDim.x * 4) {
-      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-      for (int j = 0; j < k; j++) {
-        const int r = token_row[(size_t)t * k + j];
-        if ((unsigned)r >= (unsigned)R_cap) continue;
-        const size_t i = (size_t)r * H + c;
+    f32x4_t lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      u32x4_t v[8][BF16 ? 1 : 2];
+      int r[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        r[j] = j0 + j < k ? token_row[(size_t)t * k + j0 + j] : -1;
+        if ((unsigned)r[j] >= (unsigned)R_cap) r[j] = -1;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        if (r[j] < 0) continue;
+        const size_t i = (size_t)r[j] * H + c;
         if constexpr (BF16) {
-          const uint2 v = *(const uint2 *)((const uint16_t *)rows + i);
-          acc += f32x4_t{bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+          v[j][0] = *(const u32x4_t *)((const uint16_t *)rows + i);
         } else {
-          acc += *(const f32x4_t *)((const float *)rows + i);
+          v[j][0] = *(const u32x4_t *)((const float *)rows + i);
+          v[j][1] = *(const u32x4_t *)((const float *)rows + i + 4);
         }
       }
-      mx4::store4<BF16>(y, (size_t)t * H + c, acc);
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        if (r[j] < 0) continue;
+        if constexpr (BF16) {
+          lo += f32x4_t{bf16_lo(v[j][0].x), bf16_hi(v[j][0].x), bf16_lo(v[j][0].y), bf16_hi(v[j][0].y)};
+          hi += f32x4_t{bf16_lo(v[j][0].z), bf16_hi(v[j][0].z), bf16_lo(v[j][0].w), bf16_hi(v[j][0].w)};
+        } else {
+          lo += __builtin_bit_cast(f32x4_t, v[j][0]);
+          hi += __builtin_bit_cast(f32x4_t, v[j][1]);
+        }
+      }
     }
+    mx4::store4<BF16>(y, (size_t)t * H + c, lo);
+    mx4::store4<BF16>(y, (size_t)t * H + c + 4, hi);
   }
 }
 
@@ -425,8 +457,10 @@ hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
   p.tp.R_cap = a.R_cap;
   p.tp.T = a.T;
   const long long dwords = (long long)a.T * (mx4::h_scale_stride(a.H) / 4);
-  hipLaunchKernelGGL(prepare_kernel<BM>, dim3(1 + (unsigned)(dwords < (1 << 20) ? (dwords + 255) / 256 : 4096)), dim3(256),
-                     0, s, p.tp, mt, gtiles, dtiles, counts, a.a_s, (uint32_t *)as);
+  const int gcap = mt * ntg, dcap = mt * ntd, most = gcap > dcap ? gcap : dcap;
+  const int parts = most < 64 * 256 ? ceil_div_i(most, 256) : 64;
+  hipLaunchKernelGGL(prepare_kernel<BM>, dim3(2 * parts + (unsigned)(dwords < (1 << 20) ? (dwords + 255) / 256 : 4096)),
+                     dim3(256), 0, s, p.tp, parts, gcap, dcap, gtiles, dtiles, counts, a.a_s, (uint32_t *)as);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   Mx4Params g = p;
@@ -452,8 +486,8 @@ hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
   hipLaunchKernelGGL((ffn_mx4_kernel<1, FA, BF16, BM>), dim3(NCU), dim3(NTHR), 0, s, d);
   err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(sum_rows_kernel<BF16>, dim3(a.T < 16384 ? a.T : 16384), dim3(256), 0, s, rows, a.token_row, a.T,
-                     a.k, a.R_cap, a.H, a.y);
+  hipLaunchKernelGGL(sum_rows_kernel<BF16>, dim3(a.T < 16384 ? a.T : 16384, ceil_div_i(a.H, SUM_THR * SUM_COLS)),
+                     dim3(SUM_THR), 0, s, rows, a.token_row, a.T, a.k, a.R_cap, a.H, a.y);
   return hipGetLastError();
 }
 
