@@ -71,17 +71,30 @@ __device__ __forceinline__ void dma(const __amdgpu_buffer_rsrc_t &r, char *to, u
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, voff, soff, 0, 0);
 }
 
-// Loads U0 .. U1 - 1 of the NL that this wave issues for step st of a tile into a ring slot (fewer activation
-// pieces than waves: some are fetched twice).
+// The stream of loads: where the next step's pieces come from and the slot they go to.  It runs RD - 1 steps ahead of
+// the products, into the next tile when a tile's steps are all on their way.
+template <int FA, int BM>
+struct Fetch {
+  __amdgpu_buffer_rsrc_t rw;
+  uint32_t off[Lay<FA, BM>::NL];
+  uint32_t sa, sw;                              // bytes to the step's pieces in activations and weights
+  __device__ __forceinline__ void start(const Tile<FA, BM> &t) {
+    rw = t.rw;
+#pragma unroll
+    for (int u = 0; u < Lay<FA, BM>::NL; u++) off[u] = t.off[u];
+    sa = sw = 0;
+  }
+};
+
+// Loads U0 .. U1 - 1 of the NL that this wave issues for a step into a ring slot (fewer activation pieces than waves:
+// some are fetched twice).
 template <int FA, int BM, int U0, int U1>
-__device__ __forceinline__ void load_pieces(const __amdgpu_buffer_rsrc_t &ra, const __amdgpu_buffer_rsrc_t &rw,
-                                            const uint32_t (&off)[Lay<FA, BM>::NL], int st, int wave, char *slot) {
+__device__ __forceinline__ void load_pieces(const __amdgpu_buffer_rsrc_t &ra, const Fetch<FA, BM> &f, int wave, char *slot) {
   using L = Lay<FA, BM>;
-  const uint32_t sa = (uint32_t)st * L::AROW, sw = (uint32_t)st * mx4::kBlk;
 #pragma unroll
   for (int u = U0; u < U1; u++) {
-    if (u < L::NA) dma(ra, slot + (wave + NWV * u) % L::PIECES * 1024, off[u], sa);
-    else dma(rw, slot + L::A_BYTES + (wave + NWV * (u - L::NA)) * 1024, off[u], sw);
+    if (u < L::NA) dma(ra, slot + (wave + NWV * u) % L::PIECES * 1024, f.off[u], f.sa);
+    else dma(f.rw, slot + L::A_BYTES + (wave + NWV * (u - L::NA)) * 1024, f.off[u], f.sw);
   }
 }
 
@@ -89,8 +102,8 @@ __device__ __forceinline__ void load_pieces(const __amdgpu_buffer_rsrc_t &ra, co
 // blocks of this wave.  ready() makes ``nxt`` usable; it is called once, before the first load for it.
 template <int MODE, int FA, bool BF16, int BM, int NB, typename READY>
 __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_buffer_rsrc_t &ra,
-                                          const Tile<FA, BM> &t, const Tile<FA, BM> &nxt, READY ready, int K, int wave,
-                                          int lane, int &slot, int &sslot, char *lds) {
+                                          const Tile<FA, BM> &t, const Tile<FA, BM> &nxt, READY ready, Fetch<FA, BM> &f,
+                                          int K, int wave, int lane, int &slot, int &sslot, char *lds) {
   using L = Lay<FA, BM>;
   const TileParams &p = mp.tp;
   const int n = lane & 15, q = lane >> 4, wn = wave & 3;
@@ -136,24 +149,16 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
             same ? t.soff : nxt.soff, (same ? c + 1 : 0) * (wave < L::SA ? 16 : mx4::kSblk));
       }
     }
-    const int sn = slot == 0 ? L::RD - 1 : slot - 1;  // the slot read in the step before
-    char *const ldn = lds + sn * L::SLOT;
+    if (kt == nst - (L::RD - 1)) f.start(nxt);
+    char *const ldn = lds + (slot == 0 ? L::RD - 1 : slot - 1) * L::SLOT;  // the slot read in the step before
     const uint32_t so = (uint32_t)slot * L::SLOT;
     const uint32_t ab = abase + so, wb = wbase + so;
-    const int st = kt + L::RD - 1;
     auto act = [&](int i) __attribute__((always_inline)) {
       if constexpr (FA == mx4::FP8)
         return mx4::piece8(*(const u32x4_t *)(lds + ab + i * 2048), *(const u32x4_t *)(lds + ab + (i * 2048 + 512)));
       else
         return mx4::piece4(*(const u32x4_t *)(lds + ab + i * 1024));
     };
-    // fetch step fs: of this tile, or of the next one (selected without a branch, which would cut the block apart)
-    const bool here = st < nst;
-    const int fs = here ? st : min(st - nst, nstep - 1);
-    const __amdgpu_buffer_rsrc_t rw = here ? t.rw : nxt.rw;
-    uint32_t off[L::NL];
-#pragma unroll
-    for (int u = 0; u < L::NL; u++) off[u] = here ? t.off[u] : nxt.off[u];
     if (kt < nstep) {
       v8i_t w[4], a[2];
 #pragma unroll
@@ -163,7 +168,7 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
       auto block = [&](auto I) __attribute__((always_inline)) {
         constexpr int i = decltype(I)::value;
         if constexpr (i + 1 < NB) a[(i + 1) & 1] = act(i + 1);
-        load_pieces<FA, BM, L::NL * i / NB, L::NL *(i + 1) / NB>(ra, rw, off, fs, wave, ldn);
+        load_pieces<FA, BM, L::NL * i / NB, L::NL *(i + 1) / NB>(ra, f, wave, ldn);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int g = 0; g < 4; g++) acc[i][g] = mx4::mfma<FA, j, j>(w[g], a[i & 1], acc[i][g], ws[g], as[i]);
@@ -172,9 +177,11 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
         (block(std::integral_constant<int, I>{}), ...);
       }(std::make_integer_sequence<int, NB>{});
     } else {
-      load_pieces<FA, BM, 0, L::NL>(ra, rw, off, fs, wave, ldn);
+      load_pieces<FA, BM, 0, L::NL>(ra, f, wave, ldn);
     }
     slot = slot + 1 == L::RD ? 0 : slot + 1;
+    f.sa = min(f.sa + L::AROW, (uint32_t)(nstep - 1) * L::AROW);
+    f.sw = min(f.sw + mx4::kBlk, (uint32_t)(nstep - 1) * mx4::kBlk);
   };
   for (int kt = 0; kt < nst; kt += 4) {
     step(std::integral_constant<int, 0>{}, kt);
@@ -202,6 +209,9 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
         mx4::store_pair<BF16>(p.out, row * p.H + t.col0 + 16 * g, q, acc[i][g] * gate[i], acc[i][g + 1] * gate[i], on);
     }
   }
+  // Ends the stores' branches here.  Without it they end where the NB cases meet, which makes the loads' state, uniform
+  // as it is, look different between lanes there: it would live in vector registers.
+  asm volatile("; end of tile, %0 blocks" ::"n"(NB));
 }
 
 template <int MODE, int FA, bool BF16, int BM>
@@ -213,7 +223,7 @@ __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
   const int nstep = K / 128;
   // Workgroups go round-robin over the 8 XCDs: XCD x takes the x-th eighth of the list, its workgroups in
   // turn, so that the tiles of one expert, which share operands, meet in one L2.
-  const int total = *mp.ntiles, per = gridDim.x >> 3, xcd = blockIdx.x & 7;
+  const int total = __builtin_amdgcn_readfirstlane(*mp.ntiles), per = gridDim.x >> 3, xcd = blockIdx.x & 7;
   const int qt = total >> 3, rem = total & 7;
   const int end = xcd * qt + min(xcd, rem) + qt + (xcd < rem ? 1 : 0);
   int at = xcd * qt + min(xcd, rem) + (blockIdx.x >> 3);
@@ -272,16 +282,21 @@ __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
   describe(cur, at);
   place(cur);
   dma(cur.rs, lds + L::RD * L::SLOT + wave * 1024 - (wave >= L::SA + 4 ? 4096 : 0), cur.soff, 0);
+  Fetch<FA, BM> fetch;
+  fetch.start(cur);
 #pragma unroll
-  for (int d = 0; d < L::RD - 1; d++) 
-    load_pieces<FA, BM, 0, L::NL>(ra, cur.rw, cur.off, min(d, nstep - 1), wave, lds + d * L::SLOT);
+  for (int d = 0; d < L::RD - 1; d++) {
+    load_pieces<FA, BM, 0, L::NL>(ra, fetch, wave, lds + d * L::SLOT);
+    fetch.sa = min(fetch.sa + L::AROW, (uint32_t)(nstep - 1) * L::AROW);
+    fetch.sw = min(fetch.sw + mx4::kBlk, (uint32_t)(nstep - 1) * mx4::kBlk);
+  }
   int slot = 0, sslot = 0;
   for (;;) {
     const bool more = at + per < end;
     at = more ? at + per : at;  // after the last tile: its own first steps again, which nobody reads
     describe(nxt, at);
     auto ready = [&]() __attribute__((always_inline)) { place(nxt); };
-#define MX4_BODY(NB) tile_body<MODE, FA, BF16, BM, NB>(mp, ra, cur, nxt, ready, K, wave, lane, slot, sslot, lds)
+#define MX4_BODY(NB) tile_body<MODE, FA, BF16, BM, NB>(mp, ra, cur, nxt, ready, fetch, K, wave, lane, slot, sslot, lds)
     // the waves of a tile may take different cases: each issues the same loads and meets the same barriers
     if constexpr (BM == 64) {
       if (cur.nb == 1) MX4_BODY(1);
