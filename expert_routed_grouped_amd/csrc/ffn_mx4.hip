@@ -51,7 +51,8 @@ struct Lay {
   static constexpr int A_BYTES = BM * AROW, W_BYTES = BN * 64, PIECES = A_BYTES / 1024;
   static constexpr int SLOT = A_BYTES + W_BYTES;
   static constexpr int SSLOT = BM * 16 + BN / 16 * 256;      // scales of four steps
-  static constexpr int FIT = (163840 - 2 * SSLOT) / SLOT, RD = FIT < 6 ? FIT : 6;  // slots of the ring
+  static constexpr int ROWS = BM * 4;                        // a word per row: tokens (gate/up) or gates (down)
+  static constexpr int FIT = (163840 - 2 * SSLOT - ROWS) / SLOT, RD = FIT < 6 ? FIT : 6;  // slots of the ring
   static constexpr int SA = BM / 64;                         // waves that fetch activation scales; the next four fetch weight scales
   static constexpr int NA = (PIECES + NWV - 1) / NWV, NL = NA + W_BYTES / 1024 / NWV;  // loads per wave and step
   static_assert(RD >= 3, "two steps ahead");
@@ -63,7 +64,7 @@ struct Tile {
   __amdgpu_buffer_rsrc_t rw, rs;                // its expert's weights; the scales this wave fetches
   uint32_t off[Lay<FA, BM>::NL];                // this lane's bytes of its wave's pieces at step 0, activations first
   uint32_t soff;                                // and of its scales
-  int col0, rbase, mvalid, arow0, nb;
+  int r0, rows, col0, rbase, mvalid, arow0, nb;
 };
 
 // 16 bytes per lane from memory to 1 KB of LDS.
@@ -98,6 +99,18 @@ __device__ __forceinline__ void load_pieces(const __amdgpu_buffer_rsrc_t &ra, co
   }
 }
 
+// A word per row of the tile, rows past its end as its last: the source rows' tokens or the gates.  By way of LDS, and
+// the tile list by scalar loads, because for a load into vector registers the compiler waits until nothing younger is
+// under way either, i.e. for the whole ring (8 us a tile).
+template <int MODE, int FA, int BM>
+__device__ __forceinline__ void fetch_rows(const TileParams &p, const Tile<FA, BM> &t, int wave, int lane, char *to) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+      MODE == 0 ? (void *)p.row_token : (void *)p.row_w, (short)0, p.R_cap * 4, kRsrcWord3);
+  const int piece = wave % (BM / 64);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + piece * 256), 4,
+                                           (t.r0 + min(piece * 64 + lane, t.rows - 1)) * 4, 0, 0, 0);
+}
+
 // One tile: the K loop and the epilogue.  MODE 0: gate/up + SwiGLU -> h.  MODE 1: down -> gated rows.  NB: 16-row
 // blocks of this wave.  ready() makes ``nxt`` usable; it is called once, before the first load for it.
 template <int MODE, int FA, bool BF16, int BM, int NB, typename READY>
@@ -114,11 +127,6 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
   for (int i = 0; i < NB; i++)
 #pragma unroll
     for (int g = 0; g < 4; g++) acc[i][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  float gate[NB];
-  if constexpr (MODE == 1) {
-#pragma unroll
-    for (int i = 0; i < NB; i++) gate[i] = p.row_w[t.rbase + min(16 * i + n, max(t.mvalid, 1) - 1)];
-  }
   // LDS bytes of this lane's operands inside a slot
   const uint32_t wbase = L::A_BYTES + (uint32_t)wn * 4096u + lane * 16u;
   const uint32_t abase = FA == mx4::FP8
@@ -136,7 +144,11 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
     asm volatile("s_barrier" ::: "memory");
     if constexpr (j == 0) {
       const int c = kt >> 2;
-      if (c == max(nch - 2, 0)) ready();
+      if (kt == 0) fetch_rows<MODE, FA, BM>(p, MODE == 0 ? nxt : t, wave, lane, lds + L::RD * L::SLOT + 2 * L::SSLOT);
+      if (c == max(nch - 2, 0)) {  // the tokens came with or before step 0's pieces: they are there from step 4 on
+        if (MODE == 0 && kt == 0) asm volatile("s_waitcnt vmcnt(0)\ns_barrier" ::: "memory");
+        ready();
+      }
       if (c < nch) {
         const char *sp = lds + L::RD * L::SLOT + sslot * L::SSLOT;
 #pragma unroll
@@ -203,10 +215,12 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
         for (int r = 0; r < 4; r++) v[g][r] = silu_fast(acc[i][g][r]) * acc[i][2 + g][r];
       mx4::store_h_block<FA>(v, on, (uint8_t *)p.out + row * mx4::code_bytes<FA>(p.I),
                              mp.out_scales + row * mx4::h_scale_stride(p.I), t.col0, q);
-    } else if (t.col0 < p.H) {  // H is a multiple of 128: a wave's 64 columns are all there or none
+    } else if (t.col0 < p.H) {
+      const float gate = *(const float *)(lds + L::RD * L::SLOT + 2 * L::SSLOT + (t.arow0 + m) * 4);
+      // H is a multiple of 128: a wave's 64 columns are all there or none
 #pragma unroll
       for (int g = 0; g < 4; g += 2)
-        mx4::store_pair<BF16>(p.out, row * p.H + t.col0 + 16 * g, q, acc[i][g] * gate[i], acc[i][g + 1] * gate[i], on);
+        mx4::store_pair<BF16>(p.out, row * p.H + t.col0 + 16 * g, q, acc[i][g] * gate, acc[i][g + 1] * gate, on);
     }
   }
   // Ends the stores' branches here.  Without it they end where the NB cases meet, which makes the loads' state, uniform
@@ -217,7 +231,7 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
 template <int MODE, int FA, bool BF16, int BM>
 __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
   using L = Lay<FA, BM>;
-  __shared__ __attribute__((aligned(1024))) char lds[L::RD * L::SLOT + 2 * L::SSLOT];
+  __shared__ __attribute__((aligned(1024))) char lds[L::RD * L::SLOT + 2 * L::SSLOT + L::ROWS];
   const TileParams &p = mp.tp;
   const int K = MODE == 0 ? p.H : p.I, Nw = MODE == 0 ? 2 * p.I : p.H;
   const int nstep = K / 128;
@@ -237,13 +251,12 @@ __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
   const __amdgpu_buffer_rsrc_t rsa =
       __builtin_amdgcn_make_buffer_rsrc((void *)mp.a_scales, (short)0, (int)(arows * ass), kRsrcWord3);
 
-  // A tile's description; the activation offsets hold the source rows of this lane's pieces and scales (rows past
-  // the tile's end repeat its last) until place() turns them into bytes, so that nothing waits for them here.
-  auto describe = [&](Tile<FA, BM> &t, int i) __attribute__((always_inline)) {
-    const int4 d = mp.tiles[i];
-    const int e = __builtin_amdgcn_readfirstlane(d.x), nt = __builtin_amdgcn_readfirstlane(d.y);
-    const int r0 = __builtin_amdgcn_readfirstlane(d.z), rp = __builtin_amdgcn_readfirstlane(d.w);
-    const int rows = rp & 0xffff, part = rp >> 16;
+  // A tile's description, and once its rows' tokens are in LDS the bytes of this lane's activation pieces and scales
+  // (rows past the tile's end repeat its last).
+  typedef int i32x4_t __attribute__((ext_vector_type(4)));
+  const auto list = (const __attribute__((address_space(4))) i32x4_t *)(uintptr_t)mp.tiles;
+  auto describe = [&](Tile<FA, BM> &t, i32x4_t d) __attribute__((always_inline)) {
+    const int e = d.x, nt = d.y, r0 = d.z, rows = d.w & 0xffff, part = d.w >> 16;
     const size_t wexp = (size_t)e * (Nw / 16);
     t.rw = __builtin_amdgcn_make_buffer_rsrc((void *)((const char *)p.w + wexp * gc), (short)0, (int)(Nw / 16 * gc),
                                              kRsrcWord3);
@@ -260,26 +273,31 @@ __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
     t.rbase = r0 + t.arow0;
     t.mvalid = min(rows - t.arow0, part);
     t.nb = min(part >> 4, (max(t.mvalid, 1) + 15) >> 4);
+    t.r0 = r0;
+    t.rows = rows;
+    if (wave >= L::SA) t.soff = group(((wave - L::SA) & 3) * 4 + q) * gs + (uint32_t)n * 16u;
+  };
+  auto place = [&](Tile<FA, BM> &t) __attribute__((always_inline)) {
     auto src = [&](int row) -> uint32_t {
-      const int r = r0 + min(row, rows - 1);
-      return MODE == 0 ? (uint32_t)p.row_token[r] : (uint32_t)r;
+      const uint32_t r = MODE == 0 ? *(const uint32_t *)(lds + L::RD * L::SLOT + 2 * L::SSLOT + row * 4)
+                                   : (uint32_t)(t.r0 + min(row, t.rows - 1));
+      return min(r, arows - 1);
     };
 #pragma unroll
     for (int u = 0; u < L::NA; u++) {
       const int b = (wave + NWV * u) % L::PIECES;
-      t.off[u] = src(FA == mx4::FP8 ? b * 8 + (lane & 7) : b * 16 + n);
+      t.off[u] = src(FA == mx4::FP8 ? b * 8 + (lane & 7) : b * 16 + n) * arb +
+                 (uint32_t)(FA == mx4::FP8 ? lane >> 3 : q) * 16u;
     }
-    t.soff = wave < L::SA ? src(wave * 64 + lane) : group(((wave - L::SA) & 3) * 4 + q) * gs + (uint32_t)n * 16u;
-  };
-  auto place = [&](Tile<FA, BM> &t) __attribute__((always_inline)) {
-#pragma unroll
-    for (int u = 0; u < L::NA; u++)
-      t.off[u] = min(t.off[u], arows - 1) * arb + (uint32_t)(FA == mx4::FP8 ? lane >> 3 : q) * 16u;
-    if (wave < L::SA) t.soff = min(t.soff, arows - 1) * ass;
+    if (wave < L::SA) t.soff = src(wave * 64 + lane) * ass;
   };
 
   Tile<FA, BM> cur, nxt;
-  describe(cur, at);
+  describe(cur, list[at]);
+  if constexpr (MODE == 0) {
+    fetch_rows<MODE, FA, BM>(p, cur, wave, lane, lds + L::RD * L::SLOT + 2 * L::SSLOT);
+    asm volatile("s_waitcnt vmcnt(0)\ns_barrier" ::: "memory");
+  }
   place(cur);
   dma(cur.rs, lds + L::RD * L::SLOT + wave * 1024 - (wave >= L::SA + 4 ? 4096 : 0), cur.soff, 0);
   Fetch<FA, BM> fetch;
@@ -291,10 +309,12 @@ __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
     fetch.sw = min(fetch.sw + mx4::kBlk, (uint32_t)(nstep - 1) * mx4::kBlk);
   }
   int slot = 0, sslot = 0;
+  i32x4_t d = list[at + per < end ? at + per : at];
   for (;;) {
     const bool more = at + per < end;
     at = more ? at + per : at;  // after the last tile: its own first steps again, which nobody reads
-    describe(nxt, at);
+    describe(nxt, d);
+    d = list[at + per < end ? at + per : at];
     auto ready = [&]() __attribute__((always_inline)) { place(nxt); };
 #define MX4_BODY(NB) tile_body<MODE, FA, BF16, BM, NB>(mp, ra, cur, nxt, ready, fetch, K, wave, lane, slot, sslot, lds)
     // the waves of a tile may take different cases: each issues the same loads and meets the same barriers
@@ -304,7 +324,6 @@ __global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
     } else {
       if (cur.nb <= 2) MX4_BODY(2);
       else if (cur.nb <= 4) MX4_BODY(4);
-      else if (L::MAXNB > 6 && cur.nb > 6) MX4_BODY(L::MAXNB);
       else MX4_BODY(6);
     }
 #undef MX4_BODY
@@ -439,17 +458,8 @@ int max_mtiles(int T, int R_cap, int El, int BM) {
   const long long a = ((long long)R_cap + (long long)El * (BM - 1)) / BM, b = (long long)El * ceil_div_i(T, BM);
   return (int)(a < b ? a : b);
 }
-// Rows of a tile: 64 while an expert has at most 64 rows on average, else 192 or 256, whichever pads an expert of
-// average size to fewer rows.
-int tile_rows(int R_cap, int El) {
-  const int avg = ceil_div_i(R_cap, El);
-  if (avg <= 64) return 64;
-  auto padded = [&](int BM) {
-    const int m = ceil_div_i(avg, BM);
-    return m * ((ceil_div_i(avg, m) + 31) & ~31);
-  };
-  return padded(256) < padded(192) ? 256 : 192;
-}
+// Rows of a tile: 64 while an expert has at most 64 rows on average, else 192.
+int tile_rows(int R_cap, int El) { return ceil_div_i(R_cap, El) <= 64 ? 64 : 192; }
 size_t list_bytes(int T, int R_cap, int El, int H, int I) {
   const int m = max_mtiles(T, R_cap, El, tile_rows(R_cap, El));
   return 256 + align_up((size_t)m * (I / 128 + ceil_div_i(H, BN)) * sizeof(int4), 256);
@@ -508,11 +518,7 @@ hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
 
 template <int FA, bool BF16>
 hipError_t launch(const FfnMx4Args &a, hipStream_t s) {
-  switch (tile_rows(a.R_cap, a.El)) {
-    case 64: return launch_tiles<FA, BF16, 64>(a, s);
-    case 192: return launch_tiles<FA, BF16, 192>(a, s);
-    default: return launch_tiles<FA, BF16, 256>(a, s);
-  }
+  return tile_rows(a.R_cap, a.El) == 64 ? launch_tiles<FA, BF16, 64>(a, s) : launch_tiles<FA, BF16, 192>(a, s);
 }
 
 }  // namespace
