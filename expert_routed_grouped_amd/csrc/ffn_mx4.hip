@@ -30,7 +30,8 @@ namespace {
 using ffn::TileParams;
 using mx4::v8i_t;
 
-constexpr int BN = 256, NTHR = 512, NWV = NTHR / 64, NCU = 256;
+// Waves 0 .. 7 multiply, waves 8 .. 11 load.
+constexpr int BN = 256, NC = 8, NP = 4, NTHR = (NC + NP) * 64, NCU = 256;
 
 struct Mx4Params {
   TileParams tp;               // offsets, row_token, row_w, El, H, I, R_cap, T; a / w / out: codes (out: rows for down)
@@ -46,25 +47,20 @@ constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw buffer, 32-bit data format
 
 template <int FA, int BM>
 struct Lay {
-  static constexpr int MAXNB = BM / 32;                      // 16-row blocks of a wave
   static constexpr int AROW = FA == mx4::FP8 ? 128 : 64;     // activation bytes of a row and step
-  static constexpr int A_BYTES = BM * AROW, W_BYTES = BN * 64, PIECES = A_BYTES / 1024;
-  static constexpr int SLOT = A_BYTES + W_BYTES;
+  static constexpr int A_BYTES = BM * AROW, W_BYTES = BN * 64, SLOT = A_BYTES + W_BYTES;
   static constexpr int SSLOT = BM * 16 + BN / 16 * 256;      // scales of four steps
   static constexpr int ROWS = BM * 4;                        // a word per row: tokens (gate/up) or gates (down)
   static constexpr int FIT = (163840 - 2 * SSLOT - ROWS) / SLOT, RD = FIT < 6 ? FIT : 6;  // slots of the ring
-  static constexpr int SA = BM / 64;                         // waves that fetch activation scales; the next four fetch weight scales
-  static constexpr int NA = (PIECES + NWV - 1) / NWV, NL = NA + W_BYTES / 1024 / NWV;  // loads per wave and step
-  static_assert(RD >= 3, "two steps ahead");
-};
-
-// A tile as one wave sees it.
-template <int FA, int BM>
-struct Tile {
-  __amdgpu_buffer_rsrc_t rw, rs;                // its expert's weights; the scales this wave fetches
-  uint32_t off[Lay<FA, BM>::NL];                // this lane's bytes of its wave's pieces at step 0, activations first
-  uint32_t soff;                                // and of its scales
-  int r0, rows, col0, rbase, mvalid, arow0, nb;
+  static constexpr int SCALES = RD * SLOT, ROW0 = SCALES + 2 * SSLOT, BYTES = ROW0 + ROWS;
+  static constexpr int NA = A_BYTES / 1024 / NP, NL = NA + W_BYTES / 1024 / NP;  // loads per loading wave and step
+  static constexpr int SA = BM / 64, SP = SA + 4, NS = (SP + NP - 1) / NP;  // scale pieces: activations, all; loads a wave
+  static_assert(RD >= 3 && RD <= 6 && A_BYTES % (1024 * NP) == 0, "two steps ahead; whole pieces");
+  // Load u of a wave fetches scale piece scale_piece(wave, u); past the last one a weight piece again.
+  static __device__ __forceinline__ int scale_piece(int pw, int u) {
+    const int b = pw + NP * u;
+    return b < SP ? b : SA + (b & 3);
+  }
 };
 
 // 16 bytes per lane from memory to 1 KB of LDS.
@@ -72,51 +68,183 @@ __device__ __forceinline__ void dma(const __amdgpu_buffer_rsrc_t &r, char *to, u
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, voff, soff, 0, 0);
 }
 
-// The stream of loads: where the next step's pieces come from and the slot they go to.  It runs RD - 1 steps ahead of
-// the products, into the next tile when a tile's steps are all on their way.
-template <int FA, int BM>
-struct Fetch {
-  __amdgpu_buffer_rsrc_t rw;
-  uint32_t off[Lay<FA, BM>::NL];
-  uint32_t sa, sw;                              // bytes to the step's pieces in activations and weights
-  __device__ __forceinline__ void start(const Tile<FA, BM> &t) {
-    rw = t.rw;
-#pragma unroll
-    for (int u = 0; u < Lay<FA, BM>::NL; u++) off[u] = t.off[u];
-    sa = sw = 0;
+// The workgroup's share of the tile list.  Workgroups go round-robin over the 8 XCDs: XCD x takes the x-th eighth of
+// the list, its workgroups in turn, so that the tiles of one expert, which share operands, meet in one L2.  The
+// list is read by scalar loads.
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+struct Share {
+  const __attribute__((address_space(4))) i32x4_t *list;
+  int at, end, per;
+  __device__ __forceinline__ explicit Share(const Mx4Params &mp) {
+    list = (const __attribute__((address_space(4))) i32x4_t *)(uintptr_t)mp.tiles;
+    const int total = *(const __attribute__((address_space(4))) int *)(uintptr_t)mp.ntiles, xcd = blockIdx.x & 7;
+    const int qt = total >> 3, rem = total & 7;
+    per = gridDim.x >> 3;
+    end = xcd * qt + min(xcd, rem) + qt + (xcd < rem ? 1 : 0);
+    at = xcd * qt + min(xcd, rem) + (blockIdx.x >> 3);
   }
 };
 
-// Loads U0 .. U1 - 1 of the NL that this wave issues for a step into a ring slot (fewer activation pieces than waves:
-// some are fetched twice).
-template <int FA, int BM, int U0, int U1>
-__device__ __forceinline__ void load_pieces(const __amdgpu_buffer_rsrc_t &ra, const Fetch<FA, BM> &f, int wave, char *slot) {
+// ---------------------------------------------------------------- the loading waves
+// A tile as one loading wave sees it.
+template <int FA, int BM>
+struct Source {
+  __amdgpu_buffer_rsrc_t rw, rs[Lay<FA, BM>::NS];  // its expert's weights; the scales this wave fetches
+  uint32_t off[Lay<FA, BM>::NL];                   // this lane's bytes of its wave's pieces at step 0, activations first
+  uint32_t soff[Lay<FA, BM>::NS];                  // and of its scales
+  int r0, rows;
+};
+
+template <int MODE, int FA, int BM>
+__device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw, int lane, char *lds) {
   using L = Lay<FA, BM>;
+  const TileParams &p = mp.tp;
+  const int K = MODE == 0 ? p.H : p.I, Nw = MODE == 0 ? 2 * p.I : p.H;
+  const int nstep = K / 128, nch = (nstep + 3) / 4, nst = max(nstep, L::RD - 1);
+  const int n = lane & 15, q = lane >> 4;
+  const uint32_t arb = (uint32_t)mx4::code_bytes<FA>(K), ass = (uint32_t)mx4::h_scale_stride(K);
+  const uint32_t gc = (uint32_t)mx4::group_codes(K), gs = (uint32_t)mx4::group_scales(K);
+  const uint32_t arows = MODE == 0 ? (uint32_t)p.T : (uint32_t)p.R_cap;
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)p.a, (short)0, (int)(arows * arb), kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rsa =
+      __builtin_amdgcn_make_buffer_rsrc((void *)mp.a_scales, (short)0, (int)(arows * ass), kRsrcWord3);
+  const __amdgpu_buffer_rsrc_t rrow = __builtin_amdgcn_make_buffer_rsrc(
+      MODE == 0 ? (void *)p.row_token : (void *)p.row_w, (short)0, p.R_cap * 4, kRsrcWord3);
+
+  // What of a tile needs its description only.
+  auto describe = [&](Source<FA, BM> &t, i32x4_t d) __attribute__((always_inline)) {
+    const int nt = d.y;
+    const size_t wexp = (size_t)d.x * (Nw / 16);
+    t.r0 = d.z;
+    t.rows = d.w & 0xffff;
+    t.rw = __builtin_amdgcn_make_buffer_rsrc((void *)((const char *)p.w + wexp * gc), (short)0, (int)(Nw / 16 * gc),
+                                             kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rsw =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(mp.w_scales + wexp * gs), (short)0, (int)(Nw / 16 * gs), kRsrcWord3);
+    auto group = [&](int i) -> uint32_t {  // weight group of LDS piece i
+      if constexpr (MODE == 0) return (uint32_t)(nt * 8 + (i >> 2) * 2 + (i & 1) + ((i >> 1) & 1) * (p.I / 16));
+      else return (uint32_t)min(nt * 16 + i, p.H / 16 - 1);
+    };
 #pragma unroll
-  for (int u = U0; u < U1; u++) {
-    if (u < L::NA) dma(ra, slot + (wave + NWV * u) % L::PIECES * 1024, f.off[u], f.sa);
-    else dma(f.rw, slot + L::A_BYTES + (wave + NWV * (u - L::NA)) * 1024, f.off[u], f.sw);
+    for (int u = 0; u < L::NL - L::NA; u++) t.off[L::NA + u] = group(pw + NP * u) * gc + (uint32_t)lane * 16u;
+#pragma unroll
+    for (int u = 0; u < L::NS; u++) {
+      const int b = L::scale_piece(pw, u);
+      t.rs[u] = b < L::SA ? rsa : rsw;
+      if (b >= L::SA) t.soff[u] = group((b - L::SA) * 4 + q) * gs + (uint32_t)n * 16u;
+    }
+  };
+  // A word per row of the tile to LDS, rows past its end as its last: the source rows' tokens or the gates.  Not into
+  // registers: for such a load the compiler waits until nothing younger is under way either, i.e. for the whole ring.
+  auto fetch_rows = [&](const Source<FA, BM> &t) __attribute__((always_inline)) {
+    const int piece = pw % (BM / 64);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rrow, (lds_void *)(lds + L::ROW0 + piece * 256), 4,
+                                             (t.r0 + min(piece * 64 + lane, t.rows - 1)) * 4, 0, 0, 0);
+  };
+  // What of a tile needs its rows' tokens: the bytes of this lane's activation pieces and scales.
+  auto place = [&](Source<FA, BM> &t) __attribute__((always_inline)) {
+    auto src = [&](int row) -> uint32_t {
+      const uint32_t r = MODE == 0 ? *(const uint32_t *)(lds + L::ROW0 + row * 4) : (uint32_t)(t.r0 + min(row, t.rows - 1));
+      return min(r, arows - 1);
+    };
+#pragma unroll
+    for (int u = 0; u < L::NA; u++) {
+      const int b = pw + NP * u;
+      t.off[u] = src(FA == mx4::FP8 ? b * 8 + (lane & 7) : b * 16 + n) * arb +
+                 (uint32_t)(FA == mx4::FP8 ? lane >> 3 : q) * 16u;
+    }
+#pragma unroll
+    for (int u = 0; u < L::NS; u++)
+      if (L::scale_piece(pw, u) < L::SA) t.soff[u] = src(L::scale_piece(pw, u) * 64 + lane) * ass;
+  };
+
+  // The stream of loads runs RD - 1 steps ahead of the products, into the next tile when a tile's steps are all on
+  // their way.
+  __amdgpu_buffer_rsrc_t rw;
+  uint32_t off[L::NL], sa = 0, sw = 0;  // bytes to the step's pieces in activations and weights
+  auto start = [&](const Source<FA, BM> &t) __attribute__((always_inline)) {
+    rw = t.rw;
+#pragma unroll
+    for (int u = 0; u < L::NL; u++) off[u] = t.off[u];
+    sa = sw = 0;
+  };
+  auto load_step = [&](int slot) __attribute__((always_inline)) {
+    char *to = lds + slot * L::SLOT + pw * 1024;
+#pragma unroll
+    for (int u = 0; u < L::NL; u++) {
+      if (u < L::NA) dma(ra, to + u * NP * 1024, off[u], sa);
+      else dma(rw, to + L::A_BYTES + (u - L::NA) * NP * 1024, off[u], sw);
+    }
+    sa = min(sa + L::AROW, (uint32_t)(nstep - 1) * L::AROW);
+    sw = min(sw + mx4::kBlk, (uint32_t)(nstep - 1) * mx4::kBlk);
+  };
+  auto load_scales = [&](const Source<FA, BM> &t, const Source<FA, BM> &other, bool same, int c, int sslot)
+                         __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < L::NS; u++) {
+      const int b = L::scale_piece(pw, u);
+      dma(same ? t.rs[u] : other.rs[u], lds + L::SCALES + sslot * L::SSLOT + b * 1024, same ? t.soff[u] : other.soff[u],
+          same ? c * (b < L::SA ? 16 : mx4::kSblk) : 0);
+    }
+  };
+
+  Source<FA, BM> cur, nxt;
+  describe(cur, sh.list[sh.at]);
+  i32x4_t d = sh.list[sh.at + sh.per < sh.end ? sh.at + sh.per : sh.at];
+  if constexpr (MODE == 0) {
+    fetch_rows(cur);
+    asm volatile("s_waitcnt vmcnt(0)\ns_barrier" ::: "memory");
   }
+  place(cur);
+  load_scales(cur, cur, true, 0, 0);
+  start(cur);
+#pragma unroll
+  for (int i = 0; i < L::RD - 1; i++) load_step(i);
+  int slot = 0, sslot = 0;
+  for (;;) {
+    const bool more = sh.at + sh.per < sh.end;
+    if (more) sh.at += sh.per;  // after the last tile: its own first steps again, which nobody reads
+    describe(nxt, d);
+    d = sh.list[sh.at + sh.per < sh.end ? sh.at + sh.per : sh.at];
+    // After a tile whose last scale piece is short its successor's first scales are younger than the count below says.
+    if ((nstep & 3) != 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (int kt = 0; kt < nst; kt++) {
+      // What is read in this step was issued RD - 1 steps ago or earlier (the scales of a whole piece, four); newer are
+      // the pieces of RD - 2 steps.
+      asm volatile("s_waitcnt vmcnt(%0)\ns_barrier" ::"n"(L::NL *(L::RD - 2)) : "memory");
+      if (kt == 0) fetch_rows(MODE == 0 ? nxt : cur);
+      if ((kt & 3) == 0) {
+        const int c = kt >> 2;
+        if (c == max(nch - 2, 0)) {  // the rows came before step 0's pieces: they are there from step 4 on
+          if (MODE == 0 && kt == 0) asm volatile("s_waitcnt vmcnt(0)\ns_barrier" ::: "memory");
+          place(nxt);
+        }
+        if (c < nch) {
+          sslot ^= 1;
+          load_scales(cur, nxt, c + 1 < nch, c + 1, sslot);
+        }
+      }
+      if (kt == nst - (L::RD - 1)) start(nxt);
+      load_step(slot == 0 ? L::RD - 1 : slot - 1);  // the slot read in the step before
+      slot = slot + 1 == L::RD ? 0 : slot + 1;
+    }
+    if (!more) break;
+    cur = nxt;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
 }
 
-// A word per row of the tile, rows past its end as its last: the source rows' tokens or the gates.  By way of LDS, and
-// the tile list by scalar loads, because for a load into vector registers the compiler waits until nothing younger is
-// under way either, i.e. for the whole ring (8 us a tile).
-template <int MODE, int FA, int BM>
-__device__ __forceinline__ void fetch_rows(const TileParams &p, const Tile<FA, BM> &t, int wave, int lane, char *to) {
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-      MODE == 0 ? (void *)p.row_token : (void *)p.row_w, (short)0, p.R_cap * 4, kRsrcWord3);
-  const int piece = wave % (BM / 64);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + piece * 256), 4,
-                                           (t.r0 + min(piece * 64 + lane, t.rows - 1)) * 4, 0, 0, 0);
-}
+// ---------------------------------------------------------------- the multiplying waves
+// A tile as one of them sees it.
+struct Tile {
+  int col0, rbase, mvalid, arow0, nb;
+};
 
 // One tile: the K loop and the epilogue.  MODE 0: gate/up + SwiGLU -> h.  MODE 1: down -> gated rows.  NB: 16-row
-// blocks of this wave.  ready() makes ``nxt`` usable; it is called once, before the first load for it.
-template <int MODE, int FA, bool BF16, int BM, int NB, typename READY>
-__device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_buffer_rsrc_t &ra,
-                                          const Tile<FA, BM> &t, const Tile<FA, BM> &nxt, READY ready, Fetch<FA, BM> &f,
-                                          int K, int wave, int lane, int &slot, int &sslot, char *lds) {
+// blocks of this wave.
+template <int MODE, int FA, bool BF16, int BM, int NB>
+__device__ __forceinline__ void multiply(const Mx4Params &mp, const Tile &t, int K, int wave, int lane, int &slot,
+                                         int &sslot, char *lds) {
   using L = Lay<FA, BM>;
   const TileParams &p = mp.tp;
   const int n = lane & 15, q = lane >> 4, wn = wave & 3;
@@ -136,35 +264,19 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
   auto step = [&](auto JC, int kt) __attribute__((always_inline)) {
     constexpr int j = decltype(JC)::value;
     if (kt >= nst) return;
-    // everything this step reads was issued RD - 1 steps ago or earlier (the scales of a whole piece, four); newer
-    // are the pieces of RD - 2 steps.  After a tile whose last piece is short its successor's first scales are
-    // younger than that.
-    if (j == 0 && kt == 0 && (nstep & 3) != 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L::NL *(L::RD - 2)) : "memory");
-    asm volatile("s_barrier" ::: "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)\ns_barrier" ::: "memory");  // this wave is done with the slot before
     if constexpr (j == 0) {
-      const int c = kt >> 2;
-      if (kt == 0) fetch_rows<MODE, FA, BM>(p, MODE == 0 ? nxt : t, wave, lane, lds + L::RD * L::SLOT + 2 * L::SSLOT);
-      if (c == max(nch - 2, 0)) {  // the tokens came with or before step 0's pieces: they are there from step 4 on
-        if (MODE == 0 && kt == 0) asm volatile("s_waitcnt vmcnt(0)\ns_barrier" ::: "memory");
-        ready();
-      }
-      if (c < nch) {
-        const char *sp = lds + L::RD * L::SLOT + sslot * L::SSLOT;
+      if (MODE == 0 && kt == 0 && nch <= 2) asm volatile("s_barrier" ::: "memory");  // the loading waves' extra one
+      if (kt < nstep) {
+        const char *sp = lds + L::SCALES + sslot * L::SSLOT;
 #pragma unroll
         for (int g = 0; g < 4; g++) ws[g] = *(const uint32_t *)(sp + BM * 16 + (wn * 4 + g) * 256 + lane * 4);
 #pragma unroll
         for (int i = 0; i < NB; i++) as[i] = *(const uint32_t *)(sp + (t.arow0 + 16 * i + n) * 16 + q * 4);
         sslot ^= 1;
-        const bool same = c + 1 < nch;
-        dma(same ? t.rs : nxt.rs, lds + L::RD * L::SLOT + sslot * L::SSLOT + wave * 1024 - (wave >= L::SA + 4 ? 4096 : 0),
-            same ? t.soff : nxt.soff, (same ? c + 1 : 0) * (wave < L::SA ? 16 : mx4::kSblk));
       }
     }
-    if (kt == nst - (L::RD - 1)) f.start(nxt);
-    char *const ldn = lds + (slot == 0 ? L::RD - 1 : slot - 1) * L::SLOT;  // the slot read in the step before
-    const uint32_t so = (uint32_t)slot * L::SLOT;
-    const uint32_t ab = abase + so, wb = wbase + so;
+    const uint32_t ab = abase + (uint32_t)slot * L::SLOT, wb = wbase + (uint32_t)slot * L::SLOT;
     auto act = [&](int i) __attribute__((always_inline)) {
       if constexpr (FA == mx4::FP8)
         return mx4::piece8(*(const u32x4_t *)(lds + ab + i * 2048), *(const u32x4_t *)(lds + ab + (i * 2048 + 512)));
@@ -176,24 +288,15 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
 #pragma unroll
       for (int g = 0; g < 4; g++) w[g] = mx4::piece4(*(const u32x4_t *)(lds + wb + g * 1024));
       a[0] = act(0);
-      // block i: fetch the next operand and a share of the step to come, then multiply
-      auto block = [&](auto I) __attribute__((always_inline)) {
-        constexpr int i = decltype(I)::value;
-        if constexpr (i + 1 < NB) a[(i + 1) & 1] = act(i + 1);
-        load_pieces<FA, BM, L::NL * i / NB, L::NL *(i + 1) / NB>(ra, f, wave, ldn);
+#pragma unroll
+      for (int i = 0; i < NB; i++) {
+        if (i + 1 < NB) a[(i + 1) & 1] = act(i + 1);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int g = 0; g < 4; g++) acc[i][g] = mx4::mfma<FA, j, j>(w[g], a[i & 1], acc[i][g], ws[g], as[i]);
-      };
-      [&]<int... I>(std::integer_sequence<int, I...>) __attribute__((always_inline)) {
-        (block(std::integral_constant<int, I>{}), ...);
-      }(std::make_integer_sequence<int, NB>{});
-    } else {
-      load_pieces<FA, BM, 0, L::NL>(ra, f, wave, ldn);
+      }
     }
     slot = slot + 1 == L::RD ? 0 : slot + 1;
-    f.sa = min(f.sa + L::AROW, (uint32_t)(nstep - 1) * L::AROW);
-    f.sw = min(f.sw + mx4::kBlk, (uint32_t)(nstep - 1) * mx4::kBlk);
   };
   for (int kt = 0; kt < nst; kt += 4) {
     step(std::integral_constant<int, 0>{}, kt);
@@ -215,122 +318,56 @@ __device__ __forceinline__ void tile_body(const Mx4Params &mp, const __amdgpu_bu
         for (int r = 0; r < 4; r++) v[g][r] = silu_fast(acc[i][g][r]) * acc[i][2 + g][r];
       mx4::store_h_block<FA>(v, on, (uint8_t *)p.out + row * mx4::code_bytes<FA>(p.I),
                              mp.out_scales + row * mx4::h_scale_stride(p.I), t.col0, q);
-    } else if (t.col0 < p.H) {
-      const float gate = *(const float *)(lds + L::RD * L::SLOT + 2 * L::SSLOT + (t.arow0 + m) * 4);
-      // H is a multiple of 128: a wave's 64 columns are all there or none
+    } else if (t.col0 < p.H) {  // H is a multiple of 128: a wave's 64 columns are all there or none
+      const float gate = *(const float *)(lds + L::ROW0 + (t.arow0 + m) * 4);
 #pragma unroll
       for (int g = 0; g < 4; g += 2)
         mx4::store_pair<BF16>(p.out, row * p.H + t.col0 + 16 * g, q, acc[i][g] * gate, acc[i][g + 1] * gate, on);
     }
   }
-  // Ends the stores' branches here.  Without it they end where the NB cases meet, which makes the loads' state, uniform
+  // Ends the stores' branches here.  Without it they end where the NB cases meet, which makes the ring's state, uniform
   // as it is, look different between lanes there: it would live in vector registers.
   asm volatile("; end of tile, %0 blocks" ::"n"(NB));
 }
 
 template <int MODE, int FA, bool BF16, int BM>
-__global__ __launch_bounds__(NTHR, 1) void ffn_mx4_kernel(Mx4Params mp) {
+__global__ __launch_bounds__(NTHR, 3) void ffn_mx4_kernel(Mx4Params mp) {  // three waves per SIMD
   using L = Lay<FA, BM>;
-  __shared__ __attribute__((aligned(1024))) char lds[L::RD * L::SLOT + 2 * L::SSLOT + L::ROWS];
-  const TileParams &p = mp.tp;
-  const int K = MODE == 0 ? p.H : p.I, Nw = MODE == 0 ? 2 * p.I : p.H;
-  const int nstep = K / 128;
-  // Workgroups go round-robin over the 8 XCDs: XCD x takes the x-th eighth of the list, its workgroups in
-  // turn, so that the tiles of one expert, which share operands, meet in one L2.
-  const int total = __builtin_amdgcn_readfirstlane(*mp.ntiles), per = gridDim.x >> 3, xcd = blockIdx.x & 7;
-  const int qt = total >> 3, rem = total & 7;
-  const int end = xcd * qt + min(xcd, rem) + qt + (xcd < rem ? 1 : 0);
-  int at = xcd * qt + min(xcd, rem) + (blockIdx.x >> 3);
-  if (at >= end) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3, n = lane & 15, q = lane >> 4;
-  const uint32_t arb = (uint32_t)mx4::code_bytes<FA>(K), ass = (uint32_t)mx4::h_scale_stride(K);
-  const uint32_t gc = (uint32_t)mx4::group_codes(K), gs = (uint32_t)mx4::group_scales(K);
-  const uint32_t arows = MODE == 0 ? (uint32_t)p.T : (uint32_t)p.R_cap;
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)p.a, (short)0, (int)(arows * arb), kRsrcWord3);
-  const __amdgpu_buffer_rsrc_t rsa =
-      __builtin_amdgcn_make_buffer_rsrc((void *)mp.a_scales, (short)0, (int)(arows * ass), kRsrcWord3);
-
-  // A tile's description, and once its rows' tokens are in LDS the bytes of this lane's activation pieces and scales
-  // (rows past the tile's end repeat its last).
-  typedef int i32x4_t __attribute__((ext_vector_type(4)));
-  const auto list = (const __attribute__((address_space(4))) i32x4_t *)(uintptr_t)mp.tiles;
-  auto describe = [&](Tile<FA, BM> &t, i32x4_t d) __attribute__((always_inline)) {
-    const int e = d.x, nt = d.y, r0 = d.z, rows = d.w & 0xffff, part = d.w >> 16;
-    const size_t wexp = (size_t)e * (Nw / 16);
-    t.rw = __builtin_amdgcn_make_buffer_rsrc((void *)((const char *)p.w + wexp * gc), (short)0, (int)(Nw / 16 * gc),
-                                             kRsrcWord3);
-    if (wave < L::SA) t.rs = rsa;
-    else t.rs = __builtin_amdgcn_make_buffer_rsrc((void *)(mp.w_scales + wexp * gs), (short)0, (int)(Nw / 16 * gs), kRsrcWord3);
-    auto group = [&](int i) -> uint32_t {  // weight group of LDS piece i
-      if constexpr (MODE == 0) return (uint32_t)(nt * 8 + (i >> 2) * 2 + (i & 1) + ((i >> 1) & 1) * (p.I / 16));
-      else return (uint32_t)min(nt * 16 + i, p.H / 16 - 1);
-    };
-#pragma unroll
-    for (int u = 0; u < 2; u++) t.off[L::NA + u] = group(wave + NWV * u) * gc + (uint32_t)lane * 16u;
-    t.col0 = MODE == 0 ? nt * 128 + wn * 32 : nt * BN + wn * 64;
+  __shared__ __attribute__((aligned(1024))) char lds[L::BYTES];
+  Share sh(mp);
+  if (sh.at >= sh.end) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave >= NC) {
+    load_tiles<MODE, FA, BM>(mp, sh, wave - NC, lane, lds);
+    return;
+  }
+  const int wm = wave >> 2, wn = wave & 3, K = MODE == 0 ? mp.tp.H : mp.tp.I;
+  if constexpr (MODE == 0) asm volatile("s_barrier" ::: "memory");  // the loading waves' extra one
+  i32x4_t d = sh.list[sh.at];
+  int slot = 0, sslot = 0;
+  for (;;) {
+    const int rows = d.w & 0xffff, part = d.w >> 16;
+    Tile t;
+    t.col0 = MODE == 0 ? d.y * 128 + wn * 32 : d.y * BN + wn * 64;
     t.arow0 = wm * part;
-    t.rbase = r0 + t.arow0;
+    t.rbase = d.z + t.arow0;
     t.mvalid = min(rows - t.arow0, part);
     t.nb = min(part >> 4, (max(t.mvalid, 1) + 15) >> 4);
-    t.r0 = r0;
-    t.rows = rows;
-    if (wave >= L::SA) t.soff = group(((wave - L::SA) & 3) * 4 + q) * gs + (uint32_t)n * 16u;
-  };
-  auto place = [&](Tile<FA, BM> &t) __attribute__((always_inline)) {
-    auto src = [&](int row) -> uint32_t {
-      const uint32_t r = MODE == 0 ? *(const uint32_t *)(lds + L::RD * L::SLOT + 2 * L::SSLOT + row * 4)
-                                   : (uint32_t)(t.r0 + min(row, t.rows - 1));
-      return min(r, arows - 1);
-    };
-#pragma unroll
-    for (int u = 0; u < L::NA; u++) {
-      const int b = (wave + NWV * u) % L::PIECES;
-      t.off[u] = src(FA == mx4::FP8 ? b * 8 + (lane & 7) : b * 16 + n) * arb +
-                 (uint32_t)(FA == mx4::FP8 ? lane >> 3 : q) * 16u;
-    }
-    if (wave < L::SA) t.soff = src(wave * 64 + lane) * ass;
-  };
-
-  Tile<FA, BM> cur, nxt;
-  describe(cur, list[at]);
-  if constexpr (MODE == 0) {
-    fetch_rows<MODE, FA, BM>(p, cur, wave, lane, lds + L::RD * L::SLOT + 2 * L::SSLOT);
-    asm volatile("s_waitcnt vmcnt(0)\ns_barrier" ::: "memory");
-  }
-  place(cur);
-  dma(cur.rs, lds + L::RD * L::SLOT + wave * 1024 - (wave >= L::SA + 4 ? 4096 : 0), cur.soff, 0);
-  Fetch<FA, BM> fetch;
-  fetch.start(cur);
-#pragma unroll
-  for (int d = 0; d < L::RD - 1; d++) {
-    load_pieces<FA, BM, 0, L::NL>(ra, fetch, wave, lds + d * L::SLOT);
-    fetch.sa = min(fetch.sa + L::AROW, (uint32_t)(nstep - 1) * L::AROW);
-    fetch.sw = min(fetch.sw + mx4::kBlk, (uint32_t)(nstep - 1) * mx4::kBlk);
-  }
-  int slot = 0, sslot = 0;
-  i32x4_t d = list[at + per < end ? at + per : at];
-  for (;;) {
-    const bool more = at + per < end;
-    at = more ? at + per : at;  // after the last tile: its own first steps again, which nobody reads
-    describe(nxt, d);
-    d = list[at + per < end ? at + per : at];
-    auto ready = [&]() __attribute__((always_inline)) { place(nxt); };
-#define MX4_BODY(NB) tile_body<MODE, FA, BF16, BM, NB>(mp, ra, cur, nxt, ready, fetch, K, wave, lane, slot, sslot, lds)
-    // the waves of a tile may take different cases: each issues the same loads and meets the same barriers
+    sh.at += sh.per;
+    if (sh.at < sh.end) d = sh.list[sh.at];
+#define MX4_BODY(NB) multiply<MODE, FA, BF16, BM, NB>(mp, t, K, wave, lane, slot, sslot, lds)
+    // the waves of a tile may take different cases: each meets the same barriers
     if constexpr (BM == 64) {
-      if (cur.nb == 1) MX4_BODY(1);
+      if (t.nb == 1) MX4_BODY(1);
       else MX4_BODY(2);
     } else {
-      if (cur.nb <= 2) MX4_BODY(2);
-      else if (cur.nb <= 4) MX4_BODY(4);
+      if (t.nb <= 2) MX4_BODY(2);
+      else if (t.nb <= 4) MX4_BODY(4);
       else MX4_BODY(6);
     }
 #undef MX4_BODY
-    if (!more) break;
-    cur = nxt;
+    if (sh.at >= sh.end) break;
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
 }
 
 // The tile list: expert by expert, then N tile by N tile, then M tile by M tile.  Workgroup ``part`` of ``parts``
