@@ -150,8 +150,9 @@ __device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw
 #pragma unroll
     for (int u = 0; u < L::NA; u++) {
       const int b = pw + NP * u;
-      t.off[u] = src(FA == mx4::FP8 ? b * 8 + (lane & 7) : b * 16 + n) * arb +
-                 (uint32_t)(FA == mx4::FP8 ? lane >> 3 : q) * 16u;
+      const int row = FA == mx4::FP8 ? b * 8 + (lane >> 3) : b * 16 + (lane >> 2);
+      const int chunk = FA == mx4::FP8 ? (lane & 7) ^ (row >> 1 & 7) : (lane & 3) ^ (row >> 2 & 3);
+      t.off[u] = src(row) * arb + (uint32_t)chunk * 16u;
     }
 #pragma unroll
     for (int u = 0; u < L::NS; u++)
@@ -257,9 +258,7 @@ __device__ __forceinline__ void multiply(const Mx4Params &mp, const Tile &t, int
     for (int g = 0; g < 4; g++) acc[i][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   // LDS bytes of this lane's operands inside a slot
   const uint32_t wbase = L::A_BYTES + (uint32_t)wn * 4096u + lane * 16u;
-  const uint32_t abase = FA == mx4::FP8
-                             ? (uint32_t)(t.arow0 >> 3) * 1024u + (uint32_t)(n >> 3) * 1024u + q * 128u + (n & 7) * 16u
-                             : (uint32_t)(t.arow0 >> 4) * 1024u + lane * 16u;
+  const uint32_t abase = (uint32_t)(t.arow0 + n) * L::AROW + (uint32_t)(FA == mx4::FP8 ? q ^ (n >> 1) : q ^ (n >> 2)) * 16u;
   uint32_t ws[4], as[NB];
   auto step = [&](auto JC, int kt) __attribute__((always_inline)) {
     constexpr int j = decltype(JC)::value;
@@ -277,9 +276,10 @@ __device__ __forceinline__ void multiply(const Mx4Params &mp, const Tile &t, int
       }
     }
     const uint32_t ab = abase + (uint32_t)slot * L::SLOT, wb = wbase + (uint32_t)slot * L::SLOT;
+    const uint32_t ab4 = ab ^ 64u;  // chunk q + 4
     auto act = [&](int i) __attribute__((always_inline)) {
       if constexpr (FA == mx4::FP8)
-        return mx4::piece8(*(const u32x4_t *)(lds + ab + i * 2048), *(const u32x4_t *)(lds + ab + (i * 2048 + 512)));
+        return mx4::piece8(*(const u32x4_t *)(lds + ab + i * 2048), *(const u32x4_t *)(lds + ab4 + i * 2048));
       else
         return mx4::piece4(*(const u32x4_t *)(lds + ab + i * 1024));
     };
