@@ -47,15 +47,25 @@ constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw buffer, 32-bit data format
 
 template <int FA, int BM>
 struct Lay {
-  static constexpr int AROW = FA == mx4::FP8 ? 128 : 64;     // activation bytes of a row and step
-  static constexpr int A_BYTES = BM * AROW, W_BYTES = BN * 64, SLOT = A_BYTES + W_BYTES;
+  // Activations come as 128 bytes of a row, a whole cache line: one step of E4M3, two of E2M1.  Of those, half the rows
+  // come with one step's loads and half with the next's, a step ahead of the weights.
+  static constexpr int PS = FA == mx4::FP8 ? 1 : 2;
+  static constexpr int A_BYTES = BM * 128, W_BYTES = BN * 64;
   static constexpr int SSLOT = BM * 16 + BN / 16 * 256;      // scales of four steps
   static constexpr int ROWS = BM * 4;                        // a word per row: tokens (gate/up) or gates (down)
-  static constexpr int FIT = (163840 - 2 * SSLOT - ROWS) / SLOT, RD = FIT < 6 ? FIT : 6;  // slots of the ring
-  static constexpr int SCALES = RD * SLOT, ROW0 = SCALES + 2 * SSLOT, BYTES = ROW0 + ROWS;
-  static constexpr int NA = A_BYTES / 1024 / NP, NL = NA + W_BYTES / 1024 / NP;  // loads per loading wave and step
+  static constexpr int a_slots(int rd) { return PS == 1 ? rd : rd / 2 + 1; }
+  static constexpr int bytes(int rd) { return a_slots(rd) * A_BYTES + rd * W_BYTES + 2 * SSLOT + ROWS; }
+  static constexpr int ring(int rd) { return bytes(rd) <= 163840 ? rd : ring(rd - PS); }
+  static constexpr int RD = ring(6), RA = a_slots(RD);       // slots of the rings of weights and activations
+  static constexpr int W0 = RA * A_BYTES, SCALES = W0 + RD * W_BYTES, ROW0 = SCALES + 2 * SSLOT, BYTES = ROW0 + ROWS;
+  static constexpr int NA = A_BYTES / 1024 / NP / PS, NW = W_BYTES / 1024 / NP, NL = NA + NW;  // loads per loading wave and step
   static constexpr int SA = BM / 64, SP = SA + 4, NS = (SP + NP - 1) / NP;  // scale pieces: activations, all; loads a wave
-  static_assert(RD >= 3 && RD <= 6 && A_BYTES % (1024 * NP) == 0, "two steps ahead; whole pieces");
+  static_assert(RD >= 3 && A_BYTES % (1024 * NP * PS) == 0, "two steps ahead; whole pieces");
+  // Steps that a tile takes.  A short one idles, so that loads reach only one tile ahead.
+  static __host__ __device__ int steps(int nstep) {
+    const int least = RD - 2 + PS, n = PS == 1 ? nstep : (nstep + 1) & ~1;
+    return n > least ? n : least;
+  }
   // Load u of a wave fetches scale piece scale_piece(wave, u); past the last one a weight piece again.
   static __device__ __forceinline__ int scale_piece(int pw, int u) {
     const int b = pw + NP * u;
@@ -90,7 +100,7 @@ struct Share {
 template <int FA, int BM>
 struct Source {
   __amdgpu_buffer_rsrc_t rw, rs[Lay<FA, BM>::NS];  // its expert's weights; the scales this wave fetches
-  uint32_t off[Lay<FA, BM>::NL];                   // this lane's bytes of its wave's pieces at step 0, activations first
+  uint32_t off[Lay<FA, BM>::NA * Lay<FA, BM>::PS], woff[Lay<FA, BM>::NW];  // this lane's bytes of its wave's pieces at step 0
   uint32_t soff[Lay<FA, BM>::NS];                  // and of its scales
   int r0, rows;
 };
@@ -100,7 +110,7 @@ __device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw
   using L = Lay<FA, BM>;
   const TileParams &p = mp.tp;
   const int K = MODE == 0 ? p.H : p.I, Nw = MODE == 0 ? 2 * p.I : p.H;
-  const int nstep = K / 128, nch = (nstep + 3) / 4, nst = max(nstep, L::RD - 1);
+  const int nstep = K / 128, nch = (nstep + 3) / 4, nst = L::steps(nstep);
   const int n = lane & 15, q = lane >> 4;
   const uint32_t arb = (uint32_t)mx4::code_bytes<FA>(K), ass = (uint32_t)mx4::h_scale_stride(K);
   const uint32_t gc = (uint32_t)mx4::group_codes(K), gs = (uint32_t)mx4::group_scales(K);
@@ -126,7 +136,7 @@ __device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw
       else return (uint32_t)min(nt * 16 + i, p.H / 16 - 1);
     };
 #pragma unroll
-    for (int u = 0; u < L::NL - L::NA; u++) t.off[L::NA + u] = group(pw + NP * u) * gc + (uint32_t)lane * 16u;
+    for (int u = 0; u < L::NW; u++) t.woff[u] = group(pw + NP * u) * gc + (uint32_t)lane * 16u;
 #pragma unroll
     for (int u = 0; u < L::NS; u++) {
       const int b = L::scale_piece(pw, u);
@@ -148,10 +158,8 @@ __device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw
       return min(r, arows - 1);
     };
 #pragma unroll
-    for (int u = 0; u < L::NA; u++) {
-      const int b = pw + NP * u;
-      const int row = FA == mx4::FP8 ? b * 8 + (lane >> 3) : b * 16 + (lane >> 2);
-      const int chunk = FA == mx4::FP8 ? (lane & 7) ^ (row >> 1 & 7) : (lane & 3) ^ (row >> 2 & 3);
+    for (int u = 0; u < L::NA * L::PS; u++) {
+      const int row = (pw + NP * u) * 8 + (lane >> 3), chunk = (lane & 7) ^ (row >> 1 & 7);
       t.off[u] = src(row) * arb + (uint32_t)chunk * 16u;
     }
 #pragma unroll
@@ -159,25 +167,39 @@ __device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw
       if (L::scale_piece(pw, u) < L::SA) t.soff[u] = src(L::scale_piece(pw, u) * 64 + lane) * ass;
   };
 
-  // The stream of loads runs RD - 1 steps ahead of the products, into the next tile when a tile's steps are all on
-  // their way.
+  // The stream of loads runs RD - 1 steps ahead of the products (E2M1 activations: RD), into the next tile when a
+  // tile's steps are all on their way.
   __amdgpu_buffer_rsrc_t rw;
-  uint32_t off[L::NL], sa = 0, sw = 0;  // bytes to the step's pieces in activations and weights
-  auto start = [&](const Source<FA, BM> &t) __attribute__((always_inline)) {
+  uint32_t off[L::NA * L::PS], woff[L::NW];
+  int as = 0, ws = 0, aslot = 0, wslot = 0;  // steps of activations and weights so far; the slots they go to
+  auto start_a = [&](const Source<FA, BM> &t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < L::NA * L::PS; u++) off[u] = t.off[u];
+    as = 0;
+  };
+  auto start_w = [&](const Source<FA, BM> &t) __attribute__((always_inline)) {
     rw = t.rw;
 #pragma unroll
-    for (int u = 0; u < L::NL; u++) off[u] = t.off[u];
-    sa = sw = 0;
+    for (int u = 0; u < L::NW; u++) woff[u] = t.woff[u];
+    ws = 0;
   };
-  auto load_step = [&](int slot) __attribute__((always_inline)) {
-    char *to = lds + slot * L::SLOT + pw * 1024;
+  auto load_a = [&]() __attribute__((always_inline)) {
+    const bool second = L::PS == 2 && (as & 1);
+    char *to = lds + aslot * L::A_BYTES + pw * 1024 + (second ? L::NA * NP * 1024 : 0);
+    const uint32_t at = (uint32_t)min(as, nstep - 1) / L::PS * 128u;
 #pragma unroll
-    for (int u = 0; u < L::NL; u++) {
-      if (u < L::NA) dma(ra, to + u * NP * 1024, off[u], sa);
-      else dma(rw, to + L::A_BYTES + (u - L::NA) * NP * 1024, off[u], sw);
-    }
-    sa = min(sa + L::AROW, (uint32_t)(nstep - 1) * L::AROW);
-    sw = min(sw + mx4::kBlk, (uint32_t)(nstep - 1) * mx4::kBlk);
+    for (int u = 0; u < L::NA; u++)  // the second half of an odd row's last line may lie behind the buffer: it reads 0
+      dma(ra, to + u * NP * 1024, (second ? off[(L::PS - 1) * L::NA + u] : off[u]) + at, 0);
+    if (L::PS == 1 || second) aslot = aslot + 1 == L::RA ? 0 : aslot + 1;
+    as++;
+  };
+  auto load_w = [&]() __attribute__((always_inline)) {
+    char *to = lds + L::W0 + wslot * L::W_BYTES + pw * 1024;
+    const uint32_t at = (uint32_t)min(ws, nstep - 1) * mx4::kBlk;
+#pragma unroll
+    for (int u = 0; u < L::NW; u++) dma(rw, to + u * NP * 1024, woff[u], at);
+    wslot = wslot + 1 == L::RD ? 0 : wslot + 1;
+    ws++;
   };
   auto load_scales = [&](const Source<FA, BM> &t, const Source<FA, BM> &other, bool same, int c, int sslot)
                          __attribute__((always_inline)) {
@@ -198,10 +220,14 @@ __device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw
   }
   place(cur);
   load_scales(cur, cur, true, 0, 0);
-  start(cur);
-#pragma unroll
-  for (int i = 0; i < L::RD - 1; i++) load_step(i);
-  int slot = 0, sslot = 0;
+  start_a(cur);
+  start_w(cur);
+  if constexpr (L::PS == 2) load_a();
+  for (int i = 0; i < L::RD - 1; i++) {
+    load_a();
+    load_w();
+  }
+  int sslot = 0;
   for (;;) {
     const bool more = sh.at + sh.per < sh.end;
     if (more) sh.at += sh.per;  // after the last tile: its own first steps again, which nobody reads
@@ -225,9 +251,10 @@ __device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw
           load_scales(cur, nxt, c + 1 < nch, c + 1, sslot);
         }
       }
-      if (kt == nst - (L::RD - 1)) start(nxt);
-      load_step(slot == 0 ? L::RD - 1 : slot - 1);  // the slot read in the step before
-      slot = slot + 1 == L::RD ? 0 : slot + 1;
+      if (kt == nst - (L::RD - 2 + L::PS)) start_a(nxt);
+      if (kt == nst - (L::RD - 1)) start_w(nxt);
+      load_a();  // into slots read in the step before, or earlier
+      load_w();
     }
     if (!more) break;
     cur = nxt;
@@ -244,21 +271,22 @@ struct Tile {
 // One tile: the K loop and the epilogue.  MODE 0: gate/up + SwiGLU -> h.  MODE 1: down -> gated rows.  NB: 16-row
 // blocks of this wave.
 template <int MODE, int FA, bool BF16, int BM, int NB>
-__device__ __forceinline__ void multiply(const Mx4Params &mp, const Tile &t, int K, int wave, int lane, int &slot,
-                                         int &sslot, char *lds) {
+__device__ __forceinline__ void multiply(const Mx4Params &mp, const Tile &t, int K, int wave, int lane, int &aslot,
+                                         int &wslot, int &sslot, char *lds) {
   using L = Lay<FA, BM>;
   const TileParams &p = mp.tp;
   const int n = lane & 15, q = lane >> 4, wn = wave & 3;
   const int nstep = K / 128, nch = (nstep + 3) / 4;
-  const int nst = max(nstep, L::RD - 1);  // a shorter tile idles, so that loads reach only one tile ahead
+  const int nst = L::steps(nstep);
   f32x4_t acc[NB][4];
 #pragma unroll
   for (int i = 0; i < NB; i++)
 #pragma unroll
     for (int g = 0; g < 4; g++) acc[i][g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // LDS bytes of this lane's operands inside a slot
-  const uint32_t wbase = L::A_BYTES + (uint32_t)wn * 4096u + lane * 16u;
-  const uint32_t abase = (uint32_t)(t.arow0 + n) * L::AROW + (uint32_t)(FA == mx4::FP8 ? q ^ (n >> 1) : q ^ (n >> 2)) * 16u;
+  // LDS bytes of this lane's operands inside their slots; of a row's eight 16-byte chunks c is at c ^ (row / 2 % 8),
+  // so that 16 rows at one chunk meet all banks
+  const uint32_t wbase = L::W0 + (uint32_t)wn * 4096u + lane * 16u;
+  const uint32_t abase = (uint32_t)(t.arow0 + n) * 128u + (uint32_t)(q ^ (n >> 1)) * 16u;
   uint32_t ws[4], as[NB];
   auto step = [&](auto JC, int kt) __attribute__((always_inline)) {
     constexpr int j = decltype(JC)::value;
@@ -275,13 +303,13 @@ __device__ __forceinline__ void multiply(const Mx4Params &mp, const Tile &t, int
         sslot ^= 1;
       }
     }
-    const uint32_t ab = abase + (uint32_t)slot * L::SLOT, wb = wbase + (uint32_t)slot * L::SLOT;
-    const uint32_t ab4 = ab ^ 64u;  // chunk q + 4
+    const uint32_t wb = wbase + (uint32_t)wslot * L::W_BYTES;
+    const uint32_t ab = abase + (uint32_t)aslot * L::A_BYTES, ab4 = ab ^ 64u;  // chunk q, chunk q + 4
     auto act = [&](int i) __attribute__((always_inline)) {
       if constexpr (FA == mx4::FP8)
         return mx4::piece8(*(const u32x4_t *)(lds + ab + i * 2048), *(const u32x4_t *)(lds + ab4 + i * 2048));
       else
-        return mx4::piece4(*(const u32x4_t *)(lds + ab + i * 1024));
+        return mx4::piece4(*(const u32x4_t *)(lds + (j & 1 ? ab4 : ab) + i * 2048));
     };
     if (kt < nstep) {
       v8i_t w[4], a[2];
@@ -296,7 +324,8 @@ __device__ __forceinline__ void multiply(const Mx4Params &mp, const Tile &t, int
         for (int g = 0; g < 4; g++) acc[i][g] = mx4::mfma<FA, j, j>(w[g], a[i & 1], acc[i][g], ws[g], as[i]);
       }
     }
-    slot = slot + 1 == L::RD ? 0 : slot + 1;
+    if (L::PS == 1 || (j & 1)) aslot = aslot + 1 == L::RA ? 0 : aslot + 1;
+    wslot = wslot + 1 == L::RD ? 0 : wslot + 1;
   };
   for (int kt = 0; kt < nst; kt += 4) {
     step(std::integral_constant<int, 0>{}, kt);
@@ -344,7 +373,7 @@ __global__ __launch_bounds__(NTHR, 3) void ffn_mx4_kernel(Mx4Params mp) {  // th
   const int wm = wave >> 2, wn = wave & 3, K = MODE == 0 ? mp.tp.H : mp.tp.I;
   if constexpr (MODE == 0) asm volatile("s_barrier" ::: "memory");  // the loading waves' extra one
   i32x4_t d = sh.list[sh.at];
-  int slot = 0, sslot = 0;
+  int aslot = 0, wslot = 0, sslot = 0;
   for (;;) {
     const int rows = d.w & 0xffff, part = d.w >> 16;
     Tile t;
@@ -355,7 +384,7 @@ __global__ __launch_bounds__(NTHR, 3) void ffn_mx4_kernel(Mx4Params mp) {  // th
     t.nb = min(part >> 4, (max(t.mvalid, 1) + 15) >> 4);
     sh.at += sh.per;
     if (sh.at < sh.end) d = sh.list[sh.at];
-#define MX4_BODY(NB) multiply<MODE, FA, BF16, BM, NB>(mp, t, K, wave, lane, slot, sslot, lds)
+#define MX4_BODY(NB) multiply<MODE, FA, BF16, BM, NB>(mp, t, K, wave, lane, aslot, wslot, sslot, lds)
     // the waves of a tile may take different cases: each meets the same barriers
     if constexpr (BM == 64) {
       if (t.nb == 1) MX4_BODY(1);
