@@ -1,26 +1,29 @@
 // Grouped expert FFN with MXFP4 weights (moe_grouped_ffn_mx4) for gfx950: the tile kernel.
 //
-// h = Q(silu(G) U), G, U = Wgu a; o = Wd h; y[t] = sum over t's rows of row_w o, in four launches: the
-// activation scales into lane order (a byte per 32 values), gate/up, down (rows scaled by their gate into the
-// workspace, in y's type) and the sum to token order, which adds a token's rows in slot order, so the result does
-// not depend on scheduling.
+// h = Q(silu(G) U), G, U = Wgu a; o = Wd h; y[t] = sum over t's rows of row_w o, in four launches: the tile lists
+// and the activation scales in lane order, gate/up, down (rows scaled by their gate into the workspace, in y's type)
+// and the sum to token order, which adds a token's rows in slot order, so the result does not depend on scheduling.
 //
-// A tile is up to BM rows of one expert (equal tiles per expert, rounded to 32 rows) x 256 weight rows, eight
-// waves as 2 (rows) x 4 (weight rows), K in steps of 128.  The weights are the first operand of
+// A tile is up to BM rows of one expert (equal tiles per expert, rounded to 32 rows) x 256 weight rows, K in steps of
+// 128.  Eight waves multiply, as 2 (rows) x 4 (weight rows); the weights are the first operand of
 // v_mfma_scale_f32_16x16x128_f8f6f4, so an accumulator holds four neighbouring output columns of one token: the
 // gate/up epilogue finds a 32-column block of h in four lanes, and the down epilogue stores neighbouring columns.
-// Both operands go from memory to LDS by buffer loads (no registers, no address arithmetic in the loop) into a
-// ring of RD slots, RD - 1 steps ahead; each slot holds them in the order in which the operand reads are
-// contiguous, 1 KB pieces that one wave's load fills: packed weight blocks as they are, eight rows x 128 bytes
-// of E4M3 rows, 16 rows x 64 bytes of E2M1 rows.  The scales of four steps (16 bytes a row) follow the same way, one
-// load per wave every four steps, into two slots of their own (loaded straight into registers by the lanes that
-// use them, four times the requests, they cost a third of the loop's time).  Every wave issues the same loads every
-// step, so the wait at the top of a step is a fixed count; one barrier per step.
+// Four more waves load, from memory straight to LDS, into rings that run two to five steps ahead: packed weight blocks
+// as they are, 128-byte lines of activation rows with their 16-byte chunks swizzled, and every four steps the scales
+// of four steps.  Waves of their own for this, because a wave that multiplies and loads stalls its products at every
+// load that finds the address unit busy, and waits for its stores before it can count its loads (6000 tokens with
+// E2M1 activations: gate/up 430 us without, 375 with).  Every loading wave issues the same loads every step, so its wait
+// at the top of a step is a fixed count; one barrier per step.
 //
-// One workgroup per compute unit works through a list of tiles (written by the launch before), because a tile's
-// own latencies -- finding it, its rows' tokens, the first loads, the stores -- were 14 us of the 43 to 54 us a gate/up
-// tile took: the next tile's description and tokens are fetched while a tile is computed, and its last RD - 1 steps
-// fetch the next tile's first ones.
+// One workgroup per compute unit works through a list of tiles (written by the launch before), and its loading
+// waves run into the next tile while the others finish one.
+//
+// What bounds it (32 experts x 384 rows, K = 8192, 4096 weight rows): with E4M3 activations 292 us or 2.8 PFLOP/s,
+// what a large fp8 library product reaches; the loads alone take 246 us, the products alone 239.  With E2M1 213 us or 3.9
+// PFLOP/s, loads alone 190, products alone 161: the path from L2 and beyond to LDS, 42 KB per us and compute unit of
+// the 47 that the Infinity Cache gives (135 when L2 holds everything).  Touching the weights' lines eight steps ahead
+// made it slower (254 us), and so did weights laid out tile by tile (227 us) and two workgroups of 128 weight rows on a
+// compute unit, which load more bytes per product (535 us instead of 440 for the 6000 tokens' gate/up).
 #include "mx4_common.h"
 
 #include <utility>
@@ -524,8 +527,9 @@ int max_mtiles(int T, int R_cap, int El, int BM) {
   const long long a = ((long long)R_cap + (long long)El * (BM - 1)) / BM, b = (long long)El * ceil_div_i(T, BM);
   return (int)(a < b ? a : b);
 }
-// Rows of a tile: 64 while an expert has at most 64 rows on average, else 192.
-int tile_rows(int R_cap, int El) { return ceil_div_i(R_cap, El) <= 64 ? 64 : 192; }
+// Rows of a tile: 64 while an expert has at most 40 rows on average, else 192.  128 experts, H = 4096, I = 1536, E4M3: 16
+// rows each 232 us (192-row tiles: 252), 32 rows 245 (261), 48 rows 277 (266), 64 rows 318 (282), 128 rows 437 (372).
+int tile_rows(int R_cap, int El) { return ceil_div_i(R_cap, El) <= 40 ? 64 : 192; }
 size_t list_bytes(int T, int R_cap, int El, int H, int I) {
   const int m = max_mtiles(T, R_cap, El, tile_rows(R_cap, El));
   return 256 + align_up((size_t)m * (I / 128 + ceil_div_i(H, BN)) * sizeof(int4), 256);

@@ -34,7 +34,8 @@ struct Half {
 };
 
 // How many waves share a gate/up tile when ``tiles`` of them exist: as few as keep about six waves per compute
-// unit busy (S is a power of two, at most one wave per 512 of the contraction).
+// unit busy (S is a power of two, at most one wave per 512 of the contraction).  Whole FFN of one token, eight experts of
+// 4096 x 1536: 23.9 us; 25.3 with half as many waves, 26.4 with twice; from 8 tokens on all three alike.
 __host__ __device__ __forceinline__ int split_for(int tiles, int H) {
   int S = 1;
   while (S < NW && tiles * S < 1536 && S * 512 < H) S *= 2;

@@ -193,6 +193,15 @@ def test_grouped_ffn_full_width(T, act):
     check_ffn(T, 8, 2, 4096, 1536, 0, 8, act, torch.bfloat16, seed=T)
 
 
+@pytest.mark.parametrize("act", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T", [600, 1300])
+@pytest.mark.parametrize("n", range(1, 11))
+def test_grouped_ffn_ring(n, T, act):
+    """Every length of the contraction from one step of 128 to ten, with several tiles for each workgroup, in 64-row
+    tiles and in larger ones: what one tile leaves in the ring the next must not see."""
+    check_ffn(T, 64, 2, 128 * n, 128 * (11 - n), 0, 64, act, torch.bfloat16, seed=n)
+
+
 @pytest.mark.parametrize("T", [40, 350])
 def test_grouped_ffn_normal_activations(T):
     """Normal MXFP8 activations.  The matrix cores drop up to 7 * 2^-13 of the largest product of each group of
