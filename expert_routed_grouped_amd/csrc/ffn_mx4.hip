@@ -395,6 +395,7 @@ __global__ __launch_bounds__(NTHR, 3) void ffn_mx4_kernel(Mx4Params mp) {  // th
     } else {
       if (t.nb <= 2) MX4_BODY(2);
       else if (t.nb <= 4) MX4_BODY(4);
+      else if (t.nb == 5) MX4_BODY(5);  // three tiles for 385 to 480 rows: 3% of 6000 tokens; a case of 3 gave nothing
       else MX4_BODY(6);
     }
 #undef MX4_BODY
