@@ -81,6 +81,11 @@ __device__ __forceinline__ void dma(const __amdgpu_buffer_rsrc_t &r, char *to, u
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, voff, soff, 0, 0);
 }
 
+// The same for lines that are read once.
+__device__ __forceinline__ void dma_once(const __amdgpu_buffer_rsrc_t &r, char *to, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, voff, soff, 0, 2);
+}
+
 // The workgroup's share of the tile list.  Workgroups go round-robin over the 8 XCDs: XCD x takes the x-th eighth of
 // the list, its workgroups in turn, so that the tiles of one expert, which share operands, meet in one L2.  The
 // list is read by scalar loads.
@@ -200,7 +205,12 @@ __device__ __forceinline__ void load_tiles(const Mx4Params &mp, Share sh, int pw
     char *to = lds + L::W0 + wslot * L::W_BYTES + pw * 1024;
     const uint32_t at = (uint32_t)min(ws, nstep - 1) * mx4::kBlk;
 #pragma unroll
-    for (int u = 0; u < L::NW; u++) dma(rw, to + u * NP * 1024, woff[u], at);
+    for (int u = 0; u < L::NW; u++) {
+      // Non-temporal where an expert has one tile of rows and its weights are read once (509 tokens: gate/up 143 -> 131 us,
+      // down 86 -> 81); where two tiles share them it costs (6000 tokens, E2M1: 320 -> 332 us, 231 -> 241).
+      if constexpr (BM == 64) dma_once(rw, to + u * NP * 1024, woff[u], at);
+      else dma(rw, to + u * NP * 1024, woff[u], at);
+    }
     wslot = wslot + 1 == L::RD ? 0 : wslot + 1;
     ws++;
   };
@@ -472,7 +482,8 @@ __global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int parts, i
 }
 
 // y[t] = sum of t's rows in slot order; a slot without a row (or with one out of range) adds nothing.  A thread sums
-// eight columns, the loads of eight slots in flight.
+// eight columns, the loads of eight slots in flight (509 tokens 18 -> 8 us) and non-temporal (6000 tokens 83 -> 70 us, 0.44
+// GB at 6.3 TB/s; the same for the stores of the down launch costs that 15 us).
 constexpr int SUM_THR = 256, SUM_COLS = 8;
 template <bool BF16>
 __global__ __launch_bounds__(SUM_THR) void sum_rows_kernel(const void *__restrict__ rows,
@@ -495,10 +506,10 @@ __global__ __launch_bounds__(SUM_THR) void sum_rows_kernel(const void *__restric
         if (r[j] < 0) continue;
         const size_t i = (size_t)r[j] * H + c;
         if constexpr (BF16) {
-          v[j][0] = *(const u32x4_t *)((const uint16_t *)rows + i);
+          v[j][0] = __builtin_nontemporal_load((const u32x4_t *)((const uint16_t *)rows + i));
         } else {
-          v[j][0] = *(const u32x4_t *)((const float *)rows + i);
-          v[j][1] = *(const u32x4_t *)((const float *)rows + i + 4);
+          v[j][0] = __builtin_nontemporal_load((const u32x4_t *)((const float *)rows + i));
+          v[j][1] = __builtin_nontemporal_load((const u32x4_t *)((const float *)rows + i + 4));
         }
       }
 #pragma unroll

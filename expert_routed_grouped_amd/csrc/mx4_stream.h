@@ -2,7 +2,8 @@
 // few-token layer).
 //
 // With a few rows per expert the work is one read of the active experts' weights, so the split is made for
-// bytes in flight, not for reuse.
+// bytes in flight, not for reuse; the weights are loaded non-temporally (64 tokens: gate/up 137 -> 128 us or 6.7 TB/s, down 75
+// -> 72).
 //
 // Gate/up: a wave takes 16 rows of an expert x 32 intermediate columns (one block of the quantised
 // intermediate): 32 gate and 32 up rows of the weights, through a ring of four 128-k steps (17 KB in flight per
@@ -74,7 +75,7 @@ __device__ __forceinline__ void gate_up_tile(const Half &p, int H, int I, int e,
     auto load = [&](int j, int c) __attribute__((always_inline)) {
       const int st = min(4 * c + j, nstep - 1);
 #pragma unroll
-      for (int g = 0; g < 4; g++) w[j][g] = *(const u32x4_t *)(wp[g] + (size_t)st * mx4::kBlk);
+      for (int g = 0; g < 4; g++) w[j][g] = __builtin_nontemporal_load((const u32x4_t *)(wp[g] + (size_t)st * mx4::kBlk));
       a[j] = mx4::act_frag<FA>(arow, st, q);
       as[j] = mx4::act_scale(asrow, st, q);
     };
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(NTHR) void down_sum_kernel(DownArgs a) {
     u.as = *(const uint32_t *)(a.p.a_s + ((size_t)beg + min(n & 7, rows - 1)) * hss + (size_t)c * 16 + 4 * q);
     const int last = nstep - 1;  // steps past the end are read again and not used
 #pragma unroll
-    for (int j = 0; j < 4; j++) u.w[j] = *(const u32x4_t *)(wp + (size_t)min(4 * c + j, last) * mx4::kBlk);
+    for (int j = 0; j < 4; j++) u.w[j] = __builtin_nontemporal_load((const u32x4_t *)(wp + (size_t)min(4 * c + j, last) * mx4::kBlk));
     const uint8_t *arow = a.p.a + ((size_t)beg + min(lane & 7, rows - 1)) * mx4::code_bytes<FA>(K);
 #pragma unroll
     for (int i = 0; i < NA; i++) {
