@@ -8,13 +8,15 @@
 // past the routing items waits for that count (for workgroups that drew earlier tickets, so they run; the wait is
 // bounded all the same).  Then every workgroup takes the top k of every token and groups the assignments for
 // itself, in LDS, rather than wait for one that does it and hands it out (a hand-over between workgroups on
-// different XCDs costs about 5 us), the one with the first free ticket writes down what launch 2 needs, and all share the gate/up
-// tiles.
+// different XCDs costs about 5 us; one token 52 -> 37 us), the one with the first free ticket writes down what
+// launch 2 needs, and all share the gate/up tiles.
 //
-// What bounds it: at one token the chain, H dependent additions whose order is the routing contract (about 3 ns
-// each), then the weights' bytes.  Against instruction issue the chain has the packed fp32 router (no unpacking)
+// What bounds it: at one token the chain, H dependent additions whose order is the routing contract (3.0 ns each),
+// then the weights' bytes.  Against instruction issue the chain has the packed fp32 router (no unpacking)
 // and its x operand broadcast inside rows of 16 lanes by the FMA itself (DPP), so 16 steps cost 16 FMAs, four loads
-// and one LDS read: 16 us of 4096 steps.  (Touching the matrix beforehand with the idle waves made it slower, 23 us.)
+// and one LDS read: 16 us of 4096 steps (12.4 for the FMAs alone, 10.2 without DPP).  Touching the matrix beforehand
+// with the idle waves made it slower, 23 us.  Launch 1 takes 37 us for one token of 128 experts of 4096 x 1536, top 8,
+// 63 for five, 142 for 24.
 #include "mx4_stream.h"
 #include "route_dev.h"
 

@@ -192,7 +192,7 @@ size_t ffn_mx4_ws_bytes(int T, int R_cap, int El, int H, int I, int y_bf16);
 hipError_t launch_ffn_mx4(const FfnMx4Args &a, hipStream_t s);
 // Weight-streaming path for few rows per expert (ffn_mx4_stream.hip), T <= kMx4StreamMaxT: h and its scales into
 // ``h`` / ``hs``, then the down half, which also sums to token order; launch_down_sum_mx4 is that half alone.
-// (Beyond, a tile kernel: 128 experts of 4096 x 1536, top 8, 64 tokens 210 us this way, 65 by tiles 225.)
+// (Beyond, a tile kernel: 128 experts of 4096 x 1536, top 8, 64 tokens 201 us this way, 65 by tiles 206.)
 constexpr int kMx4StreamMaxT = 64;
 hipError_t launch_ffn_mx4_stream(const FfnMx4Args &a, uint8_t *h, uint8_t *hs, hipStream_t s);
 hipError_t launch_down_sum_mx4(const FfnMx4Args &a, const uint8_t *h, const uint8_t *hs, hipStream_t s);

@@ -2,8 +2,8 @@
 // few-token layer).
 //
 // With a few rows per expert the work is one read of the active experts' weights, so the split is made for
-// bytes in flight, not for reuse; the weights are loaded non-temporally (64 tokens: gate/up 137 -> 128 us or 6.7 TB/s, down 75
-// -> 72).
+// bytes in flight, not for reuse, and the weights are loaded non-temporally (64 tokens, 128 experts of 4096 x 1536:
+// gate/up 137 -> 128 us or 6.7 TB/s, down 75 -> 72 us).
 //
 // Gate/up: a wave takes 16 rows of an expert x 32 intermediate columns (one block of the quantised
 // intermediate): 32 gate and 32 up rows of the weights, through a ring of four 128-k steps (17 KB in flight per
@@ -12,9 +12,9 @@
 //
 // Down: one workgroup owns 16 output columns for every token; its waves take the experts' tiles of 8 rows in
 // turn (few rows per expert leave most of a 16-row operand empty; eight rows load in full lines and reach their
-// lanes through LDS, which took the 64-token case from 88 to 75 us), add gate * o into a sum per wave, token and column in LDS, and the sums are joined in wave order at the
-// end.  Every byte of the down weights is read by one workgroup, nothing is added atomically, and y is
-// written once, rounded once.
+// lanes through LDS, 88 -> 75 us), add gate * o into a sum per wave, token and column in LDS, and the sums are
+// joined in wave order at the end.  Every byte of the down weights is read by one workgroup, nothing is added
+// atomically, and y is written once, rounded once.
 #pragma once
 #include "mx4_common.h"
 

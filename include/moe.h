@@ -12,7 +12,9 @@
  *
  * plus moe_route_dispatch (the first two calls of a decode batch in one
  * launch), moe_decode_layer (all four of a decode batch in one launch), moe_shared_expert (an always-active expert added to y), the W8A8
- * MXFP8 variant of the expert FFN (moe_quantize_mx, moe_grouped_ffn_mx) and
+ * MXFP8 variant of the expert FFN (moe_quantize_mx, moe_grouped_ffn_mx), MXFP4
+ * experts (moe_quantize_mx4, moe_dequantize_mx, moe_pack_mx4, moe_grouped_ffn_mx4,
+ * and moe_decode_layer_mx4, a few tokens' whole layer in two launches) and
  * moe_pack_weights / moe_pack_router (one-time reorderings of resident expert
  * and router weights for faster reads), and moe_grouped_ffn_noalloc (the expert
  * FFN for callers that cannot allocate a workspace).
