@@ -415,7 +415,8 @@ __global__ __launch_bounds__(NTHR, 3) void ffn_mx4_kernel(Mx4Params mp) {  // th
 
 // The tile list: expert by expert, then N tile by N tile, then M tile by M tile.  Workgroup ``part`` of ``parts``
 // writes its share; each counts the M tiles of all experts for itself (a hand-over costs more than El loads do).  One
-// workgroup writing all of it, a wave an expert, took 27 us.  smem: El + 1 ints, the first M tile of each expert.
+// workgroup writing all of it, a wave an expert, took 27 us, this 5.  cap: M tiles at most, as the workspace has room
+// for.  smem: El + 1 ints, the first M tile of each expert.
 template <int BM>
 __device__ void list_tiles(const TileParams &p, int NT, int cap, int part, int parts, int4 *out, int *count, int *smem) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -430,13 +431,13 @@ __device__ void list_tiles(const TileParams &p, int NT, int cap, int part, int p
     for (int b = 0; b < p.El; b += 64) {
       const int t = b + lane < p.El ? smem[b + lane] : 0;
       const int incl = ffn::wave_incl_scan_i(t, lane);
-      if (b + lane < p.El) smem[b + lane] = n0 + incl - t;
-      n0 += __shfl(incl, 63, 64);
+      if (b + lane < p.El) smem[b + lane] = min(n0 + incl - t, cap);  // cap: whatever the offsets say
+      n0 = min(n0 + __shfl(incl, 63, 64), cap);
     }
     if (lane == 0) smem[p.El] = n0;
   }
   __syncthreads();
-  const int n = (int)min((long long)smem[p.El] * NT, (long long)cap);
+  const int n = smem[p.El] * NT;
   if (part == 0 && threadIdx.x == 0) *count = n;
   for (int i = part * blockDim.x + threadIdx.x; i < n; i += parts * blockDim.x) {
     int e = 0;  // the last expert whose tiles start at or before i (an expert without tiles starts where the next does)
@@ -456,14 +457,14 @@ __device__ void list_tiles(const TileParams &p, int NT, int cap, int part, int p
 // activation scales [T, K/32] into lane order: dword q of piece c of a row has the scales 16c + 4j + q, j = 0 .. 3 (0
 // past the end of the row).
 template <int BM>
-__global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int parts, int gcap, int dcap, int4 *gtiles,
+__global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int parts, int cap, int4 *gtiles,
                                                       int4 *dtiles, int *counts, const uint8_t *__restrict__ s,
                                                       uint32_t *__restrict__ out) {
   if ((int)blockIdx.x < 2 * parts) {
     __shared__ int smem[1024 + 1];
     const int part = blockIdx.x >> 1;
-    if (blockIdx.x & 1) list_tiles<BM>(p, (p.H + BN - 1) / BN, dcap, part, parts, dtiles, counts + 1, smem);
-    else list_tiles<BM>(p, p.I / 128, gcap, part, parts, gtiles, counts, smem);
+    if (blockIdx.x & 1) list_tiles<BM>(p, (p.H + BN - 1) / BN, cap, part, parts, dtiles, counts + 1, smem);
+    else list_tiles<BM>(p, p.I / 128, cap, part, parts, gtiles, counts, smem);
     return;
   }
   const int K = p.H, kb = K / 32, dw = (K + 511) / 512 * 4, b0 = blockIdx.x - 2 * parts;
@@ -540,7 +541,8 @@ int max_mtiles(int T, int R_cap, int El, int BM) {
   return (int)(a < b ? a : b);
 }
 // Rows of a tile: 64 while an expert has at most 40 rows on average, else 192.  128 experts, H = 4096, I = 1536, E4M3: 16
-// rows each 232 us (192-row tiles: 252), 32 rows 245 (261), 48 rows 277 (266), 64 rows 318 (282), 128 rows 437 (372).
+// rows each 218 us (192-row tiles: 246), 32 rows 230 (261), 40 rows 234 (259), 48 rows 259 (261), 64 rows 350 (274), 128
+// rows 492 (349).
 int tile_rows(int R_cap, int El) { return ceil_div_i(R_cap, El) <= 40 ? 64 : 192; }
 size_t list_bytes(int T, int R_cap, int El, int H, int I) {
   const int m = max_mtiles(T, R_cap, El, tile_rows(R_cap, El));
@@ -564,10 +566,10 @@ hipError_t launch_tiles(const FfnMx4Args &a, hipStream_t s) {
   p.tp.R_cap = a.R_cap;
   p.tp.T = a.T;
   const long long dwords = (long long)a.T * (mx4::h_scale_stride(a.H) / 4);
-  const int gcap = mt * ntg, dcap = mt * ntd, most = gcap > dcap ? gcap : dcap;
+  const int most = mt * (ntg > ntd ? ntg : ntd);
   const int parts = most < 64 * 256 ? ceil_div_i(most, 256) : 64;
   hipLaunchKernelGGL(prepare_kernel<BM>, dim3(2 * parts + (unsigned)(dwords < (1 << 20) ? (dwords + 255) / 256 : 4096)),
-                     dim3(256), 0, s, p.tp, parts, gcap, dcap, gtiles, dtiles, counts, a.a_s, (uint32_t *)as);
+                     dim3(256), 0, s, p.tp, parts, mt, gtiles, dtiles, counts, a.a_s, (uint32_t *)as);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   Mx4Params g = p;
