@@ -427,7 +427,8 @@ def decode_layer_error_word(workspace: torch.Tensor) -> int:
 
 # ---- MXFP4 (include/moe.h, the *_mx4 calls) ----
 # The C ABI cannot see buffer sizes, so the shape, type and device of every tensor are checked here.  A call is short
-# next to what Python adds to it: one pass over each argument, raw addresses and streams.
+# next to what Python adds to it: one pass over each argument, raw addresses and streams.  Tensors a call allocates
+# belong to the stream it runs on (``stream``, or the device's current one).
 def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, device):
     """Address of a contiguous GPU tensor of this type, shape and device (None stays None)."""
     if t is None:
@@ -468,6 +469,17 @@ class _On:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """What a call allocates itself comes from the pool of the stream it runs on: memory of another stream's pool may
+    have work of that stream ahead of it, or be handed out again while this call still runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _out_dtype(dtype) -> int:
     if dtype == torch.bfloat16:
         return MOE_BF16
@@ -482,9 +494,9 @@ def moe_quantize_mx4(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scal
     rows, K = x.shape
     dt, dev, u8 = _out_dtype(x.dtype), x.device, torch.uint8
     if codes is None:
-        codes = torch.empty((rows, K // 2), dtype=u8, device=dev)
+        codes = _new((rows, K // 2), u8, dev, stream)
     if scales is None:
-        scales = torch.empty((rows, K // 32), dtype=u8, device=dev)
+        scales = _new((rows, K // 32), u8, dev, stream)
     args = (_arg(x, "x", x.dtype, (rows, K), dev), dt, rows, K, _arg(codes, "codes", u8, (rows, K // 2), dev),
             _arg(scales, "scales", u8, (rows, K // 32), dev))
     with _On(dev) as on:
@@ -502,7 +514,7 @@ def moe_dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, out: Optional[t
     fp4 = codes.shape[1] == K // 2
     if out is None:
         _out_dtype(dtype)
-        out = torch.empty((rows, K), dtype=dtype, device=dev)
+        out = _new((rows, K), dtype, dev, stream)
     args = (_arg(codes, "codes", u8, (rows, K // 2 if fp4 else K), dev),
             _arg(scales, "scales", u8, (rows, K // 32), dev), MOE_MXFP4 if fp4 else MOE_MXFP8, rows, K,
             _arg(out, "out", out.dtype, (rows, K), dev), _out_dtype(out.dtype))
@@ -521,8 +533,8 @@ def moe_pack_mx4(codes: torch.Tensor, scales: torch.Tensor, stream=None):
                        _arg(scales, "scales", u8, (*lead, N, K // 32), dev))
     if N % 16 != 0 or K % 128 != 0:
         raise MoEError("moe_pack_mx4", -2, "N must be a multiple of 16 and K of 128")
-    pc = torch.empty((*lead, N // 16, K // 128, 1024), dtype=u8, device=dev)
-    ps = torch.empty((*lead, N // 16, (K + 511) // 512, 256), dtype=u8, device=dev)
+    pc = _new((*lead, N // 16, K // 128, 1024), u8, dev, stream)
+    ps = _new((*lead, N // 16, (K + 511) // 512, 256), u8, dev, stream)
     with _On(dev) as on:
         _check("moe_pack_mx4", lib().moe_pack_mx4(pcodes, pscales, (lead[0] if lead else 1) * N, K, pc.data_ptr(),
                                                   ps.data_ptr(), on.stream(stream)))
@@ -568,10 +580,10 @@ def moe_grouped_ffn_mx4(a_codes: torch.Tensor, a_scales: torch.Tensor, offsets: 
         raise ValueError(f"row_token and row_w must hold T * min(k, E_loc) = {T * min(k, El)} entries")
     if y is None:
         _out_dtype(dtype)
-        y = torch.empty((T, H), dtype=dtype, device=dev)
+        y = _new((T, H), dtype, dev, stream)
     ydt = _out_dtype(y.dtype)
     if workspace is None:
-        workspace = torch.empty(moe_ffn_mx4_workspace_size(T, k, El, H, I, ydt), dtype=u8, device=dev)
+        workspace = _new((moe_ffn_mx4_workspace_size(T, k, El, H, I, ydt),), u8, dev, stream)
     args = (_arg(a_codes, "a_codes", u8, (T, H // 2 if fp4 else H), dev), _arg(a_scales, "a_scales", u8, (T, H // 32), dev),
             MOE_MXFP4 if fp4 else MOE_MXFP8, _arg(offsets, "offsets", i32, (El + 1,), dev),
             _arg(row_token, "row_token", i32, row_token.shape, dev), _arg(row_w, "row_w", torch.float32, row_w.shape, dev),
@@ -605,12 +617,12 @@ def moe_decode_layer_mx4(x: torch.Tensor, w_router_packed: torch.Tensor, bias: O
     if El != e_end - e_begin:
         raise ValueError(f"weights hold {El} experts, [{e_begin}, {e_end}) has {e_end - e_begin}")
     if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_ids = _new((T, k), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=f32, device=dev)
+        topk_w = _new((T, k), f32, dev, stream)
     if y is None:
         _out_dtype(dtype)
-        y = torch.empty((T, H), dtype=dtype, device=dev)
+        y = _new((T, H), dtype, dev, stream)
     args = (_arg(x, "x", torch.bfloat16, (T, H), dev), _arg(w_router_packed, "w_router_packed", f32, (H // 4, E, 4), dev),
             _arg(bias, "bias", f32, (E,), dev), T, H, E, k, e_begin, e_end, I, *w,
             _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev), _arg(topk_w, "topk_w", f32, (T, k), dev),

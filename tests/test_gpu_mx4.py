@@ -286,6 +286,27 @@ def test_grouped_ffn_graph_and_stream(T):
         assert torch.equal(got, y)
 
 
+@pytest.mark.parametrize("T", [30, 333])
+def test_grouped_ffn_own_buffers_on_a_stream(T):
+    """What a call on another stream allocates is not handed to the current stream while the call still runs."""
+    s = setup(T, 8, 2, 384, 256, 0, 8, seed=11)
+    p = moe.moe_permute(s["ids"], s["gates"], 8, 0, 8)
+    args = (p["offsets"], p["row_token"], p["row_w"], p["token_row"], s["wgu"], s["wd"])
+    want = moe.moe_grouped_ffn_mx4(*moe.moe_quantize_mx4(s["x"]), *args)
+    n = moe.moe_ffn_mx4_workspace_size(T, 2, 8, 384, 256, moe.MOE_BF16)
+    side = torch.cuda.Stream()
+    for use in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        a, sc = moe.moe_quantize_mx4(s["x"], stream=use)
+        y = moe.moe_grouped_ffn_mx4(a, sc, *args, stream=use)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        torch.cuda.current_stream().synchronize()
+        side.synchronize()
+        assert torch.equal(y, want), junk[0][0]
+
+
 def test_grouped_ffn_empty_batch():
     s = setup(1, 4, 2, 256, 128, 0, 4, seed=10)
     e = lambda *shape, dt=torch.uint8: torch.empty(shape, dtype=dt, device=DEV)  # noqa: E731
