@@ -163,19 +163,33 @@ __device__ __forceinline__ int group_all(const Params &p, const Groups &g, bool 
   if (staged)
     for (int i = threadIdx.x; i < p.T * 16 * EC; i += NTHR) *((f32x4_t *)scratch + i) = *((const f32x4_t *)p.logits + i);
   __syncthreads();
-  for (int t = wave; t < p.T; t += NW) {
-    int e;
-    float w;
-    rt::topk_lane<EC>((staged ? scratch : p.logits) + (size_t)t * 64 * EC, p.E, p.k, lane, e, w);
-    if (lane < p.k) {
+  // A wave's tokens are wave, wave + NW, ...; four at a time when it has more than one (64 tokens, 32 local experts:
+  // 83.5 -> 80 us).
+  auto pick = [&](auto NC, int t0) __attribute__((always_inline)) {
+    constexpr int N = decltype(NC)::value;
+    const float *l[N];
+    int e[N];
+    float w[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) l[i] = (staged ? scratch : p.logits) + (size_t)min(t0 + i * NW, p.T - 1) * 64 * EC;
+    rt::topk_lanes<EC, N>(l, p.E, p.k, lane, e, w);
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int t = t0 + i * NW;
+      if (lane >= p.k || t >= p.T) continue;
       if (write) {
-        p.ids[(size_t)t * p.k + lane] = e;
-        p.gates[(size_t)t * p.k + lane] = w;
+        p.ids[(size_t)t * p.k + lane] = e[i];
+        p.gates[(size_t)t * p.k + lane] = w[i];
       }
-      const int l = (unsigned)(e - p.lo) < (unsigned)p.El ? e - p.lo : -1;
-      if (l >= 0) atomicOr(g.set + l, 1ull << t);
-      g.sel[t * p.k + lane] = make_int2(l, __float_as_int(w));
+      const int el = (unsigned)(e[i] - p.lo) < (unsigned)p.El ? e[i] - p.lo : -1;
+      if (el >= 0) atomicOr(g.set + el, 1ull << t);
+      g.sel[t * p.k + lane] = make_int2(el, __float_as_int(w[i]));
     }
+  };
+  if (p.T <= NW) {
+    if (wave < p.T) pick(std::integral_constant<int, 1>{}, wave);
+  } else {
+    for (int t = wave; t < p.T; t += 4 * NW) pick(std::integral_constant<int, 4>{}, t);
   }
   __syncthreads();
   if (wave == 0) {

@@ -277,34 +277,60 @@ __device__ __forceinline__ void route_tokens(const void *__restrict__ x, const v
   }
 }
 
-// Top-k + gates of one token from its logits (wave-wide; every lane of the wave takes part): lane
-// j < k gets the j-th expert and its gate.  Lanes own experts lane + 64q.
+// Top-k + gates of N tokens from their logits (wave-wide; every lane of the wave takes part): lane
+// j < k gets each token's j-th expert and its gate.  Lanes own experts lane + 64q.  Several tokens share the time
+// that one token's reductions wait for each other.
+template <int EC, int N>
+__device__ __forceinline__ void topk_lanes(const float *const (&lgt)[N], int E, int k, int lane, int (&my_e)[N],
+                                           float (&gate)[N]) {
+  uint64_t key[N][EC];
+  float my_v[N], m[N];
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+#pragma unroll
+    for (int q = 0; q < EC; q++) {
+      int eq = q * 64 + lane;
+      key[i][q] = eq < E ? (((uint64_t)ord_key(lgt[i][eq]) << 32) | (uint32_t)~(uint32_t)eq) : 0ull;
+    }
+    my_v[i] = m[i] = 0.0f;
+    my_e[i] = 0;
+  }
+  for (int j = 0; j < k; j++) {
+    uint64_t best[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      best[i] = key[i][0];
+#pragma unroll
+      for (int q = 1; q < EC; q++) best[i] = key[i][q] > best[i] ? key[i][q] : best[i];
+      best[i] = wave_max_u64(best[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      const int es = (int)~(uint32_t)best[i];
+      const float vs = ord_val((uint32_t)(best[i] >> 32));
+#pragma unroll
+      for (int q = 0; q < EC; q++)
+        if (q * 64 + lane == es) key[i][q] = 0ull;
+      if (j == 0) m[i] = vs;
+      if (lane == j) { my_v[i] = vs; my_e[i] = es; }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    float u = lane < k ? expf(my_v[i] - m[i]) : 0.0f;
+    float sum = wave_sum_f32(u);
+    gate[i] = u / sum;
+  }
+}
+
 template <int EC>
 __device__ __forceinline__ void topk_lane(const float *lgt, int E, int k, int lane, int &my_e, float &gate) {
-  uint64_t key[EC];
-#pragma unroll
-  for (int q = 0; q < EC; q++) {
-    int eq = q * 64 + lane;
-    key[q] = eq < E ? (((uint64_t)ord_key(lgt[eq]) << 32) | (uint32_t)~(uint32_t)eq) : 0ull;
-  }
-  float my_v = 0.0f, m = 0.0f;
-  my_e = 0;
-  for (int j = 0; j < k; j++) {
-    uint64_t best = key[0];
-#pragma unroll
-    for (int q = 1; q < EC; q++) best = key[q] > best ? key[q] : best;
-    best = wave_max_u64(best);
-    const int es = (int)~(uint32_t)best;
-    const float vs = ord_val((uint32_t)(best >> 32));
-#pragma unroll
-    for (int q = 0; q < EC; q++)
-      if (q * 64 + lane == es) key[q] = 0ull;
-    if (j == 0) m = vs;
-    if (lane == j) { my_v = vs; my_e = es; }
-  }
-  float u = lane < k ? expf(my_v - m) : 0.0f;
-  float sum = wave_sum_f32(u);
-  gate = u / sum;
+  const float *const l[1] = {lgt};
+  int e[1];
+  float g[1];
+  topk_lanes<EC, 1>(l, E, k, lane, e, g);
+  my_e = e[0];
+  gate = g[0];
 }
 
 // The same, written to ids_t[0 .. k) and gates_t[0 .. k).
