@@ -127,7 +127,8 @@ class LayerBuffers:
 def convert_experts_mx4(dev: dict) -> dict:
     """Add the routed experts of ``dev`` (bf16 or fp32 weights, row-major) in MXFP4, quantised and packed, as
     ``dev["wgu_mx4"]`` and ``dev["wd_mx4"]``, and the packed router weight; run_layer with Mx4LayerBuffers reads
-    those.  Done once, like loading the weights; the originals may be dropped afterwards."""
+    those.  Done once, like loading the weights; the originals may be dropped afterwards.  The shared expert keeps its
+    weights, row-major or as a later pack_weights leaves them."""
     if dev.get("packed"):
         raise ValueError("convert the row-major weights, before pack_weights")
     for src, dst in (("w_gate_up", "wgu_mx4"), ("w_down", "wd_mx4")):
@@ -197,7 +198,8 @@ def _run_layer_mx4(dev: dict, bufs: Mx4LayerBuffers, stream) -> torch.Tensor:
                                 dev["wgu_mx4"], dev["wd_mx4"], y=bufs.y, workspace=bufs.workspace, stream=stream)
     if bufs.shared_ws is not None:
         moe.moe_shared_expert(dev["x"], dev["ws_gate_up"], dev["ws_down"], bufs.y, dev.get("ss_gate_up"),
-                              dev.get("ss_down"), workspace=bufs.shared_ws, stream=stream)
+                              dev.get("ss_down"), workspace=bufs.shared_ws, packed=bool(dev.get("packed", False)),
+                              stream=stream)
     return bufs.y
 
 

@@ -1,0 +1,41 @@
+"""GPU: layer.run_layer with MXFP4 experts (convert_experts_mx4, Mx4LayerBuffers) in the orders and on the streams that
+a program may use."""
+import pytest
+import torch
+
+import mx4_ref as R
+from expert_routed_grouped_amd import layer as L
+from expert_routed_grouped_amd import moe, synth
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def model(T, seed, I_s=0, act="bf16", H=512, E=24, I=256, **kw):
+    cfg = synth.LayerConfig("mx4", T=T, H=H, E=E, k=4, I=I, act=act, wdt=act, seed=seed, w_std=0.06, I_s=I_s, **kw)
+    return cfg, L.to_device(synth.make_inputs(cfg))
+
+
+@pytest.mark.parametrize("T,act", [(9, "mxfp8"), (9, "mxfp4"), (150, "mxfp8")])
+def test_shared_expert_with_packed_weights(T, act):
+    """convert_experts_mx4, then pack_weights, then run_layer gives what it gives before pack_weights.
+
+    The two runs of the shared expert may add in another order (fp32), so that a value of its h can round to the
+    neighbouring bf16: one step, 2^-7 of it; its down product and the sum into y are fp32 with at most I_s + 8 additions."""
+    I_s = 192
+    cfg, dev = model(T, 91, I_s=I_s, e_begin=4, e_end=20)
+    L.convert_experts_mx4(dev)
+    bufs = L.Mx4LayerBuffers(cfg, act=act, dtype=torch.float32)
+    want = L.run_layer(dev, bufs).clone()
+    gu, dn = dev["ws_gate_up"].double(), dev["ws_down"].double()
+    L.pack_weights(dev)
+    assert dev["packed"]
+    y = L.run_layer(dev, bufs)
+    a = dev["x"].double() @ gu.T
+    G, U = a[:, :I_s], a[:, I_s:]
+    shared = G * torch.sigmoid(G) * U
+    mag = shared.abs() @ dn.abs().T
+    bound = (2.0 ** -7 + 2 * (I_s + 8) * 2.0 ** -24) * mag + 2.0 ** -20 * want.abs()
+    assert bool(((y - want).double().abs() <= bound).all())
+    # and the bound would not let another layout pass
+    assert float(bound.square().mean().sqrt()) < 0.2 * float((shared @ dn.T).square().mean().sqrt())
