@@ -62,15 +62,48 @@ def pack_weights(dev: dict) -> dict:
     return dev
 
 
-def pack_router(dev: dict) -> dict:
+def pack_router(dev: dict, stream=None) -> dict:
     """Add the router weight in the layout of moe_pack_router (exact fp32, [H/4, E, 4]) as
     ``dev["w_router_packed"]``; decode-sized batches (moe_route_dispatch) then read it.  Done once,
-    like loading the weights; routing is bit-identical."""
+    like loading the weights; routing is bit-identical.  Runs on ``stream`` (or the current one);
+    run_layer orders its own reads after it, whatever stream it is given."""
     w = dev["w_router"]
     if w.shape[1] % 4 == 0 and (dev.get("w_router_packed") is None or not _router_pack_current(dev)):
-        dev["w_router_packed"] = moe.moe_pack_router(w)
+        if _capturing(w):
+            raise RuntimeError("pack the router before capturing: the copy would not be written until the graph runs")
+        packed = moe.moe_pack_router(w) if stream is None else moe.moe_pack_router(w, stream=stream)
+        dev["w_router_packed"] = packed
         dev["w_router_packed_src"] = (w.data_ptr(), w._version)
+        if getattr(packed, "is_cuda", False):
+            s, done = moe.torch_stream(stream, w.device), torch.cuda.Event()
+            done.record(s)
+            dev["w_router_packed_on"] = (s.cuda_stream, done)
     return dev
+
+
+def _capturing(t: torch.Tensor) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
+def _packed_router(dev: dict, stream) -> torch.Tensor:
+    """The packed router weight for a call on ``stream`` (None: the current one).  If ``w_router`` was replaced or edited
+    since, it is packed again, on that stream.  A stream other than the one it was packed on waits for the packing, and
+    a copy that is replaced is not freed before that stream has read it.  In a capture nothing is ordered (a capture
+    starts with the work before it done, and takes no event from outside), and a stale router is packed for the graph
+    alone, each time that it runs."""
+    w = dev["w_router"]
+    if dev.get("w_router_packed") is None or not _router_pack_current(dev):
+        if _capturing(w):
+            return moe.moe_pack_router(w, stream=stream)
+        pack_router(dev, stream)
+    packed = dev["w_router_packed"]
+    if getattr(packed, "is_cuda", False):
+        s = moe.torch_stream(stream, w.device)
+        at, done = dev["w_router_packed_on"]
+        if s.cuda_stream != at and not _capturing(packed):
+            s.wait_event(done)
+            packed.record_stream(s)
+    return packed
 
 
 def _router_pack_current(dev: dict) -> bool:
@@ -183,11 +216,9 @@ class Mx4LayerBuffers:
 def _run_layer_mx4(dev: dict, bufs: Mx4LayerBuffers, stream) -> torch.Tensor:
     cfg = bufs.cfg
     if bufs.one_call:
-        wp = dev.get("w_router_packed")
-        if wp is None or not _router_pack_current(dev):
-            wp = pack_router(dev)["w_router_packed"]
-        moe.moe_decode_layer_mx4(dev["x"], wp, dev["bias"], cfg.k, cfg.lo, cfg.hi, dev["wgu_mx4"], dev["wd_mx4"],
-                                 bufs.workspace, bufs.topk_ids, bufs.topk_w, bufs.y, stream=stream)
+        moe.moe_decode_layer_mx4(dev["x"], _packed_router(dev, stream), dev["bias"], cfg.k, cfg.lo, cfg.hi,
+                                 dev["wgu_mx4"], dev["wd_mx4"], bufs.workspace, bufs.topk_ids, bufs.topk_w, bufs.y,
+                                 stream=stream)
     else:
         p = bufs.perm
         moe.moe_route(dev["x"], dev["w_router"], dev["bias"], cfg.k, bufs.topk_ids, bufs.topk_w, stream=stream)
@@ -212,9 +243,7 @@ def run_layer(dev: dict, bufs, stream=None) -> torch.Tensor:
     cfg = bufs.cfg
     p = bufs.perm
     packed = bool(dev.get("packed", False))
-    wp = dev.get("w_router_packed")
-    if wp is not None and not _router_pack_current(dev):  # w_router replaced or edited: pack again
-        wp = pack_router(dev)["w_router_packed"]
+    wp = _packed_router(dev, stream) if dev.get("w_router_packed") is not None else None
     if bufs.dec_ws is not None:  # the whole layer in one launch
         moe.moe_decode_layer(dev["x"], dev["w_router"] if wp is None else wp, dev["bias"], cfg.k, cfg.E, cfg.lo, cfg.hi,
                              dev["w_gate_up"], dev["w_down"], dev.get("s_gate_up"), dev.get("s_down"), bufs.dec_ws,

@@ -149,6 +149,15 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def torch_stream(stream, device):
+    """``stream`` (a stream, its raw address or None: the device's current one) as a torch stream."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if hasattr(stream, "wait_event"):
+        return stream
+    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+
+
 def moe_version() -> int:
     return lib().moe_version()
 
@@ -356,7 +365,7 @@ def moe_pack_router(w_router: torch.Tensor, stream=None) -> torch.Tensor:
     """The router weight [E, H] (bf16 or fp32) as exact fp32 in the layout of moe_pack_router,
     [H/4, E, 4]; pass it to moe_route_dispatch with ``router_packed=True``."""
     E, H = w_router.shape
-    out = torch.empty((H // 4, E, 4), dtype=torch.float32, device=w_router.device)
+    out = _new((H // 4, E, 4), torch.float32, w_router.device, stream)
     _check("moe_pack_router", lib().moe_pack_router(_ptr(w_router), _dtype(w_router), E, H, _ptr(out),
                                                     _stream(stream)))
     return out
@@ -474,9 +483,7 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
     have work of that stream ahead of it, or be handed out again while this call still runs."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(torch_stream(stream, device)):
         return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -39,3 +39,57 @@ def test_shared_expert_with_packed_weights(T, act):
     assert bool(((y - want).double().abs() <= bound).all())
     # and the bound would not let another layout pass
     assert float(bound.square().mean().sqrt()) < 0.2 * float((shared @ dn.T).square().mean().sqrt())
+
+
+@pytest.mark.parametrize("mx4", [True, False])
+def test_edited_router_on_another_stream(mx4):
+    """w_router is edited, then the layer runs on a stream while the current one is busy, then on a third: every call
+    routes with the new weight, and the current stream's new tensors do not land on a copy that is still read."""
+    cfg, dev = model(9, 92)
+    if mx4:
+        L.convert_experts_mx4(dev)
+        bufs = [L.Mx4LayerBuffers(cfg) for _ in range(2)]
+    else:
+        L.pack_router(dev)
+        bufs = [L.LayerBuffers(cfg) for _ in range(2)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    for _ in range(4):
+        w = torch.randn(dev["w_router"].shape, device=DEV, generator=g) * 0.05
+        dev["w_router"].copy_(w)
+        want, gates = moe.moe_route(dev["x"], dev["w_router"], None, 4)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)  # the current stream is behind
+        L.run_layer(dev, bufs[0], stream=a)
+        L.run_layer(dev, bufs[1], stream=b)
+        junk = [torch.full((512 // 4, 24, 4), 1e9, device=DEV) for _ in range(4)]
+        torch.cuda.synchronize()
+        for f in bufs:
+            assert torch.equal(f.topk_ids, want) and torch.equal(f.topk_w, gates)
+        del junk
+
+
+def test_edited_router_captured():
+    """A graph captured while the packed router is stale packs it for itself; calls outside pack their own."""
+    cfg, dev = model(9, 93)
+    L.convert_experts_mx4(dev)
+    bufs, other = L.Mx4LayerBuffers(cfg), L.Mx4LayerBuffers(cfg)
+    L.run_layer(dev, bufs)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    new = lambda: torch.randn(dev["w_router"].shape, device=DEV, generator=g) * 0.05  # noqa: E731
+    dev["w_router"].copy_(new())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        L.run_layer(dev, bufs)
+    for _ in range(3):
+        want = moe.moe_route(dev["x"], dev["w_router"], None, 4)
+        L.run_layer(dev, other)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for f in (bufs, other):
+            assert torch.equal(f.topk_ids, want[0]) and torch.equal(f.topk_w, want[1])
+        assert torch.equal(bufs.y, other.y)
+        dev["w_router"].copy_(new())

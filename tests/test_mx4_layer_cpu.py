@@ -60,3 +60,127 @@ def test_shared_expert_is_told_of_packed_weights(rec, T, act, pack):
     L.run_layer(dev, bufs)
     (args, kw), = rec.named("moe_shared_expert")
     assert args[1] is dev["ws_gate_up"] and kw.get("packed", False) is pack
+
+
+# ------------------------------------------------------------------ the packed router and streams
+class FakeEvent:
+    def __init__(self, log):
+        self.log = log
+
+    def record(self, stream):
+        self.log.append(("record", stream.cuda_stream, self))
+
+
+class FakeStream:
+    def __init__(self, at, log):
+        self.cuda_stream, self.log = at, log
+
+    def wait_event(self, event):
+        self.log.append(("wait", self.cuda_stream, event))
+
+
+class FakePacked:
+    """What moe_pack_router returns on a GPU, as far as the layer looks at it."""
+    is_cuda = True
+
+    def __init__(self, log):
+        self.log = log
+
+    def record_stream(self, stream):
+        self.log.append(("keep", stream.cuda_stream, self))
+
+
+@pytest.fixture
+def streams(rec, monkeypatch):
+    """(log, a function that makes streams); stream 0 is the current one.  Packing notes the stream it runs on."""
+    log = []
+    of = lambda n: FakeStream(n, log)  # noqa: E731
+    current = of(0)
+    monkeypatch.setattr(torch.cuda, "Event", lambda: FakeEvent(log))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(L, "_capturing", lambda t: False)
+
+    def pack(w, stream=None):
+        log.append(("pack", 0 if stream is None else stream.cuda_stream, None))
+        return FakePacked(log)
+    monkeypatch.setattr(moe, "moe_pack_router", pack)
+    return log, of
+
+
+def old_model():
+    """A decode batch of the layer with bf16 experts and a packed router weight."""
+    cfg = LayerConfig("bf16 cpu", T=4, H=128, E=4, k=2, I=128)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    dev = dict(cfg=cfg, x=bf(4, 128), w_router=bf(4, 128), bias=None, w_gate_up=bf(4, 256, 128), w_down=bf(4, 128, 128))
+    return L.pack_router(dev), L.LayerBuffers(cfg, device="cpu")
+
+
+@pytest.fixture(params=["mx4", "bf16"])
+def routed(request, rec, streams):
+    """(log, streams, a layer with a packed router weight, its buffers, the router weights its calls got)."""
+    rec.replace("moe_route_dispatch")
+    rec.replace("moe_grouped_ffn")
+    if request.param == "mx4":
+        dev, bufs = model(4)
+        L.convert_experts_mx4(dev)
+        used = lambda: rec.named("moe_decode_layer_mx4")  # noqa: E731
+    else:
+        dev, bufs = old_model()
+        used = lambda: rec.named("moe_route_dispatch")  # noqa: E731
+    return (*streams, dev, bufs, used)
+
+
+def test_router_is_repacked_on_the_stream_of_the_call(routed):
+    log, stream, dev, bufs, used = routed
+    s = stream(7)
+    dev["w_router"].add_(1.0)
+    del log[:]
+    L.run_layer(dev, bufs, stream=s)
+    assert [e[:2] for e in log if e[0] == "pack"] == [("pack", 7)]
+    (args, kw), = used()
+    assert args[1] is dev["w_router_packed"] and kw["stream"] is s
+
+
+def test_router_packed_on_another_stream_is_waited_for_and_kept(routed):
+    """Packed on stream 0 (or, after an edit, on stream 7): a call on another stream waits for that, and the memory
+    is not handed out again before the call has read it; a call on the same stream needs neither."""
+    log, stream, dev, bufs, used = routed
+    a, b = stream(7), stream(9)
+    for s, at in ((b, 0), (a, None)):
+        del log[:]
+        if at is None:
+            dev["w_router"].add_(1.0)
+            L.run_layer(dev, bufs, stream=a)
+            del log[:]
+            s = b
+        packed = dev["w_router_packed"]
+        L.run_layer(dev, bufs, stream=s)
+        assert [e[:2] for e in log] == [("wait", 9), ("keep", 9)] and log[1][2] is packed
+    del log[:]
+    L.run_layer(dev, bufs, stream=a)
+    assert log == []
+
+
+def test_router_repacked_in_a_capture_stays_in_the_graph(routed, monkeypatch):
+    """A graph that is being captured packs a stale router for itself: its copy is not written before the graph runs,
+    so that calls outside must not take it for theirs."""
+    log, stream, dev, bufs, used = routed
+    before = dev["w_router_packed"]
+    dev["w_router"].add_(1.0)
+    monkeypatch.setattr(L, "_capturing", lambda t: True)
+    del log[:]
+    s = stream(7)
+    L.run_layer(dev, bufs, stream=s)
+    assert [e[:2] for e in log] == [("pack", 7)]
+    assert used()[-1][0][1] is not before and dev["w_router_packed"] is before
+    with pytest.raises(RuntimeError, match="captur"):
+        L.pack_router(dev)
+    monkeypatch.setattr(L, "_capturing", lambda t: False)
+    del log[:]
+    L.run_layer(dev, bufs, stream=s)
+    assert ("pack", 7) in [e[:2] for e in log] and used()[-1][0][1] is dev["w_router_packed"] is not before
+    # and a router that is up to date is used as it is, without an event from outside the capture
+    monkeypatch.setattr(L, "_capturing", lambda t: True)
+    del log[:]
+    L.run_layer(dev, bufs, stream=stream(9))
+    assert log == []
