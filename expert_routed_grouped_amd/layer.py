@@ -73,7 +73,7 @@ def pack_router(dev: dict, stream=None) -> dict:
             raise RuntimeError("pack the router before capturing: the copy would not be written until the graph runs")
         packed = moe.moe_pack_router(w) if stream is None else moe.moe_pack_router(w, stream=stream)
         dev["w_router_packed"] = packed
-        dev["w_router_packed_src"] = (w.data_ptr(), w._version)
+        dev["w_router_packed_src"] = (w, w.data_ptr(), w._version)
         if getattr(packed, "is_cuda", False):
             s, done = moe.torch_stream(stream, w.device), torch.cuda.Event()
             done.record(s)
@@ -108,9 +108,11 @@ def _packed_router(dev: dict, stream) -> torch.Tensor:
 
 def _router_pack_current(dev: dict) -> bool:
     """True while ``w_router_packed`` was made from the present ``w_router`` tensor, unmodified since
-    (same storage, same in-place version counter)."""
+    (the same tensor, storage and in-place version counter).  The tensor itself is held, so that no
+    other can come to have its address."""
     w = dev["w_router"]
-    return dev.get("w_router_packed_src") == (w.data_ptr(), w._version)
+    src = dev.get("w_router_packed_src")
+    return src is not None and src[0] is w and src[1:] == (w.data_ptr(), w._version)
 
 
 class LayerBuffers:

@@ -184,3 +184,20 @@ def test_router_repacked_in_a_capture_stays_in_the_graph(routed, monkeypatch):
     del log[:]
     L.run_layer(dev, bufs, stream=stream(9))
     assert log == []
+
+
+def test_router_replaced_at_the_same_address(rec):
+    """A new weight may get the memory of the one it replaces, with the same version count: it is packed all the same."""
+    import numpy as np
+    memory = np.zeros((4, 128), dtype=np.float32)
+    dev, bufs = model(4)
+    dev["w_router"] = torch.from_numpy(memory)
+    L.convert_experts_mx4(dev)
+    first = dev["w_router_packed"]
+    at = dev["w_router"].data_ptr()
+    memory[:] = 1.0
+    dev["w_router"] = torch.from_numpy(memory)
+    assert dev["w_router"].data_ptr() == at and dev["w_router"]._version == 0
+    L.run_layer(dev, bufs)
+    (args, _), = rec.named("moe_decode_layer_mx4")
+    assert args[1] is not first and bool((args[1] == 1).all())
