@@ -73,7 +73,7 @@ def pack_router(dev: dict, stream=None) -> dict:
             raise RuntimeError("pack the router before capturing: the copy would not be written until the graph runs")
         packed = moe.moe_pack_router(w) if stream is None else moe.moe_pack_router(w, stream=stream)
         dev["w_router_packed"] = packed
-        dev["w_router_packed_src"] = (w, w.data_ptr(), w._version)
+        dev["w_router_packed_src"] = (w, w.data_ptr(), _version(w))
         if getattr(packed, "is_cuda", False):
             s, done = moe.torch_stream(stream, w.device), torch.cuda.Event()
             done.record(s)
@@ -106,13 +106,18 @@ def _packed_router(dev: dict, stream) -> torch.Tensor:
     return packed
 
 
+def _version(t: torch.Tensor):
+    return None if t.is_inference() else t._version
+
+
 def _router_pack_current(dev: dict) -> bool:
     """True while ``w_router_packed`` was made from the present ``w_router`` tensor, unmodified since
     (the same tensor, storage and in-place version counter).  The tensor itself is held, so that no
-    other can come to have its address."""
+    other can come to have its address.  Edits of an inference tensor, which has no such counter, do not
+    show: replace the tensor instead."""
     w = dev["w_router"]
     src = dev.get("w_router_packed_src")
-    return src is not None and src[0] is w and src[1:] == (w.data_ptr(), w._version)
+    return src is not None and src[0] is w and src[1:] == (w.data_ptr(), _version(w))
 
 
 class LayerBuffers:

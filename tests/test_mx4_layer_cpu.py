@@ -201,3 +201,18 @@ def test_router_replaced_at_the_same_address(rec):
     L.run_layer(dev, bufs)
     (args, _), = rec.named("moe_decode_layer_mx4")
     assert args[1] is not first and bool((args[1] == 1).all())
+
+
+def test_router_made_in_inference_mode(rec):
+    """Weights loaded under torch.inference_mode have no version counter; replacing the tensor still shows."""
+    dev, bufs = model(4)
+    with torch.inference_mode():
+        dev["w_router"] = torch.zeros((4, 128), dtype=torch.bfloat16)
+    L.convert_experts_mx4(dev)
+    first = dev["w_router_packed"]
+    L.run_layer(dev, bufs)
+    assert rec.named("moe_decode_layer_mx4")[0][0][1] is first
+    with torch.inference_mode():
+        dev["w_router"] = torch.ones((4, 128), dtype=torch.bfloat16)
+    L.run_layer(dev, bufs)
+    assert bool((rec.named("moe_decode_layer_mx4")[1][0][1] == 1).all())
