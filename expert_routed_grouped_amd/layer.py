@@ -66,7 +66,8 @@ def pack_router(dev: dict, stream=None) -> dict:
     """Add the router weight in the layout of moe_pack_router (exact fp32, [H/4, E, 4]) as
     ``dev["w_router_packed"]``; decode-sized batches (moe_route_dispatch) then read it.  Done once,
     like loading the weights; routing is bit-identical.  Runs on ``stream`` (or the current one);
-    run_layer orders its own reads after it, whatever stream it is given."""
+    run_layer orders its own reads after it, whatever stream it is given.  A graph captured from run_layer
+    keeps the copy of its capture: capture again after a change of the router weight."""
     w = dev["w_router"]
     if w.shape[1] % 4 == 0 and (dev.get("w_router_packed") is None or not _router_pack_current(dev)):
         if _capturing(w):
@@ -89,8 +90,8 @@ def _packed_router(dev: dict, stream) -> torch.Tensor:
     """The packed router weight for a call on ``stream`` (None: the current one).  If ``w_router`` was replaced or edited
     since, it is packed again, on that stream.  A stream other than the one it was packed on waits for the packing, and
     a copy that is replaced is not freed before that stream has read it.  In a capture nothing is ordered (a capture
-    starts with the work before it done, and takes no event from outside), and a stale router is packed for the graph
-    alone, each time that it runs."""
+    starts with the work before it done, and takes no event from outside); the graph goes on reading the copy of that
+    time, which is kept for it, and a router that is stale then is packed for the graph alone, each time that it runs."""
     w = dev["w_router"]
     if dev.get("w_router_packed") is None or not _router_pack_current(dev):
         if _capturing(w):
@@ -100,7 +101,11 @@ def _packed_router(dev: dict, stream) -> torch.Tensor:
     if getattr(packed, "is_cuda", False):
         s = moe.torch_stream(stream, w.device)
         at, done = dev["w_router_packed_on"]
-        if s.cuda_stream != at and not _capturing(packed):
+        if _capturing(packed):
+            captured = dev.setdefault("w_router_packed_captured", [])
+            if not any(c is packed for c in captured):
+                captured.append(packed)
+        elif s.cuda_stream != at:
             s.wait_event(done)
             packed.record_stream(s)
     return packed

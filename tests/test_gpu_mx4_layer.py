@@ -93,3 +93,26 @@ def test_edited_router_captured():
             assert torch.equal(f.topk_ids, want[0]) and torch.equal(f.topk_w, want[1])
         assert torch.equal(bufs.y, other.y)
         dev["w_router"].copy_(new())
+
+
+def test_graph_keeps_its_router_copy():
+    """A graph captured with one router weight goes on routing with it after the weight was edited and packed again,
+    whatever was allocated since."""
+    cfg, dev = model(9, 94)
+    L.convert_experts_mx4(dev)
+    bufs, other = L.Mx4LayerBuffers(cfg), L.Mx4LayerBuffers(cfg)
+    L.run_layer(dev, bufs)
+    want = [t.clone() for t in (bufs.topk_ids, bufs.topk_w, bufs.y)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        L.run_layer(dev, bufs)
+    for _ in range(3):
+        dev["w_router"].mul_(-1.0)
+        L.run_layer(dev, other)
+        ids = moe.moe_route(dev["x"], dev["w_router"], None, 4)[0]
+        junk = [torch.full((512 // 4, 24, 4), 1e9, device=DEV) for _ in range(8)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(other.topk_ids, ids)
+        assert all(torch.equal(a, b) for a, b in zip(want, (bufs.topk_ids, bufs.topk_w, bufs.y)))
+        del junk

@@ -216,3 +216,25 @@ def test_router_made_in_inference_mode(rec):
         dev["w_router"] = torch.ones((4, 128), dtype=torch.bfloat16)
     L.run_layer(dev, bufs)
     assert bool((rec.named("moe_decode_layer_mx4")[1][0][1] == 1).all())
+
+
+def test_router_copy_of_a_graph_outlives_a_repack(rec, routed, monkeypatch):
+    """A captured call holds the address of the packed copy: packing again must not free what the graph reads."""
+    import weakref
+    log, stream, dev, bufs, used = routed
+
+    def edit_and_run():
+        dev["w_router"].add_(1.0)
+        L.run_layer(dev, bufs)
+        del rec.calls[:], log[:]  # they hold the copies too
+
+    copy = weakref.ref(dev["w_router_packed"])
+    monkeypatch.setattr(L, "_capturing", lambda t: True)
+    for _ in range(3):
+        L.run_layer(dev, bufs)
+    monkeypatch.setattr(L, "_capturing", lambda t: False)
+    edit_and_run()
+    assert copy() is not None and len(dev["w_router_packed_captured"]) == 1
+    unread = weakref.ref(dev["w_router_packed"])  # no graph reads this one
+    edit_and_run()
+    assert unread() is None
