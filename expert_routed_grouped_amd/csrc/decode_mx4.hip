@@ -81,10 +81,10 @@ __device__ __forceinline__ void route_item(const Params &p, int t, int c, int EP
     if (c == 0) {  // H is a multiple of 128: 16 neighbouring lanes loop together
       uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < 8; j++) m = max(m, mx4::abs_bits(f[j]));
+      for (int j = 0; j < 8; j++) m = max(m, mx_abs_bits(f[j]));
       m = max(m, (uint32_t)__shfl_xor((int)m, 1, 64));
       m = max(m, (uint32_t)__shfl_xor((int)m, 2, 64));
-      const uint32_t s = mx4::scale_of_bits<8>(m);
+      const uint32_t s = mx_scale_of_bits<8>(m);
       float u[8];
 #pragma unroll
       for (int j = 0; j < 8; j++) u[j] = ldexpf(f[j], 127 - (int)s);

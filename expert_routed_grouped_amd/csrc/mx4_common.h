@@ -73,16 +73,6 @@ __host__ __device__ __forceinline__ size_t h_scale_stride(int I) { return (size_
 // Place of block b (columns 32b ..) in its row.
 __device__ __forceinline__ int h_scale_pos(int b) { return (b & ~15) + (b & 3) * 4 + ((b >> 2) & 3); }
 
-// Scale byte of a block from the bit pattern of its largest magnitude (the maximum over bit patterns
-// orders NaN above infinity above every finite value).  EMAX: exponent of the format's largest power of
-// two (2 for E2M1, 8 for E4M3).
-template <int EMAX>
-__device__ __forceinline__ uint32_t scale_of_bits(uint32_t amax_bits) {
-  const int ef = (int)(amax_bits >> 23);
-  return ef == 255 ? 255u : (uint32_t)max(ef - EMAX, 0);
-}
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
 // E2M1 codes of a and b (already divided by the scale), a in the low half.  The packed conversion of
 // gfx950 rounds to nearest, ties to even, and saturates at 6 (checked over -8 .. 8 in steps of 1/512
 // and at every midpoint).
@@ -109,10 +99,10 @@ __device__ __forceinline__ void store_h_block(const float (&v)[2][4], bool on, u
 #pragma unroll
   for (int g = 0; g < 2; g++)
 #pragma unroll
-    for (int r = 0; r < 4; r++) m = max(m, abs_bits(v[g][r]));
+    for (int r = 0; r < 4; r++) m = max(m, mx_abs_bits(v[g][r]));
   m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
   m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-  const uint32_t s = scale_of_bits<FA == FP8 ? 8 : 2>(m);
+  const uint32_t s = mx_scale_of_bits<FA == FP8 ? 8 : 2>(m);
   const int ex = 127 - (int)s;
   if (!on) return;
 #pragma unroll

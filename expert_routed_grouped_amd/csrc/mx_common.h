@@ -5,11 +5,22 @@
 // one E8M0 scale byte s (value 2^(s-127)); each value is an OCP E4M3 code.
 // Block rule used here: s = clamp(floor(log2 amax) - 8 + 127, 0, 254) (s = 0 for
 // an all-zero block), code = E4M3 nearest to v / 2^(s-127), ties to even,
-// magnitudes >= 448 saturate to 448, sign bit kept.
+// magnitudes >= 448 saturate to 448, sign bit kept; a block that holds a NaN or an infinity gets
+// s = 255, so that all of it reads as NaN.
 #pragma once
 #include "common.h"
 
 #include <type_traits>
+
+// E8M0 scale byte of a block from the bit pattern of its largest magnitude (the maximum over bit patterns
+// orders NaN above infinity above every finite value; the floating-point maximum would drop NaN).  EMAX:
+// exponent of the format's largest power of two (2 for E2M1, 8 for E4M3).
+template <int EMAX>
+__device__ __forceinline__ uint32_t mx_scale_of_bits(uint32_t amax_bits) {
+  const int ef = (int)(amax_bits >> 23);
+  return ef == 255 ? 255u : (uint32_t)max(ef - EMAX, 0);
+}
+__device__ __forceinline__ uint32_t mx_abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // E8M0 scale byte of a block whose largest magnitude is amax (finite, >= 0): the
 // fp32 exponent field ef gives floor(log2 amax) = ef - 127 for normal amax, and

@@ -24,19 +24,19 @@ __global__ __launch_bounds__(256) void quantize_mx_kernel(const void *__restrict
       const f32x4_t a = *((const f32x4_t *)x + 2 * v), b = *((const f32x4_t *)x + 2 * v + 1);
       f[0] = a[0]; f[1] = a[1]; f[2] = a[2]; f[3] = a[3]; f[4] = b[0]; f[5] = b[1]; f[6] = b[2]; f[7] = b[3];
     }
-    float amax = 0.0f;
+    uint32_t amax = 0;
 #pragma unroll
-    for (int j = 0; j < 8; j++) amax = fmaxf(amax, fabsf(f[j]));
-    amax = fmaxf(amax, __shfl_xor(amax, 1, 64));
-    amax = fmaxf(amax, __shfl_xor(amax, 2, 64));
-    const uint32_t s = mx_scale_of(amax);
+    for (int j = 0; j < 8; j++) amax = max(amax, mx_abs_bits(f[j]));
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, 64));
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, 64));
+    const uint32_t s = mx_scale_of_bits<8>(amax);
     uint32_t lo = 0, hi = 0;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       lo |= e4m3_encode(ldexpf(f[j], 127 - (int)s)) << (8 * j);
       hi |= e4m3_encode(ldexpf(f[4 + j], 127 - (int)s)) << (8 * j);
     }
-    *((uint2 *)codes + v) = make_uint2(lo, hi);
+    *((uint2 *)codes + v) = s == 255 ? make_uint2(0, 0) : make_uint2(lo, hi);
     if ((v & 3) == 0) scales[v >> 2] = (uint8_t)s;
   }
 }

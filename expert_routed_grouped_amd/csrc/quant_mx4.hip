@@ -54,9 +54,9 @@ __global__ __launch_bounds__(256) void quantize_mx4_kernel(const u32x4_t *__rest
       for (int j = 0; j < V; j++) {
         if constexpr (BF16) f[j] = (j & 1) ? bf16_hi(r[u][j >> 1]) : bf16_lo(r[u][j >> 1]);
         else f[j] = __uint_as_float(r[u][j]);
-        m = max(m, mx4::abs_bits(f[j]));
+        m = max(m, mx_abs_bits(f[j]));
       }
-      const uint32_t s = mx4::scale_of_bits<2>(block_max<N>(m));
+      const uint32_t s = mx_scale_of_bits<2>(block_max<N>(m));
 #pragma unroll
       for (int j = 0; j < V; j++) f[j] = ldexpf(f[j], 127 - (int)s);
       if (v >= nvec) continue;

@@ -44,7 +44,8 @@
  *    detected on the host before anything is enqueued (then nothing ran).
  *    MOE_ERR_HIP means a launch failed (hipGetLastError after the launch).
  *    Faults inside kernels surface, as usual for HIP, at the next
- *    synchronisation of the stream.  NaN/Inf input values are not checked.
+ *    synchronisation of the stream.  NaN/Inf input values are not checked; the
+ *    quantising calls say what becomes of them.
  *  - Element types: MOE_F32 (float), MOE_BF16 (bfloat16 bit patterns, uint16),
  *    MOE_FP8_E4M3 (OCP E4M3 codes, uint8; only for expert weights, always with
  *    fp32 per-output-channel scales), MOE_MXFP8 (OCP microscaling: E4M3 codes,
@@ -309,6 +310,8 @@ int moe_pack_weights(const void *w, int w_dtype, int E, int N, int K, void *pack
  *   amax = max |v|;  s = amax == 0 ? 0 : clamp(floor(log2 amax) - 8 + 127, 0, 254)
  *   scales[r, b] = s;  codes[r, 32b+i] = E4M3 code nearest to v_i / 2^(s-127),
  *   ties to the even code, magnitudes >= 448 saturate to 448, sign bit kept.
+ *   A block that holds a NaN or an infinity gets s = 255 (the E8M0 NaN) and zero
+ *   codes: all of it reads as NaN, in moe_dequantize_mx and in the products.
  * x: rows x K, MOE_F32 or MOE_BF16; codes [rows, K] uint8; scales [rows, K/32]
  * uint8.  K must be a multiple of 32 and rows >= 0; x 16-byte aligned, codes
  * 8-byte aligned.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE,
