@@ -293,12 +293,12 @@ __device__ __forceinline__ void body(const MxParams &mp, const Src &src, int K,
           f32x4_t v[8];
 #pragma unroll
           for (int q = 0; q < 8; q++) v[q] = *(const f32x4_t *)(st + m * LS + 4 * q);
-          float amax = 0.0f;
+          uint32_t amax = 0;
 #pragma unroll
           for (int q = 0; q < 8; q++)
 #pragma unroll
-            for (int c = 0; c < 4; c++) amax = fmaxf(amax, fabsf(v[q][c]));
-          const uint32_t sc = mx_scale_of(amax);
+            for (int c = 0; c < 4; c++) amax = max(amax, mx_abs_bits(v[q][c]));
+          const uint32_t sc = mx_scale_of_bits<8>(amax);  // 255: NaN whatever the codes
           const int ex = 127 - (int)sc;
           u32x4_t w[2];
 #pragma unroll

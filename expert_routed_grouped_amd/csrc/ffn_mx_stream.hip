@@ -229,7 +229,7 @@ __global__ __launch_bounds__(64 * XWAVES) void ffn_mx_stream_kernel(MxsParams mp
       for (int r = 0; r < 16; r++) {
         const int m = mb * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
         const float hv = silu_fast(acc[mb][0][r]) * acc[mb][1][r];
-        const uint32_t sc = mx_scale_of(halfwave_amax(hv));
+        const uint32_t sc = mx_scale_of_bits<8>(halfwave_amax(hv));
         if (m < rows) {
           const size_t row = (size_t)(r0 + m);
           hq[row * p.I + col] = (uint8_t)e4m3_encode(ldexpf(hv, 127 - (int)sc));

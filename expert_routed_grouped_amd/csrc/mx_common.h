@@ -14,21 +14,14 @@
 
 // E8M0 scale byte of a block from the bit pattern of its largest magnitude (the maximum over bit patterns
 // orders NaN above infinity above every finite value; the floating-point maximum would drop NaN).  EMAX:
-// exponent of the format's largest power of two (2 for E2M1, 8 for E4M3).
+// exponent of the format's largest power of two (2 for E2M1, 8 for E4M3).  The exponent field ef gives
+// floor(log2 amax) = ef - 127 for normal amax, and ef - EMAX <= 0 covers zero, subnormal and tiny blocks.
 template <int EMAX>
 __device__ __forceinline__ uint32_t mx_scale_of_bits(uint32_t amax_bits) {
   const int ef = (int)(amax_bits >> 23);
   return ef == 255 ? 255u : (uint32_t)max(ef - EMAX, 0);
 }
 __device__ __forceinline__ uint32_t mx_abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// E8M0 scale byte of a block whose largest magnitude is amax (finite, >= 0): the
-// fp32 exponent field ef gives floor(log2 amax) = ef - 127 for normal amax, and
-// ef - 8 <= 0 covers zero, subnormal and tiny blocks.
-__device__ __forceinline__ uint32_t mx_scale_of(float amax) {
-  const int ef = (int)((__float_as_uint(amax) >> 23) & 0xFF);
-  return (uint32_t)max(ef - 8, 0);
-}
 
 // E4M3 code of a finite fp32 value: round to nearest, ties to the even code,
 // saturating at 448, sign bit kept.  The gfx950 packed conversion to OCP E4M3
@@ -41,17 +34,17 @@ __device__ __forceinline__ uint32_t e4m3_encode(float v) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, 0.0f, 0, false) & 0xFFu;
 }
 
-// Largest magnitude over the 32 lanes of this half-wave (lanes 0-31 or 32-63), in every lane of
-// it: DPP butterflies inside each row of 16 lanes (quad swaps, then the mirrored half row, then
-// the mirrored row), then one exchange between the two rows.  Every lane must take part.
-__device__ __forceinline__ float halfwave_amax(float v) {
-  auto dpp = [](float x, auto CTRL) __attribute__((always_inline)) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(CTRL)::value, 0xf, 0xf, true));
+// Bit pattern of the largest magnitude over the 32 lanes of this half-wave (lanes 0-31 or 32-63), in
+// every lane of it: DPP butterflies inside each row of 16 lanes (quad swaps, then the mirrored half
+// row, then the mirrored row), then one exchange between the two rows.  Every lane must take part.
+__device__ __forceinline__ uint32_t halfwave_amax(float v) {
+  auto dpp = [](uint32_t x, auto CTRL) __attribute__((always_inline)) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(CTRL)::value, 0xf, 0xf, true);
   };
-  float a = fabsf(v);
-  a = fmaxf(a, dpp(a, std::integral_constant<int, 0xB1>{}));   // quad_perm [1, 0, 3, 2]
-  a = fmaxf(a, dpp(a, std::integral_constant<int, 0x4E>{}));   // quad_perm [2, 3, 0, 1]
-  a = fmaxf(a, dpp(a, std::integral_constant<int, 0x141>{}));  // row_half_mirror
-  a = fmaxf(a, dpp(a, std::integral_constant<int, 0x140>{}));  // row_mirror
-  return fmaxf(a, __shfl_xor(a, 16, 64));
+  uint32_t a = mx_abs_bits(v);
+  a = max(a, dpp(a, std::integral_constant<int, 0xB1>{}));   // quad_perm [1, 0, 3, 2]
+  a = max(a, dpp(a, std::integral_constant<int, 0x4E>{}));   // quad_perm [2, 3, 0, 1]
+  a = max(a, dpp(a, std::integral_constant<int, 0x141>{}));  // row_half_mirror
+  a = max(a, dpp(a, std::integral_constant<int, 0x140>{}));  // row_mirror
+  return max(a, (uint32_t)__shfl_xor((int)a, 16, 64));
 }

@@ -146,7 +146,7 @@ static uint8_t mx_block(const double *v, int n, uint8_t *codes)
 
 static double elem(const void *p, int dt, size_t i);
 
-/* R8: rows x K values (f32 or bf16) -> codes [rows, K], scales [rows, K/32]; K % 32 == 0. */
+/* R8: rows x K finite values (f32 or bf16) -> codes [rows, K], scales [rows, K/32]; K % 32 == 0. */
 void oracle_mx_quantize(const void *x, int x_dt, int rows, int K, uint8_t *codes, uint8_t *scales)
 {
 #pragma omp parallel for schedule(static)

@@ -65,6 +65,36 @@ def test_ffn_mx4_intermediate_overflow(T, act):
     check_rows(y0, moe.moe_grouped_ffn_mx4(*quantize_act(s["x"], act), *args), T // 2)
 
 
+@pytest.mark.parametrize("T,E", [(20, 4), (600, 4)])  # weight streaming; tiles
+@pytest.mark.parametrize("kind", ["nan", "inf", "overflow"])
+def test_ffn_mx_rows(T, E, kind):
+    """The W8A8 FFN with MXFP8 weights, per-row outputs."""
+    g = gen(23)
+    H, I = 256, 128
+    w = [moe.moe_quantize_mx(torch.randn((E * n, k), device=DEV, generator=g) * 0.05) for n, k in ((2 * I, H), (H, I))]
+    wgu, wd = ((c.view(E, -1, k), s.view(E, -1, k // 32)) for (c, s), k in zip(w, (H, I)))
+    x = torch.randn((T, H), device=DEV, generator=g).bfloat16()
+    top, ids = torch.randn((T, E), device=DEV, generator=g).topk(2, 1)
+    p = moe.moe_permute(ids.int().contiguous(), torch.softmax(top, 1).contiguous(), E, 0, E)
+
+    def run():
+        rows = torch.empty((2 * T, H), dtype=torch.float32, device=DEV)
+        moe.moe_grouped_ffn_mx(*moe.moe_quantize_mx(x), p["offsets"], p["row_token"], p["row_w"], T, 2 * T, *wgu, *wd,
+                               y_perm=rows)
+        return rows
+    r0 = run()
+    bad = T // 2
+    if kind == "overflow":
+        x[bad] *= 1e30
+    else:
+        x[bad, 77] = math.nan if kind == "nan" else math.inf
+    r1 = run()
+    hit = p["row_token"] == bad
+    assert int(hit.sum()) == 2
+    assert bool(r1[hit].isnan().all())
+    assert torch.equal(r1[~hit], r0[~hit]) and bool(r1[~hit].isfinite().all())
+
+
 @pytest.mark.parametrize("T", [1, 64, 65, 150])
 @pytest.mark.parametrize("act", ["mxfp8", "mxfp4"])
 @pytest.mark.parametrize("bad", [math.nan, math.inf], ids=["nan", "inf"])
