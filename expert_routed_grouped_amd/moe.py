@@ -158,6 +158,15 @@ def torch_stream(stream, device):
     return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """What a call allocates itself comes from the pool of the stream it runs on: memory of another stream's pool may
+    have work of that stream ahead of it, or be handed out again while this call still runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch_stream(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def moe_version() -> int:
     return lib().moe_version()
 
@@ -168,9 +177,9 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, bias: Optional[torch.Tens
     T, H = x.shape
     E = w_router.shape[0]
     if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        topk_ids = _new((T, k), torch.int32, x.device, stream)
     if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=x.device)
+        topk_w = _new((T, k), torch.float32, x.device, stream)
     _check("moe_route", lib().moe_route(_ptr(x), _dtype(x), _ptr(w_router), _dtype(w_router), _ptr(bias), T, H, E, k,
                                         _ptr(topk_ids), _ptr(topk_w), _stream(stream)))
     return topk_ids, topk_w
@@ -188,19 +197,19 @@ def moe_permute(topk_ids: torch.Tensor, topk_w: torch.Tensor, E: int, e_begin: i
     R_cap = T * min(k, El)
     dev = topk_ids.device
     o = dict(out) if out else {}
-    o.setdefault("counts", torch.empty(El, dtype=torch.int32, device=dev))
-    o.setdefault("offsets", torch.empty(El + 1, dtype=torch.int32, device=dev))
-    o.setdefault("row_token", torch.empty(max(R_cap, 1), dtype=torch.int32, device=dev))
-    o.setdefault("row_w", torch.empty(max(R_cap, 1), dtype=torch.float32, device=dev))
-    o.setdefault("token_row", torch.empty((T, k), dtype=torch.int32, device=dev))
-    o.setdefault("workspace", torch.empty(max(moe_permute_workspace_size(T, k, El), 256), dtype=torch.uint8, device=dev))
+    for name, shape, dtype in (("counts", (El,), torch.int32), ("offsets", (El + 1,), torch.int32),
+                               ("row_token", (max(R_cap, 1),), torch.int32), ("row_w", (max(R_cap, 1),), torch.float32),
+                               ("token_row", (T, k), torch.int32),
+                               ("workspace", (max(moe_permute_workspace_size(T, k, El), 256),), torch.uint8)):
+        if name not in o:
+            o[name] = _new(shape, dtype, dev, stream)
     H = 0
     xdt = MOE_BF16
     if x is not None:
         H = x.shape[1]
         xdt = _dtype(x)
         if x_perm is None:
-            x_perm = torch.empty((max(R_cap, 1), H), dtype=x.dtype, device=dev)
+            x_perm = _new((max(R_cap, 1), H), x.dtype, dev, stream)
         o["x_perm"] = x_perm
     _check("moe_permute", lib().moe_permute(_ptr(topk_ids), _ptr(topk_w), T, k, E, e_begin, e_end,
                                             _ptr(o["counts"]), _ptr(o["offsets"]), _ptr(o["row_token"]),
@@ -239,7 +248,7 @@ def moe_grouped_ffn(a: torch.Tensor, offsets: torch.Tensor, row_token: torch.Ten
     adt = _dtype(a)
     need = moe_ffn_workspace_size(R_cap, El, H, I, adt)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=a.device)
+        workspace = _new((need,), torch.uint8, a.device, stream)
     flags = (MOE_FFN_GATHER if gather else 0) | (MOE_FFN_ZERO_Y if zero_y else 0)
     flags |= {"both": 0, "gate_up": MOE_FFN_ONLY_GATE_UP, "down": MOE_FFN_ONLY_DOWN}[phase]
     flags |= MOE_FFN_PACKED_WEIGHTS if packed else 0
@@ -275,9 +284,9 @@ def moe_quantize_mx(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scale
     """MXFP8 quantisation of a [rows, K] fp32/bf16 tensor -> (codes uint8 [rows, K], scales uint8 [rows, K/32])."""
     rows, K = x.shape
     if codes is None:
-        codes = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+        codes = _new((rows, K), torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+        scales = _new((rows, K // 32), torch.uint8, x.device, stream)
     _check("moe_quantize_mx", lib().moe_quantize_mx(_ptr(x), _dtype(x), rows, K, _ptr(codes), _ptr(scales),
                                                     _stream(stream)))
     return codes, scales
@@ -299,7 +308,7 @@ def moe_grouped_ffn_mx(a_codes: torch.Tensor, a_scales: torch.Tensor, offsets: t
     I = twoI // 2
     need = moe_ffn_mx_workspace_size(R_cap, I)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=a_codes.device)
+        workspace = _new((need,), torch.uint8, a_codes.device, stream)
     flags = (MOE_FFN_GATHER if gather else 0) | (MOE_FFN_ZERO_Y if zero_y else 0)
     flags |= {"both": 0, "gate_up": MOE_FFN_ONLY_GATE_UP, "down": MOE_FFN_ONLY_DOWN}[phase]
     flags |= MOE_FFN_PACKED_WEIGHTS if packed else 0
@@ -315,7 +324,7 @@ def moe_combine(y_perm: torch.Tensor, token_row: torch.Tensor, topk_w: torch.Ten
     T, k = token_row.shape
     H = y_perm.shape[1]
     if y is None:
-        y = torch.empty((T, H), dtype=torch.float32, device=y_perm.device)
+        y = _new((T, H), torch.float32, y_perm.device, stream)
     _check("moe_combine", lib().moe_combine(_ptr(y_perm), _ptr(token_row), _ptr(topk_w), T, k, H, _ptr(y),
                                             _stream(stream)))
     return y
@@ -336,7 +345,7 @@ def moe_shared_expert(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Te
     xdt = _dtype(x)
     need = moe_shared_workspace_size(T, I_s, xdt)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _new((need,), torch.uint8, x.device, stream)
     _check("moe_shared_expert", lib().moe_shared_expert(
         _ptr(x), xdt, T, H, I_s, _ptr(w_gate_up), _ptr(w_down), _dtype(w_gate_up), _ptr(s_gate_up), _ptr(s_down),
         _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -349,7 +358,7 @@ def moe_pack_weights(w: torch.Tensor, out: Optional[torch.Tensor] = None, stream
     same shape and dtype (pass it with ``packed=True``)."""
     E, N, K = (1, *w.shape) if w.dim() == 2 else w.shape
     if out is None:
-        out = torch.empty_like(w)
+        out = _new(w.shape, w.dtype, w.device, stream)
     if out.shape != w.shape or out.dtype != w.dtype:
         raise ValueError("out must have the shape and dtype of w")
     _check("moe_pack_weights", lib().moe_pack_weights(_ptr(w), _dtype(w), E, N, K, _ptr(out), _stream(stream)))
@@ -436,8 +445,7 @@ def decode_layer_error_word(workspace: torch.Tensor) -> int:
 
 # ---- MXFP4 (include/moe.h, the *_mx4 calls) ----
 # The C ABI cannot see buffer sizes, so the shape, type and device of every tensor are checked here.  A call is short
-# next to what Python adds to it: one pass over each argument, raw addresses and streams.  Tensors a call allocates
-# belong to the stream it runs on (``stream``, or the device's current one).
+# next to what Python adds to it: one pass over each argument, raw addresses and streams.
 def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, device):
     """Address of a contiguous GPU tensor of this type, shape and device (None stays None)."""
     if t is None:
@@ -476,15 +484,6 @@ class _On:
         if getattr(stream, "device", None) not in (None, torch.device("cuda", self.index)):
             raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{self.index}")
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """What a call allocates itself comes from the pool of the stream it runs on: memory of another stream's pool may
-    have work of that stream ahead of it, or be handed out again while this call still runs."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch_stream(stream, device)):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _out_dtype(dtype) -> int:
