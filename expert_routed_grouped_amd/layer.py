@@ -7,6 +7,7 @@ inputs to the device.  All arithmetic runs in the library's kernels.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from typing import Optional
 
 import numpy as np
@@ -18,6 +19,11 @@ from . import moe
 # than writing per-row outputs and reducing them with moe_combine (measured on MI355X:
 # ~0.33 T atomic adds/s against ~6-7 TB/s of streaming stores).
 FUSED_COMBINE_MAX_ELEMS = 16 * 1024 * 1024
+
+
+def _on(t: torch.Tensor):
+    """The tensor's device as the current one: the library launches on that."""
+    return moe._On(t.device) if t.is_cuda else nullcontext()
 
 
 def to_device(inputs: dict, device="cuda") -> dict:
@@ -57,7 +63,8 @@ def pack_weights(dev: dict) -> dict:
         return dev
     for key in ("w_gate_up", "w_down", "ws_gate_up", "ws_down"):
         if dev.get(key) is not None:
-            dev[key] = moe.moe_pack_weights(dev[key])
+            with _on(dev[key]):
+                dev[key] = moe.moe_pack_weights(dev[key])
     dev["packed"] = True
     return dev
 
@@ -69,7 +76,9 @@ def pack_router(dev: dict, stream=None) -> dict:
     run_layer orders its own reads after it, whatever stream it is given.  A graph captured from run_layer
     keeps the copy of its capture: capture again after a change of the router weight."""
     w = dev["w_router"]
-    if w.shape[1] % 4 == 0 and (dev.get("w_router_packed") is None or not _router_pack_current(dev)):
+    if w.shape[1] % 4 != 0 or (dev.get("w_router_packed") is not None and _router_pack_current(dev)):
+        return dev
+    with _on(w):
         if _capturing(w):
             raise RuntimeError("pack the router before capturing: the copy would not be written until the graph runs")
         packed = moe.moe_pack_router(w) if stream is None else moe.moe_pack_router(w, stream=stream)
@@ -181,8 +190,9 @@ def convert_experts_mx4(dev: dict) -> dict:
         if w.dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"{src} must be bf16 or fp32, got {w.dtype}")
         El, N, K = w.shape
-        codes, scales = moe.moe_quantize_mx4(w.reshape(El * N, K))
-        dev[dst] = moe.moe_pack_mx4(codes.view(El, N, K // 2), scales.view(El, N, K // 32))
+        with _on(w):
+            codes, scales = moe.moe_quantize_mx4(w.reshape(El * N, K))
+            dev[dst] = moe.moe_pack_mx4(codes.view(El, N, K // 2), scales.view(El, N, K // 32))
     return pack_router(dev)
 
 
@@ -250,8 +260,13 @@ def run_layer(dev: dict, bufs, stream=None) -> torch.Tensor:
     """route -> permute -> grouped FFN (-> combine) (-> shared expert), or for decode-sized batches
     moe_decode_layer (-> shared expert).  Returns y [T,H] fp32.  With Mx4LayerBuffers the experts are those of
     convert_experts_mx4 and y has the buffers' type."""
-    if isinstance(bufs, Mx4LayerBuffers):
-        return _run_layer_mx4(dev, bufs, stream)
+    with _on(dev["x"]):
+        if isinstance(bufs, Mx4LayerBuffers):
+            return _run_layer_mx4(dev, bufs, stream)
+        return _run_layer(dev, bufs, stream)
+
+
+def _run_layer(dev: dict, bufs: LayerBuffers, stream) -> torch.Tensor:
     cfg = bufs.cfg
     p = bufs.perm
     packed = bool(dev.get("packed", False))

@@ -238,3 +238,61 @@ def test_router_copy_of_a_graph_outlives_a_repack(rec, routed, monkeypatch):
     unread = weakref.ref(dev["w_router_packed"])  # no graph reads this one
     edit_and_run()
     assert unread() is None
+
+
+# ------------------------------------------------------------------ another device than the current one
+class OnDevice:
+    """A tensor's device, as far as the layer looks at it."""
+    is_cuda, device = True, torch.device("cuda", 1)
+
+    def __init__(self, shape=(4, 128)):
+        self.shape, self.dtype, self._version = shape, torch.bfloat16, 0
+
+    def data_ptr(self):
+        return id(self)
+
+    def is_inference(self):
+        return False
+
+    def reshape(self, *shape):
+        return OnDevice(shape)
+
+    view = reshape
+
+
+@pytest.mark.parametrize("T", [4, 70])
+@pytest.mark.parametrize("mx4", [True, False])
+def test_layer_on_another_device(monkeypatch, T, mx4):
+    """Every call of the layer, and of the conversion before it, is made with the tensors' device as the current one."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *exc):
+            current.pop()
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[-1])
+    monkeypatch.setattr(L, "_capturing", lambda t: False)
+    for name in ("moe_route", "moe_permute", "moe_quantize_mx", "moe_decode_layer_mx4", "moe_grouped_ffn_mx4",
+                 "moe_shared_expert", "moe_quantize_mx4", "moe_pack_mx4", "moe_pack_router", "moe_pack_weights",
+                 "moe_route_dispatch", "moe_grouped_ffn", "moe_combine"):
+        result = (OnDevice(), OnDevice()) if name == "moe_quantize_mx4" else None
+        monkeypatch.setattr(moe, name, lambda *a, name=name, result=result, **k: seen.append((name, current[-1])) or result)
+    dev, bufs = model(T, I_s=64)
+    if not mx4:
+        bufs = L.LayerBuffers(dev["cfg"], device="cpu", shared_beside_router=False)
+    dev.update(x=OnDevice(), w_router=OnDevice(), w_gate_up=OnDevice((4, 256, 128)), w_down=OnDevice((4, 128, 128)),
+               ws_gate_up=OnDevice(), ws_down=OnDevice())
+    if mx4:
+        L.convert_experts_mx4(dev)
+    else:
+        L.pack_weights(dev)
+    L.pack_router(dev)
+    L.run_layer(dev, bufs)
+    assert len(seen) >= 4 and all(at == 1 for _, at in seen), seen
+    assert current == [0]
