@@ -276,9 +276,9 @@ __global__ __launch_bounds__(NTHR, 2) void decode_route_gate_up_kernel(Params p)
   }
 }
 
-// Workgroups the device holds at once, per device and kernel instance (queried once).
-template <typename K>
-int resident_blocks(K kernel, size_t shm) {
+// Workgroups the device holds at once, per device and kernel (queried once; every call has the same LDS).
+template <auto KERNEL>
+int resident_blocks(size_t shm) {
   static std::mutex mu;
   static int cache[64];
   int dev = 0;
@@ -286,7 +286,7 @@ int resident_blocks(K kernel, size_t shm) {
   std::lock_guard<std::mutex> lock(mu);
   if (cache[dev] == 0) {
     int per_cu = 0, cus = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kernel, NTHR, shm) != hipSuccess ||
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, KERNEL, NTHR, shm) != hipSuccess ||
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
       return 0;
     cache[dev] = per_cu * cus;
@@ -300,8 +300,8 @@ constexpr size_t kLds = sizeof(float) * mx4s::RED_FLOATS + kGroupBytes;
 
 template <int EC>
 hipError_t launch(const Params &p, hipStream_t s) {
-  auto kernel = decode_route_gate_up_kernel<EC>;
-  const int resident = resident_blocks(kernel, kLds);
+  constexpr auto kernel = decode_route_gate_up_kernel<EC>;
+  const int resident = resident_blocks<kernel>(kLds);
   if (resident <= 0) return hipErrorInvalidConfiguration;
   const int tiles = p.R_cap < p.El + p.R_cap / mx4s::TM ? p.R_cap : p.El + p.R_cap / mx4s::TM;
   const long long most = p.n_route + (long long)tiles * (p.I / 32);
