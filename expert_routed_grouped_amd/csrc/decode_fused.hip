@@ -295,28 +295,33 @@ __global__ __launch_bounds__(NTHR, 2) void decode_layer_kernel(DecParams p) {  /
   }
 }
 
-// Workgroups the device holds at once, per device and kernel instance (queried once).
-template <typename K>
-int resident_blocks(K kernel, size_t shm) {
+// Workgroups the device holds at once, per device and kernel (queried when the LDS differs from the last call's).
+template <auto KERNEL>
+int resident_blocks(size_t shm) {
+  struct Held {
+    size_t shm;
+    int blocks;
+  };
   static std::mutex mu;
-  static int cache[64];
+  static Held cache[64];
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
-  if (cache[dev] == 0) {
+  Held &c = cache[dev];
+  if (c.blocks == 0 || c.shm != shm) {
     int per_cu = 0, cus = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kernel, NTHR, shm) != hipSuccess ||
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, KERNEL, NTHR, shm) != hipSuccess ||
         hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
       return 0;
-    cache[dev] = per_cu * cus;
+    c = Held{shm, per_cu * cus};
   }
-  return cache[dev];
+  return c.blocks;
 }
 
 template <int EC, bool WB, bool WP, bool FP8>
 hipError_t launch_k(const DecParams &p, size_t shm, hipStream_t s) {
-  auto kernel = decode_layer_kernel<EC, WB, WP, FP8>;
-  const int resident = resident_blocks(kernel, shm);
+  constexpr auto kernel = decode_layer_kernel<EC, WB, WP, FP8>;
+  const int resident = resident_blocks<kernel>(shm);
   if (resident <= 0) return hipErrorInvalidConfiguration;
   const int grid = p.n_items < resident ? p.n_items : resident;
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(NTHR), shm, s, p);

@@ -8,7 +8,7 @@ import pytest
 from expert_routed_grouped_amd import moe
 
 
-@pytest.mark.parametrize("kernel", ["decode_route_gate_up_kernel"])
+@pytest.mark.parametrize("kernel", ["decode_route_gate_up_kernel", "decode_layer_kernel"])
 def test_resident_workgroups_are_counted_per_kernel_instance(kernel):
     """The instances of a persistent kernel share one pointer type but not their registers: how many workgroups fit on the
     device is remembered for each of them."""
