@@ -29,6 +29,8 @@ int moe_quantize_mx4(const void *x, int x_dtype, int64_t rows, int K, uint8_t *c
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales) return MOE_ERR_NULL;
   if (!aligned(x, 16) || !aligned(codes, 4)) return MOE_ERR_ALIGN;
+  const size_t n = (size_t)rows * K, nx = n * (x_dtype == MOE_BF16 ? 2 : 4), nc = n / 2, ns = n / 32;
+  if (overlap(x, nx, codes, nc) || overlap(x, nx, scales, ns) || overlap(codes, nc, scales, ns)) return MOE_ERR_SHAPE;
   return hip_status(launch_quantize_mx4(x, x_dtype == MOE_BF16, rows, K, codes, scales, (hipStream_t)stream));
 }
 
@@ -40,6 +42,8 @@ int moe_dequantize_mx(const uint8_t *codes, const uint8_t *scales, int mx_dtype,
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !out) return MOE_ERR_NULL;
   if (!aligned(codes, mx_dtype == MOE_MXFP4 ? 4 : 8) || !aligned(out, 16)) return MOE_ERR_ALIGN;
+  const size_t n = (size_t)rows * K, nc = mx_dtype == MOE_MXFP4 ? n / 2 : n, no = n * (out_dtype == MOE_BF16 ? 2 : 4);
+  if (overlap(out, no, codes, nc) || overlap(out, no, scales, n / 32)) return MOE_ERR_SHAPE;
   return hip_status(launch_dequantize_mx(codes, scales, mx_dtype == MOE_MXFP4, rows, K, out, out_dtype == MOE_BF16,
                                          (hipStream_t)stream));
 }

@@ -365,8 +365,8 @@ int moe_grouped_ffn_mx(const uint8_t *a_codes, const uint8_t *a_scales, const in
  *   A block that holds a NaN or an infinity gets s = 255 (the E8M0 NaN) and zero codes: all of it reads
  *   as NaN, in moe_dequantize_mx and in the products.
  * x: rows x K, MOE_F32 or MOE_BF16, 16-byte aligned; codes [rows, K/2] uint8, 4-byte aligned; scales
- * [rows, K/32] uint8.  K a multiple of 32, rows >= 0, rows * K < 2^40.
- * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_HIP.
+ * [rows, K/32] uint8.  K a multiple of 32, rows >= 0, rows * K < 2^40.  No two buffers may overlap.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (also for overlapping buffers), MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_HIP.
  */
 int moe_quantize_mx4(const void *x, int x_dtype, int64_t rows, int K, uint8_t *codes, uint8_t *scales, void *stream);
 
@@ -377,7 +377,8 @@ int moe_quantize_mx4(const void *x, int x_dtype, int64_t rows, int K, uint8_t *c
  * mx_dtype: MOE_MXFP4 (codes [rows, K/2], 4-byte aligned) or MOE_MXFP8 (codes [rows, K], 8-byte aligned);
  * out [rows, K] MOE_F32 (exact) or MOE_BF16 (exact except E4M3 results below 2^-133, which round to
  * nearest even), 16-byte aligned.  A product past the largest fp32 value is infinite.  K a multiple of 32,
- * rows >= 0, rows * K < 2^40.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_HIP.
+ * rows >= 0, rows * K < 2^40.  out must not overlap codes or scales.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (also for overlapping buffers), MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_HIP.
  */
 int moe_dequantize_mx(const uint8_t *codes, const uint8_t *scales, int mx_dtype, int64_t rows, int K, void *out,
                       int out_dtype, void *stream);
