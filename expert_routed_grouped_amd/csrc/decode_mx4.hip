@@ -15,8 +15,9 @@
 // then the weights' bytes.  Against instruction issue the chain has the packed fp32 router (no unpacking)
 // and its x operand broadcast inside rows of 16 lanes by the FMA itself (DPP), so 16 steps cost 16 FMAs, four loads
 // and one LDS read: 16 us of 4096 steps (12.4 for the FMAs alone, 10.2 without DPP).  Touching the matrix beforehand
-// with the idle waves made it slower, 23 us.  Launch 1 takes 37 us for one token of 128 experts of 4096 x 1536, top 8,
-// 63 for five, 142 for 24.
+// with the idle waves made it slower, 23 us.  Launch 1 takes 38 us for one token of 128 experts of 4096 x 1536, top 8
+// (routing item 20, hand-over 3, top k and grouping 4, gate/up 11), 63 for five, 141 for 24, and 82 for 64 tokens and 32
+// local experts (23, 7, 14, 38).
 #include "mx4_stream.h"
 #include "route_dev.h"
 

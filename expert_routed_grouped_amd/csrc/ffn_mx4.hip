@@ -18,6 +18,9 @@
 // One workgroup per compute unit works through a list of tiles (written by the launch before), and its loading
 // waves run into the next tile while the others finish one.
 //
+// Times here and below are the shortest of 20 calls under a trace; medians are a few percent longer (6000 tokens: gate/up
+// 538 us with E4M3 activations, 370 with E2M1, down 302 and 245).
+//
 // What bounds it (32 experts x 384 rows, K = 8192, 4096 weight rows): with E4M3 activations 292 us or 2.8 PFLOP/s,
 // what a large fp8 library product reaches; the loads alone take 246 us, the products alone 239.  With E2M1 213 us or 3.9
 // PFLOP/s, loads alone 190, products alone 161: the path from L2 and beyond to LDS, 42 KB per us and compute unit of
@@ -482,7 +485,10 @@ __global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int parts, i
   }
 }
 
-// y[t] = sum of t's rows in slot order; a slot without a row (or with one out of range) adds nothing.  A thread sums
+// y[t] = sum of t's rows in slot order; a slot without a row (or with one out of range) adds nothing.  The rows come in y's
+// type and are added in fp32.  With bf16 y a term is thus rounded to bf16 once before the sum: fp32 rows would take 872 ->
+// 1040 us for 6000 tokens with E4M3 activations, 673 -> 821 with E2M1, and bring the error of the rounded y from about
+// 1.5 roundings of it to one; who needs that asks for fp32 y.  A thread sums
 // eight columns, the loads of eight slots in flight (509 tokens 18 -> 8 us) and non-temporal (6000 tokens 83 -> 70 us, 0.44
 // GB at 6.3 TB/s; the same for the stores of the down launch costs that 15 us).
 constexpr int SUM_THR = 256, SUM_COLS = 8;
@@ -540,9 +546,13 @@ int max_mtiles(int T, int R_cap, int El, int BM) {
   const long long a = ((long long)R_cap + (long long)El * (BM - 1)) / BM, b = (long long)El * ceil_div_i(T, BM);
   return (int)(a < b ? a : b);
 }
-// Rows of a tile: 64 while an expert has at most 40 rows on average, else 192.  128 experts, H = 4096, I = 1536, E4M3: 16
-// rows each 218 us (192-row tiles: 246), 32 rows 230 (261), 40 rows 234 (259), 48 rows 259 (261), 64 rows 350 (274), 128
-// rows 492 (349).  128-row tiles in place of 192 gain 2% at 64 rows and lose 22% at 128, 7% at 375.
+// Rows of a tile: 64 while R_cap / El, the most rows that an expert can have on average, is at most 40, else 192.  128
+// experts, H = 4096, I = 1536, top 8, all local (us with 64-row tiles, with 192-row tiles in brackets), E4M3: 16 rows each
+// 218 (243), 32 rows 230 (252), 40 rows 235 (257), 48 rows 242 (260), 64 rows 352 (278), 128 rows 493 (359); E2M1: 216
+// (228), 225 (240), 229 (245), 233 (249), 321 (259), 436 (314).  Between 48 and 64 rows it depends on how many experts
+// pass 64.  With El of E experts local, an expert has El / E of that on average: a share of 32 experts of 128 with 12 to 40
+// rows each gets 192-row tiles, E4M3 77 us instead of 69 at 12 rows, 79 instead of 75 at 31, E2M1 within 1%.
+// 128-row tiles in place of 192 gain 2% at 64 rows and lose 22% at 128, 7% at 375.
 int tile_rows(int R_cap, int El) { return ceil_div_i(R_cap, El) <= 40 ? 64 : 192; }
 size_t list_bytes(int T, int R_cap, int El, int H, int I) {
   const int m = max_mtiles(T, R_cap, El, tile_rows(R_cap, El));

@@ -201,7 +201,9 @@ class Mx4LayerBuffers:
 
     ``act``: format of the activations and the intermediate, "mxfp8" or "mxfp4"; ``dtype``: of y.  Up to 64
     tokens with MXFP8 activations take the two-launch layer (moe_decode_layer_mx4), everything else the
-    separate calls.  A shared expert adds into y in fp32, so it needs ``dtype`` torch.float32."""
+    separate calls.  A shared expert adds into y in fp32, so it needs ``dtype`` torch.float32.  They are made (the
+    workspace zeroed) on the current stream: order a first call on another stream after that, and give calls that
+    may overlap buffers of their own."""
 
     def __init__(self, cfg, device="cuda", act: str = "mxfp8", dtype=torch.bfloat16):
         if act not in ("mxfp8", "mxfp4"):
