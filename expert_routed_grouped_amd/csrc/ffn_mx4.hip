@@ -487,8 +487,8 @@ __global__ __launch_bounds__(256) void prepare_kernel(TileParams p, int parts, i
 
 // y[t] = sum of t's rows in slot order; a slot without a row (or with one out of range) adds nothing.  The rows come in y's
 // type and are added in fp32.  With bf16 y a term is thus rounded to bf16 once before the sum: fp32 rows would take 872 ->
-// 1040 us for 6000 tokens with E4M3 activations, 673 -> 821 with E2M1, and bring the error of the rounded y from about
-// 1.5 roundings of it to one; who needs that asks for fp32 y.  A thread sums
+// 1040 us for 6000 tokens with E4M3 activations, 673 -> 821 with E2M1, and bring the error of the rounded y from 1.4
+// roundings of it to one; who needs that asks for fp32 y.  A thread sums
 // eight columns, the loads of eight slots in flight (509 tokens 18 -> 8 us) and non-temporal (6000 tokens 83 -> 70 us, 0.44
 // GB at 6.3 TB/s; the same for the stores of the down launch costs that 15 us).
 constexpr int SUM_THR = 256, SUM_COLS = 8;
