@@ -69,6 +69,17 @@ def pack_weights(dev: dict) -> dict:
     return dev
 
 
+class _PackedOn:
+    """The stream that a packed router was made on, and the event after it.  Events cannot be copied: copies and pickles
+    of a layer have neither."""
+
+    def __init__(self, stream=None, done=None):
+        self.stream, self.done = stream, done
+
+    def __reduce__(self):
+        return _PackedOn, ()
+
+
 def pack_router(dev: dict, stream=None) -> dict:
     """Add the router weight in the layout of moe_pack_router (exact fp32, [H/4, E, 4]) as
     ``dev["w_router_packed"]``; decode-sized batches (moe_route_dispatch) then read it.  Done once,
@@ -87,7 +98,7 @@ def pack_router(dev: dict, stream=None) -> dict:
         if getattr(packed, "is_cuda", False):
             s, done = moe.torch_stream(stream, w.device), torch.cuda.Event()
             done.record(s)
-            dev["w_router_packed_on"] = (s.cuda_stream, done)
+            dev["w_router_packed_on"] = _PackedOn(s.cuda_stream, done)
     return dev
 
 
@@ -109,13 +120,13 @@ def _packed_router(dev: dict, stream) -> torch.Tensor:
     packed = dev["w_router_packed"]
     if getattr(packed, "is_cuda", False):
         s = moe.torch_stream(stream, w.device)
-        at, done = dev["w_router_packed_on"]
+        on = dev["w_router_packed_on"]
         if _capturing(packed):
             captured = dev.setdefault("w_router_packed_captured", [])
             if not any(c is packed for c in captured):
                 captured.append(packed)
-        elif s.cuda_stream != at:
-            s.wait_event(done)
+        elif on.done is not None and s.cuda_stream != on.stream:
+            s.wait_event(on.done)
             packed.record_stream(s)
     return packed
 

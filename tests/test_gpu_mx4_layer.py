@@ -116,3 +116,14 @@ def test_graph_keeps_its_router_copy():
         assert torch.equal(other.topk_ids, ids)
         assert all(torch.equal(a, b) for a, b in zip(want, (bufs.topk_ids, bufs.topk_w, bufs.y)))
         del junk
+
+
+def test_copied_layer():
+    import copy
+    cfg, dev = model(9, 97)
+    L.convert_experts_mx4(dev)
+    bufs = L.Mx4LayerBuffers(cfg)
+    y = L.run_layer(dev, bufs).clone()
+    other = copy.deepcopy(dev)
+    dev["w_router"].zero_()
+    assert torch.equal(L.run_layer(other, bufs), y)

@@ -296,3 +296,19 @@ def test_layer_on_another_device(monkeypatch, T, mx4):
     L.run_layer(dev, bufs)
     assert len(seen) >= 4 and all(at == 1 for _, at in seen), seen
     assert current == [0]
+
+
+def test_a_layer_with_a_packed_router_can_be_copied(routed, monkeypatch):
+    """copy.deepcopy and pickle of the layer's dict: events cannot be copied, and a copy's router is packed anew."""
+    import copy
+    log, stream, dev, bufs, used = routed
+
+    def refuse(self, protocol):
+        raise TypeError("cannot pickle 'Event' object")
+    monkeypatch.setattr(FakeEvent, "__reduce_ex__", refuse)
+    del log[:]
+    other = copy.deepcopy({k: v for k, v in dev.items() if k != "w_router_packed"})
+    other["w_router_packed"] = dev["w_router_packed"]  # the stand-in; a tensor would be copied with the rest
+    L.run_layer(other, bufs, stream=stream(9))
+    assert ("pack", 9) in [e[:2] for e in log] and used()[-1][0][1] is other["w_router_packed"]
+    assert other["w_router_packed"] is not dev["w_router_packed"]
