@@ -272,9 +272,12 @@ def _run_layer_mx4(dev: dict, bufs: Mx4LayerBuffers, stream) -> torch.Tensor:
 def run_layer(dev: dict, bufs, stream=None) -> torch.Tensor:
     """route -> permute -> grouped FFN (-> combine) (-> shared expert), or for decode-sized batches
     moe_decode_layer (-> shared expert).  Returns y [T,H] fp32.  With Mx4LayerBuffers the experts are those of
-    convert_experts_mx4 and y has the buffers' type."""
+    convert_experts_mx4 and y has the buffers' type; x then has as many tokens as the buffers."""
+    (T, H), cfg, mx4 = dev["x"].shape, bufs.cfg, isinstance(bufs, Mx4LayerBuffers)
+    if H != cfg.H or T > cfg.T or (mx4 and T != cfg.T):  # the routing would be written past the buffers
+        raise ValueError(f"x is [{T}, {H}], the buffers were made for [{cfg.T}, {cfg.H}]")
     with _on(dev["x"]):
-        if isinstance(bufs, Mx4LayerBuffers):
+        if mx4:
             return _run_layer_mx4(dev, bufs, stream)
         return _run_layer(dev, bufs, stream)
 

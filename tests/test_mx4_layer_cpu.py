@@ -286,7 +286,7 @@ def test_layer_on_another_device(monkeypatch, T, mx4):
     dev, bufs = model(T, I_s=64)
     if not mx4:
         bufs = L.LayerBuffers(dev["cfg"], device="cpu", shared_beside_router=False)
-    dev.update(x=OnDevice(), w_router=OnDevice(), w_gate_up=OnDevice((4, 256, 128)), w_down=OnDevice((4, 128, 128)),
+    dev.update(x=OnDevice((T, 128)), w_router=OnDevice(), w_gate_up=OnDevice((4, 256, 128)), w_down=OnDevice((4, 128, 128)),
                ws_gate_up=OnDevice(), ws_down=OnDevice())
     if mx4:
         L.convert_experts_mx4(dev)
@@ -312,3 +312,31 @@ def test_a_layer_with_a_packed_router_can_be_copied(routed, monkeypatch):
     L.run_layer(other, bufs, stream=stream(9))
     assert ("pack", 9) in [e[:2] for e in log] and used()[-1][0][1] is other["w_router_packed"]
     assert other["w_router_packed"] is not dev["w_router_packed"]
+
+
+@pytest.mark.parametrize("T,act", [(4, "mxfp8"), (4, "mxfp4"), (70, "mxfp8"), (70, "mxfp4")])
+@pytest.mark.parametrize("shape", ["more", "fewer", "wider"])
+def test_batch_that_does_not_fit_the_buffers(rec, T, act, shape):
+    """The routing and the codes of more tokens than the buffers hold would be written past them: refused before any call."""
+    dev, bufs = model(T, act=act)
+    L.convert_experts_mx4(dev)
+    del rec.calls[:]
+    dev["x"] = torch.zeros({"more": (T + 1, 128), "fewer": (T - 1, 128), "wider": (T, 256)}[shape], dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="buffers"):
+        L.run_layer(dev, bufs)
+    assert rec.calls == []
+
+
+@pytest.mark.parametrize("shape", [(5, 128), (4, 256)])
+def test_batch_that_does_not_fit_the_buffers_of_the_layer(rec, shape):
+    rec.replace("moe_route_dispatch")
+    rec.replace("moe_grouped_ffn")
+    dev, bufs = old_model()
+    del rec.calls[:]
+    dev["x"] = torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="buffers"):
+        L.run_layer(dev, bufs)
+    assert rec.calls == []
+    dev["x"] = torch.zeros((3, 128), dtype=torch.bfloat16)  # fewer tokens than the buffers were made for
+    L.run_layer(dev, bufs)
+    assert rec.calls
