@@ -127,3 +127,59 @@ def test_copied_layer():
     other = copy.deepcopy(dev)
     dev["w_router"].zero_()
     assert torch.equal(L.run_layer(other, bufs), y)
+
+
+@pytest.mark.parametrize("T,I_s", [(9, 0), (9, 192), (150, 0), (150, 192)])
+@pytest.mark.parametrize("act", ["mxfp8", "mxfp4"])
+def test_captured_layer(T, I_s, act):
+    """The layer captured and replayed with new tokens, eager calls on other buffers in between."""
+    cfg, dev = model(T, 98, I_s=I_s, e_begin=4, e_end=20)
+    L.convert_experts_mx4(dev)
+    dtype = torch.float32 if I_s else torch.bfloat16
+    bufs, other = (L.Mx4LayerBuffers(cfg, act=act, dtype=dtype) for _ in range(2))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    L.run_layer(dev, bufs, stream=side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        L.run_layer(dev, bufs, stream=side)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    for _ in range(4):
+        dev["x"].copy_(torch.randn(dev["x"].shape, device=DEV, generator=g))
+        L.run_layer(dev, other)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bufs.topk_ids, other.topk_ids) and torch.equal(bufs.topk_w, other.topk_w)
+        if I_s:  # the shared expert adds in no fixed order, see test_shared_expert_with_packed_weights
+            gu, dn = dev["ws_gate_up"].double(), dev["ws_down"].double()
+            a = dev["x"].double() @ gu.T
+            h = (a[:, :I_s] * torch.sigmoid(a[:, :I_s]) * a[:, I_s:]).abs()
+            bound = (2.0 ** -7 + 2 * (I_s + 8) * 2.0 ** -24) * (h @ dn.abs().T) + 2.0 ** -20 * other.y.abs()
+            assert bool(((bufs.y - other.y).double().abs() <= bound).all())
+        else:
+            assert torch.equal(bufs.y, other.y)
+
+
+@pytest.mark.parametrize("act", ["mxfp8", "mxfp4"])
+def test_layer_without_tokens(act):
+    cfg, dev = model(0, 99)
+    L.convert_experts_mx4(dev)
+    assert L.run_layer(dev, L.Mx4LayerBuffers(cfg, act=act)).shape == (0, 512)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 256, 32, 1024, 256), (64, 256, 8, 8192, 128)])
+def test_few_token_layer_at_its_limits(T, E, k, H, I):
+    """The most tokens, experts and assignments, and the widest rows, against the separate calls bit for bit."""
+    cfg = synth.LayerConfig("mx4", T=T, H=H, E=E, k=k, I=I, seed=100, w_std=0.06)
+    dev = L.to_device(synth.make_inputs(cfg))
+    L.convert_experts_mx4(dev)
+    bufs = L.Mx4LayerBuffers(cfg)
+    assert bufs.one_call
+    y = L.run_layer(dev, bufs)
+    ids, w = moe.moe_route(dev["x"], dev["w_router"], None, k)
+    p = moe.moe_permute(ids, w, E, 0, E)
+    want = moe.moe_grouped_ffn_mx4(*moe.moe_quantize_mx(dev["x"]), p["offsets"], p["row_token"], p["row_w"],
+                                   p["token_row"], dev["wgu_mx4"], dev["wd_mx4"])
+    assert torch.equal(ids, bufs.topk_ids) and torch.equal(w, bufs.topk_w) and torch.equal(y, want)
