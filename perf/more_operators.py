@@ -200,7 +200,7 @@ def prepare(case, seed):
         T, H, f = c["T"], c["H"], torch.float32
         s = {"case": c, "y": randn(T, H, dtype=DT[c["ydt"]]), "w_next": randn(H, std=0.1, dtype=f) + 1,
              "w_post": randn(H, std=0.1, dtype=f) + 1 if c["post"] else None,
-             "gate": None if c["gate"] == "none" else randn(H if c["gate"] == "channel" else T, std=0.5, dtype=f)}
+             "gate": None if c["gate"] == "none" else randn(*((H,) if c["gate"] == "channel" else (T, 1)), std=0.5, dtype=f)}
         if not c["grad"]:
             s["x"] = randn(T, H, std=2.0)
             return s
@@ -362,7 +362,7 @@ def _plain_route(s):
 def _plain_norm(s):
     c, dt = s["case"], DT[s["case"]["dtype"]]
     y = s["y"].float()
-    gate = {"none": 1.0, "channel": s["gate"], "token": None if s["gate"] is None else s["gate"][:, None]}[c["gate"]]
+    gate = 1.0 if s["gate"] is None else s["gate"]
     if not c["grad"]:
         if c["post"]:
             y = y * torch.rsqrt((y * y).mean(1, keepdim=True) + EPS) * s["w_post"]
@@ -382,7 +382,7 @@ def _plain_norm(s):
         u = yh * s["w_post"]
     else:
         dy, u, out["dw_post"] = du, y, None
-    out["dgate"] = None if c["gate"] == "none" else (d * u).sum(0 if c["gate"] == "channel" else 1)
+    out["dgate"] = None if c["gate"] == "none" else (d * u).sum(0) if c["gate"] == "channel" else (d * u).sum(1, keepdim=True)
     out["dy"] = dy.to(DT[c["ydt"]])
     return out
 
@@ -457,7 +457,7 @@ def _exact_norm(s):
     gate = None if s["gate"] is None else leaf(s["gate"])
     u = rms(y) * wp if c["post"] else y
     if gate is not None:
-        u = u * (gate if c["gate"] == "channel" else gate[:, None])
+        u = u * gate
     if not c["grad"]:
         x = c["scale"] * s["x"].to(f) + u
         return {"x": x.detach(), "n": (rms(x) * wn).detach()}
