@@ -1,0 +1,300 @@
+// Residual, gate and the RMS norms around a block (moe_block_norm, moe_block_norm_backward).
+//
+//   u = rms(y) w_post (or y),  x' = scale x + gate u,  n = rms(x') w_next,  rms(v) = v / sqrt(mean v^2 + eps)
+//
+// Backward, with r and rp the reciprocal roots, xh = x' r, yh = y rp, H the row's length:
+//   D  = dx' + r (dn w_next - xh c / H),  c = sum dn w_next xh          dx = scale D
+//   dv = gate D w_post,  dy = rp (dv - yh q / H),  q = sum dv yh
+//   dw_next = sum_t dn xh,  dw_post = sum_t gate D yh,  dgate = sum D u (over the tokens or over the row)
+// q follows from sums over dx' + r dn w_next and over xh apart, so that one reduction gives c and q:
+//   q = sum gate w_post yh (dx' + r dn w_next) - (r c / H) sum gate w_post yh xh.
+//
+// A workgroup holds a row in registers: every array is read once.  The column sums of the backward pass are kept per
+// workgroup over its rows and joined by a second launch, in a fixed order.
+#include "train.h"
+
+namespace {
+
+using train::load_n;
+using train::NormArgs;
+using train::store_n;
+
+// Sums of M values over a workgroup of W waves, the same in every thread.  ``buf`` holds 2 * M * W floats, its
+// halves used in turn, so that one barrier per sum is enough.
+template <int M, int W>
+__device__ __forceinline__ void block_sum(float (&v)[M], float *buf, int half) {
+#pragma unroll
+  for (int m = 0; m < M; m++) v[m] = train::wave_sum(v[m]);
+  if constexpr (W > 1) {
+    float *b = buf + half * M * W;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int m = 0; m < M; m++) b[m * W + (threadIdx.x >> 6)] = v[m];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < M; m++) {
+      v[m] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; w++) v[m] += b[m * W + w];
+    }
+  }
+}
+
+// Values of a type that the launch tells (weights and gates: fp32 or bf16).
+template <int N>
+__device__ __forceinline__ void load_w(const void *p, int bf16, size_t i, float (&v)[N]) {
+  if (bf16) load_n<N>((const uint16_t *)p + i, v);
+  else load_n<N>((const float *)p + i, v);
+}
+__device__ __forceinline__ float one_w(const void *p, int bf16, size_t i) {
+  return bf16 ? bf16_to_f32(((const uint16_t *)p)[i]) : ((const float *)p)[i];
+}
+
+// W waves a row, NV pieces of N values a thread.
+template <typename TX, typename TY, int W, int NV, int N>
+__global__ __launch_bounds__(W * 64) void block_norm_kernel(NormArgs a) {
+  __shared__ float buf[2 * W];
+  const int t = blockIdx.x, H = a.H;
+  const size_t row = (size_t)t * H;
+  float x[NV][N], y[NV][N];
+#pragma unroll
+  for (int v = 0; v < NV; v++) {
+    const int h = (v * W * 64 + threadIdx.x) * N;
+#pragma unroll
+    for (int i = 0; i < N; i++) x[v][i] = 0.0f, y[v][i] = 0.0f;
+    if (h < H) {
+      load_n<N>((const TX *)a.x + row + h, x[v]);
+      if (a.y) load_n<N>((const TY *)a.y + row + h, y[v]);
+    }
+  }
+  if (a.y) {
+    float rp = 1.0f;
+    if (a.w_post) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int v = 0; v < NV; v++)
+#pragma unroll
+        for (int i = 0; i < N; i++) s[0] = fmaf(y[v][i], y[v][i], s[0]);
+      block_sum<1, W>(s, buf, 0);
+      rp = 1.0f / sqrtf(s[0] / (float)H + a.eps);
+      if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rp;
+    }
+    const float gt = a.gate_kind == train::kGateToken ? one_w(a.gate, a.w_bf16, t) : 1.0f;
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+      const int h = (v * W * 64 + threadIdx.x) * N;
+      if (h < H) {
+        float f[N];
+        if (a.w_post) {
+          load_w<N>(a.w_post, a.w_bf16, h, f);
+#pragma unroll
+          for (int i = 0; i < N; i++) y[v][i] = y[v][i] * rp * f[i];
+        }
+        if (a.gate_kind == train::kGateChannel) {
+          load_w<N>(a.gate, a.w_bf16, h, f);
+#pragma unroll
+          for (int i = 0; i < N; i++) y[v][i] *= f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) x[v][i] = fmaf(a.scale, x[v][i], gt * y[v][i]);
+        if (a.x_out) store_n<N>((TX *)a.x_out + row + h, x[v]);
+      }
+    }
+  }
+  if (!a.n && !a.rstd_next) return;
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int v = 0; v < NV; v++)
+#pragma unroll
+    for (int i = 0; i < N; i++) s[0] = fmaf(x[v][i], x[v][i], s[0]);
+  block_sum<1, W>(s, buf, 1);
+  const float r = 1.0f / sqrtf(s[0] / (float)H + a.eps);
+  if (a.rstd_next && threadIdx.x == 0) a.rstd_next[t] = r;
+  if (!a.n) return;
+#pragma unroll
+  for (int v = 0; v < NV; v++) {
+    const int h = (v * W * 64 + threadIdx.x) * N;
+    if (h < H) {
+      float f[N];
+      load_w<N>(a.w_next, a.w_bf16, h, f);
+#pragma unroll
+      for (int i = 0; i < N; i++) f[i] *= x[v][i] * r;
+      store_n<N>((TX *)a.n + row + h, f);
+    }
+  }
+}
+
+// Partial column sums of one workgroup: dw_next, dw_post and a channel gate's, [3][H] each.
+template <typename TX, typename TY, int W, int NV, int N>
+__global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(NormArgs a) {
+  __shared__ float buf[2 * 3 * W];
+  const int H = a.H, tid = threadIdx.x;
+  const bool channel = a.gate_kind == train::kGateChannel;
+  float dwn[NV][N], dwp[NV][N], dgc[NV][N];
+#pragma unroll
+  for (int v = 0; v < NV; v++)
+#pragma unroll
+    for (int i = 0; i < N; i++) dwn[v][i] = 0.0f, dwp[v][i] = 0.0f, dgc[v][i] = 0.0f;
+  int half = 0;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, half ^= 1) {
+    const size_t row = (size_t)t * H;
+    const float rn = a.dn ? a.rn[t] : 0.0f, rp = a.w_post ? a.rp[t] : 1.0f;
+    const float gt = a.gate_kind == train::kGateToken ? one_w(a.gate, a.w_bf16, t) : 1.0f;
+    float xh[NV][N], yh[NV][N], b[NV][N];  // b = dx' + r dn w_next
+    float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+      const int h = (v * W * 64 + tid) * N;
+#pragma unroll
+      for (int i = 0; i < N; i++) xh[v][i] = 0.0f, yh[v][i] = 0.0f, b[v][i] = 0.0f;
+      if (h < H) {
+        if (a.dx_out) load_n<N>((const TX *)a.dx_out + row + h, b[v]);
+        if (a.dn) {
+          float dn[N], w[N];
+          load_n<N>((const TX *)a.x + row + h, xh[v]);
+          load_n<N>((const TX *)a.dn + row + h, dn);
+          load_w<N>(a.w_next, a.w_bf16, h, w);
+#pragma unroll
+          for (int i = 0; i < N; i++) {
+            xh[v][i] *= rn;
+            dwn[v][i] = fmaf(dn[i], xh[v][i], dwn[v][i]);
+            dn[i] *= w[i];
+            s[0] = fmaf(dn[i], xh[v][i], s[0]);
+            b[v][i] = fmaf(rn, dn[i], b[v][i]);
+          }
+        }
+        if (a.y) {
+          load_n<N>((const TY *)a.y + row + h, yh[v]);
+          float f[N], w[N];
+#pragma unroll
+          for (int i = 0; i < N; i++) f[i] = 1.0f;
+          if (a.w_post) load_w<N>(a.w_post, a.w_bf16, h, f);
+          if (channel) {
+            load_w<N>(a.gate, a.w_bf16, h, w);
+#pragma unroll
+            for (int i = 0; i < N; i++) f[i] *= w[i];
+          }
+#pragma unroll
+          for (int i = 0; i < N; i++) {
+            yh[v][i] *= rp;
+            const float q = f[i] * yh[v][i];
+            s[1] = fmaf(q, b[v][i], s[1]);
+            s[2] = fmaf(q, xh[v][i], s[2]);
+          }
+        }
+      }
+    }
+    block_sum<3, W>(s, buf, half);
+    const float c = rn * s[0] / (float)H;           // D = b - xh c
+    const float dot = s[1] - c * s[2], q = gt * dot / (float)H;  // sum of D u; mean of dv yh
+    if (a.d_gate && !channel && tid == 0) a.d_gate[t] = dot;
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+      const int h = (v * W * 64 + tid) * N;
+      if (h < H) {
+        float D[N], o[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          D[i] = fmaf(-xh[v][i], c, b[v][i]);
+          o[i] = a.scale * D[i];
+        }
+        if (a.dx) store_n<N>((TX *)a.dx + row + h, o);
+        if (a.y) {
+          float g[N], w[N];
+#pragma unroll
+          for (int i = 0; i < N; i++) g[i] = gt, w[i] = 1.0f;
+          if (channel) load_w<N>(a.gate, a.w_bf16, h, g);
+          if (a.w_post) load_w<N>(a.w_post, a.w_bf16, h, w);
+#pragma unroll
+          for (int i = 0; i < N; i++) {
+            const float du = g[i] * D[i], u = yh[v][i] * w[i];
+            if (channel) dgc[v][i] = fmaf(D[i], u, dgc[v][i]);
+            dwp[v][i] = fmaf(du, yh[v][i], dwp[v][i]);
+            o[i] = a.w_post ? rp * (du * w[i] - yh[v][i] * q) : du;
+          }
+          if (a.dy) store_n<N>((TY *)a.dy + row + h, o);
+        }
+      }
+    }
+  }
+  float *ws = (float *)a.ws + (size_t)blockIdx.x * 3 * H;
+#pragma unroll
+  for (int v = 0; v < NV; v++) {
+    const int h = (v * W * 64 + tid) * N;
+    if (h < H) {
+      if (a.dw_next) store_n<N>(ws + h, dwn[v]);
+      if (a.dw_post) store_n<N>(ws + H + h, dwp[v]);
+      if (a.d_gate && channel) store_n<N>(ws + 2 * (size_t)H + h, dgc[v]);
+    }
+  }
+}
+
+// The column sums of G workgroups, 64 columns a workgroup: sixteen waves take every sixteenth partial sum each.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(kSumWaves * 64) void column_sum_kernel(const float *ws, int G, int H, float *o0, float *o1,
+                                                                    float *o2) {
+  __shared__ float buf[kSumWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = blockIdx.x * 64 + lane;
+  float *o = blockIdx.y == 0 ? o0 : (blockIdx.y == 1 ? o1 : o2);
+  if (!o) return;
+  float s = 0.0f;
+  if (h < H) {
+    const float *p = ws + (size_t)blockIdx.y * H + h;
+#pragma unroll 8
+    for (int g = wave; g < G; g += kSumWaves) s += p[(size_t)g * 3 * H];
+  }
+  buf[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && h < H) {
+#pragma unroll
+    for (int w = 1; w < kSumWaves; w++) s += buf[w][lane];
+    o[h] = s;
+  }
+}
+
+constexpr int kMaxBlocks = 512;
+
+template <typename TX, typename TY, int W, int NV, int N>
+hipError_t launch(const NormArgs &a, bool backward, hipStream_t s) {
+  if (!backward) {  // T >= 1
+    hipLaunchKernelGGL((block_norm_kernel<TX, TY, W, NV, N>), dim3(a.T), dim3(W * 64), 0, s, a);
+    return hipGetLastError();
+  }
+  const int G = a.T < kMaxBlocks ? a.T : kMaxBlocks;
+  if (G > 0) hipLaunchKernelGGL((block_norm_backward_kernel<TX, TY, W, NV, N>), dim3(G), dim3(W * 64), 0, s, a);
+  hipError_t err = hipGetLastError();
+  float *gate = a.gate_kind == train::kGateChannel ? a.d_gate : nullptr;
+  if (err != hipSuccess || (!a.dw_next && !a.dw_post && !gate)) return err;
+  hipLaunchKernelGGL(column_sum_kernel, dim3(ceil_div_i(a.H, 64), 3), dim3(kSumWaves * 64), 0, s, (const float *)a.ws, G, a.H,
+                     a.dw_next, a.dw_post, gate);
+  return hipGetLastError();
+}
+
+template <typename TX, typename TY>
+hipError_t pick(const NormArgs &a, bool backward, hipStream_t s) {
+  const int H = a.H;
+  if (H % 8 == 0) {
+    if (H <= 512) return launch<TX, TY, 1, 1, 8>(a, backward, s);
+    if (H <= 2048) return launch<TX, TY, 4, 1, 8>(a, backward, s);
+    if (H <= 4096) return launch<TX, TY, 4, 2, 8>(a, backward, s);
+    if (H <= 8192) return launch<TX, TY, 8, 2, 8>(a, backward, s);
+    return launch<TX, TY, 16, 2, 8>(a, backward, s);
+  }
+  if (H <= 256) return launch<TX, TY, 1, 4, 1>(a, backward, s);
+  if (H <= 2048) return launch<TX, TY, 4, 8, 1>(a, backward, s);
+  return launch<TX, TY, 16, 16, 1>(a, backward, s);
+}
+
+hipError_t by_type(const NormArgs &a, bool backward, hipStream_t s) {
+  if (a.x_bf16) return a.y_bf16 ? pick<uint16_t, uint16_t>(a, backward, s) : pick<uint16_t, float>(a, backward, s);
+  return a.y_bf16 ? pick<float, uint16_t>(a, backward, s) : pick<float, float>(a, backward, s);
+}
+
+}  // namespace
+
+size_t train::norm_grad_ws_bytes(int T, int H) {
+  return align_up((size_t)(T < kMaxBlocks ? T : kMaxBlocks) * 3 * H * sizeof(float), 256);
+}
+hipError_t train::launch_block_norm(const NormArgs &a, hipStream_t s) { return by_type(a, false, s); }
+hipError_t train::launch_block_norm_backward(const NormArgs &a, hipStream_t s) { return by_type(a, true, s); }

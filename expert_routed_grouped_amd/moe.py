@@ -30,7 +30,12 @@ EXPORTS = ("moe_version", "moe_status_str", "moe_route", "moe_permute", "moe_per
            "moe_route_dispatch", "moe_pack_weights", "moe_pack_router", "moe_grouped_ffn_noalloc",
            "moe_decode_layer_workspace_size", "moe_decode_layer", "moe_workspace_size", "moe_quantize_mx4",
            "moe_dequantize_mx", "moe_mx4_packed_scale_bytes", "moe_pack_mx4", "moe_ffn_mx4_workspace_size",
-           "moe_grouped_ffn_mx4", "moe_decode_layer_mx4_workspace_size", "moe_decode_layer_mx4")
+           "moe_grouped_ffn_mx4", "moe_decode_layer_mx4_workspace_size", "moe_decode_layer_mx4", "moe_grouped_mm",
+           "moe_grouped_wgrad_workspace_size", "moe_grouped_wgrad", "moe_swiglu", "moe_swiglu_backward",
+           "moe_route_backward_workspace_size", "moe_route_backward", "moe_block_norm",
+           "moe_block_norm_backward_workspace_size", "moe_block_norm_backward")
+MOE_MM_TRANSPOSED, MOE_WGRAD_ADD = 1, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 MOE_OP_PERMUTE, MOE_OP_GROUPED_FFN, MOE_OP_GROUPED_FFN_F32, MOE_OP_GROUPED_FFN_MX = 0, 1, 2, 3
 MOE_OP_ROUTE_DISPATCH, MOE_OP_DECODE_LAYER, MOE_OP_SHARED_EXPERT, MOE_OP_SHARED_EXPERT_F32 = 4, 5, 6, 7
 MOE_OP_GROUPED_FFN_MX4, MOE_OP_DECODE_LAYER_MX4 = 8, 9
@@ -114,6 +119,27 @@ def lib():
         L.moe_decode_layer_mx4_workspace_size.argtypes = [I, I, I, I, I]
         L.moe_decode_layer_mx4.restype = I
         L.moe_decode_layer_mx4.argtypes = [P, P, P, I, I, I, I, I, I, I, P, P, P, P, P, P, P, I, P, Z, P]
+        U, F = ctypes.c_uint, ctypes.c_float
+        L.moe_grouped_mm.restype = I
+        L.moe_grouped_mm.argtypes = [P, P, I, P, I, P, I, I, I, I, P, I, U, P]
+        L.moe_grouped_wgrad_workspace_size.restype = Z
+        L.moe_grouped_wgrad_workspace_size.argtypes = [I, I, I, I, I]
+        L.moe_grouped_wgrad.restype = I
+        L.moe_grouped_wgrad.argtypes = [P, P, I, P, P, I, I, P, I, I, I, I, P, I, P, Z, U, P]
+        L.moe_swiglu.restype = I
+        L.moe_swiglu.argtypes = [P, I, P, P, I, I, I, P, P]
+        L.moe_swiglu_backward.restype = I
+        L.moe_swiglu_backward.argtypes = [P, P, I, P, P, I, I, I, P, P, P, P]
+        L.moe_route_backward_workspace_size.restype = Z
+        L.moe_route_backward_workspace_size.argtypes = [I, I, I, I]
+        L.moe_route_backward.restype = I
+        L.moe_route_backward.argtypes = [P, P, P, I, I, I, I, P, P, I, P, P, P, P, I, P, I, P, I, P, P, P, Z, P]
+        L.moe_block_norm.restype = I
+        L.moe_block_norm.argtypes = [P, I, P, I, P, P, P, I, I, F, F, I, I, P, P, P, P, P]
+        L.moe_block_norm_backward_workspace_size.restype = Z
+        L.moe_block_norm_backward_workspace_size.argtypes = [I, I]
+        L.moe_block_norm_backward.restype = I
+        L.moe_block_norm_backward.argtypes = [P, I, P, I, P, P, P, I, I, F, P, P, P, P, I, I, P, P, P, P, P, P, Z, P]
         _lib = L
     return _lib
 
@@ -637,3 +663,249 @@ def moe_decode_layer_mx4(x: torch.Tensor, w_router_packed: torch.Tensor, bias: O
     with _On(dev) as on:
         _check("moe_decode_layer_mx4", lib().moe_decode_layer_mx4(*args, on.stream(stream)))
     return y, topk_ids, topk_w
+
+
+def _space(workspace: Optional[torch.Tensor], need: int, dev, stream):
+    """(address, bytes) of a call's workspace, made here where the caller gives none; and the tensor to keep."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = _new((need,), torch.uint8, dev, stream)
+    return _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.nbytes, workspace
+
+
+def moe_grouped_mm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, row_index: Optional[torch.Tensor] = None,
+                   transposed: bool = False, out: Optional[torch.Tensor] = None, dtype=None, stream=None) -> torch.Tensor:
+    """Rows grouped by expert times their expert's matrix -> out [R_cap, N] of ``dtype`` (default: a's).
+
+    ``w`` is [E_loc, N, K] (a projection), or [E_loc, K, N] with ``transposed`` (the gradient of its input).  Row r reads
+    a[row_index[r]], or a[r].  R_cap is the length of ``row_index``, of ``out``, or of ``a``; rows behind offsets[-1]
+    are left as they were."""
+    dev, i32 = a.device, torch.int32
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, K], w [E_loc, N, K] (transposed: [E_loc, K, N])")
+    El, N, K = w.shape
+    if transposed:
+        N, K = K, N
+    R = out.shape[0] if out is not None else (row_index if row_index is not None else a).shape[0]
+    if row_index is not None and row_index.shape[0] < R:
+        raise ValueError(f"row_index has {row_index.shape[0]} entries for {R} rows")
+    if out is None:
+        _out_dtype(a.dtype if dtype is None else dtype)
+        out = _new((R, N), a.dtype if dtype is None else dtype, dev, stream)
+    args = (_arg(a, "a", a.dtype, (a.shape[0], K), dev),
+            None if row_index is None else _arg(row_index, "row_index", i32, (row_index.shape[0],), dev), a.shape[0],
+            _arg(w, "w", a.dtype, w.shape, dev), _out_dtype(a.dtype), _arg(offsets, "offsets", i32, (El + 1,), dev), El, R, N,
+            K, _arg(out, "out", out.dtype, (R, N), dev), _out_dtype(out.dtype), MOE_MM_TRANSPOSED if transposed else 0)
+    with _On(dev) as on:
+        _check("moe_grouped_mm", lib().moe_grouped_mm(*args, on.stream(stream)))
+    return out
+
+
+def moe_grouped_wgrad_workspace_size(E_loc: int, R_cap: int, M: int, N: int, dtype=torch.bfloat16) -> int:
+    return int(lib().moe_grouped_wgrad_workspace_size(E_loc, R_cap, M, N, _out_dtype(dtype)))
+
+
+def moe_grouped_wgrad(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, a_index: Optional[torch.Tensor] = None,
+                      b_index: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, add: bool = False,
+                      dtype=None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Weight gradient of a grouped product: out[e] = (out[e] if add) + sum over e's rows of a_r b_r^T -> [E_loc, M, N]
+    of ``dtype`` (default: a's).  ``a`` [rows, M] is the gradient of the product, ``b`` [rows, N] its input; either may
+    be gathered by an index of its rows."""
+    dev, i32 = a.device, torch.int32
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a must be [rows, M] and b [rows, N]")
+    El, M, N = offsets.shape[0] - 1, a.shape[1], b.shape[1]
+    R = min((t if i is None else i).shape[0] for t, i in ((a, a_index), (b, b_index)))
+    if out is None:
+        if add:
+            raise ValueError("add needs out")
+        _out_dtype(a.dtype if dtype is None else dtype)
+        out = _new((El, M, N), a.dtype if dtype is None else dtype, dev, stream)
+    dt = _out_dtype(a.dtype)
+    ws, nws, workspace = _space(workspace, int(lib().moe_grouped_wgrad_workspace_size(El, R, M, N, dt)), dev, stream)
+    args = (_arg(a, "a", a.dtype, a.shape, dev),
+            None if a_index is None else _arg(a_index, "a_index", i32, (a_index.shape[0],), dev), a.shape[0],
+            _arg(b, "b", a.dtype, b.shape, dev),
+            None if b_index is None else _arg(b_index, "b_index", i32, (b_index.shape[0],), dev), b.shape[0], dt,
+            _arg(offsets, "offsets", i32, (El + 1,), dev), El, R, M, N, _arg(out, "out", out.dtype, (El, M, N), dev),
+            _out_dtype(out.dtype), ws, nws, MOE_WGRAD_ADD if add else 0)
+    with _On(dev) as on:
+        _check("moe_grouped_wgrad", lib().moe_grouped_wgrad(*args, on.stream(stream)))
+    return out
+
+
+def _rows_of(offsets: Optional[torch.Tensor], dev):
+    """(address of the offsets or None, experts)."""
+    if offsets is None:
+        return None, 1
+    return _arg(offsets, "offsets", torch.int32, (offsets.shape[0],), dev), offsets.shape[0] - 1
+
+
+def moe_swiglu(gu: torch.Tensor, offsets: Optional[torch.Tensor] = None, row_w: Optional[torch.Tensor] = None,
+               h: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """h[r] = row_w[r] silu(gu[r, :I]) gu[r, I:] -> [R_cap, I] of gu's type.  Without ``offsets`` all rows are computed,
+    with them those below offsets[-1]."""
+    R, I2 = gu.shape
+    dev, I = gu.device, I2 // 2
+    if h is None:
+        h = _new((R, I), gu.dtype, dev, stream)
+    off, El = _rows_of(offsets, dev)
+    args = (_arg(gu, "gu", gu.dtype, (R, 2 * I), dev), _out_dtype(gu.dtype), off,
+            None if row_w is None else _arg(row_w, "row_w", torch.float32, (R,), dev), El, R, I,
+            _arg(h, "h", gu.dtype, (R, I), dev))
+    with _On(dev) as on:
+        _check("moe_swiglu", lib().moe_swiglu(*args, on.stream(stream)))
+    return h
+
+
+def moe_swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                        row_w: Optional[torch.Tensor] = None, dgu: Optional[torch.Tensor] = None,
+                        h: Optional[torch.Tensor] = None, d_row_w: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_swiglu -> (dgu [R_cap, 2I], h [R_cap, I] as the forward call gives it, d_row_w [R_cap] or None
+    without ``row_w``).  ``dgu`` may be ``gu`` and ``h`` may be ``dh``."""
+    R, I2 = gu.shape
+    dev, I, f32 = gu.device, I2 // 2, torch.float32
+    if dgu is None:
+        dgu = _new((R, 2 * I), gu.dtype, dev, stream)
+    if h is None:
+        h = _new((R, I), gu.dtype, dev, stream)
+    if d_row_w is None and row_w is not None:
+        d_row_w = _new((R,), f32, dev, stream)
+    off, El = _rows_of(offsets, dev)
+    args = (_arg(gu, "gu", gu.dtype, (R, 2 * I), dev), _arg(dh, "dh", gu.dtype, (R, I), dev), _out_dtype(gu.dtype), off,
+            None if row_w is None else _arg(row_w, "row_w", f32, (R,), dev), El, R, I,
+            _arg(dgu, "dgu", gu.dtype, (R, 2 * I), dev), _arg(h, "h", gu.dtype, (R, I), dev),
+            None if d_row_w is None else _arg(d_row_w, "d_row_w", f32, (R,), dev))
+    with _On(dev) as on:
+        _check("moe_swiglu_backward", lib().moe_swiglu_backward(*args, on.stream(stream)))
+    return dgu, h, d_row_w
+
+
+def moe_route_backward_workspace_size(T: int, k: int, H: int, E: int) -> int:
+    return int(lib().moe_route_backward_workspace_size(T, k, H, E))
+
+
+def moe_route_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor, d_topk_w: torch.Tensor, x: torch.Tensor,
+                       w_router: torch.Tensor, perm: dict, rows: Optional[torch.Tensor] = None,
+                       token_row: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None, dtype=None,
+                       dw_router: Optional[torch.Tensor] = None, d_bias: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of the router weight [E, H] and bias [E] (fp32) and of the layer's input [T, H] (``dtype``, default x's)
+    from that of the gates -> (dx, dw_router, d_bias).
+
+    ``perm`` is moe_permute's over all E experts.  ``rows`` [R_cap, H] are the input gradients of the local experts' rows,
+    which dx sums too; ``token_row`` [T, k] says which (default: perm's, for a layer that holds every expert)."""
+    (T, k), (E, H) = topk_ids.shape, w_router.shape
+    dev, i32, f32 = x.device, torch.int32, torch.float32
+    if dx is None:
+        _out_dtype(x.dtype if dtype is None else dtype)
+        dx = _new((T, H), x.dtype if dtype is None else dtype, dev, stream)
+    if dw_router is None:
+        dw_router = _new((E, H), f32, dev, stream)
+    if d_bias is None:
+        d_bias = _new((E,), f32, dev, stream)
+    if rows is not None and token_row is None:
+        token_row = perm["token_row"]
+    ws, nws, workspace = _space(workspace, int(lib().moe_route_backward_workspace_size(T, k, H, E)), dev, stream)
+    row_token = perm["row_token"]
+    if row_token.dim() != 1 or row_token.shape[0] < T * k:
+        raise ValueError(f"perm must be over all experts: row_token needs T * k = {T * k} entries")
+    args = (_arg(topk_ids, "topk_ids", i32, (T, k), dev), _arg(topk_w, "topk_w", f32, (T, k), dev),
+            _arg(d_topk_w, "d_topk_w", f32, (T, k), dev), T, k, E, H, _arg(x, "x", x.dtype, (T, H), dev),
+            _arg(w_router, "w_router", x.dtype, (E, H), dev), _out_dtype(x.dtype),
+            _arg(perm["offsets"], "perm offsets", i32, (E + 1,), dev),
+            _arg(row_token, "perm row_token", i32, row_token.shape, dev),
+            _arg(perm["token_row"], "perm token_row", i32, (T, k), dev),
+            None if rows is None else _arg(rows, "rows", rows.dtype, (rows.shape[0], H), dev),
+            MOE_F32 if rows is None else _out_dtype(rows.dtype),
+            None if rows is None else _arg(token_row, "token_row", i32, (T, k), dev),
+            0 if rows is None else rows.shape[0], _arg(dx, "dx", dx.dtype, (T, H), dev), _out_dtype(dx.dtype),
+            _arg(dw_router, "dw_router", f32, (E, H), dev), _arg(d_bias, "d_bias", f32, (E,), dev), ws, nws)
+    with _On(dev) as on:
+        _check("moe_route_backward", lib().moe_route_backward(*args, on.stream(stream)))
+    return dx, dw_router, d_bias
+
+
+def _norm_weights(T, H, dev, **named):
+    """MOE_* type and gate kind of the norms' weights and gate, and their addresses; all of one type."""
+    given = [t for t in named.values() if t is not None]
+    dt = given[0].dtype if given else torch.float32
+    kind = MOE_GATE_NONE
+    if named["gate"] is not None:
+        kind = MOE_GATE_CHANNEL if named["gate"].dim() == 1 else MOE_GATE_TOKEN
+    shapes = {"gate": (H,) if kind == MOE_GATE_CHANNEL else (T, 1)}
+    return _out_dtype(dt), kind, [None if t is None else _arg(t, n, dt, shapes.get(n, (H,)), dev) for n, t in named.items()]
+
+
+def moe_block_norm(x: torch.Tensor, w_next: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                   w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                   eps: float = 1e-6, x_out: Optional[torch.Tensor] = None, n: Optional[torch.Tensor] = None,
+                   stats: bool = False, stream=None):
+    """The residual around a block with the RMS norms after it and before the next one ->
+    (x_out, n, rstd_next, rstd_post):
+
+    x_out = scale x + gate rms(y) w_post (without ``w_post``: scale x + gate y), n = rms(x_out) w_next.  ``gate`` is [H]
+    (per channel) or [T, 1] (per token).  Without ``y``: n = rms(x) w_next alone, x_out None.  Without ``w_next``: n None.
+    With ``stats`` the reciprocal roots [T] that the backward pass needs are returned too, else None.  ``x_out`` may be
+    ``x`` itself."""
+    T, H = x.shape
+    dev, f32 = x.device, torch.float32
+    if y is not None and x_out is None:
+        x_out = _new((T, H), x.dtype, dev, stream)
+    if w_next is not None and n is None:
+        n = _new((T, H), x.dtype, dev, stream)
+    rn = _new((T,), f32, dev, stream) if stats and w_next is not None else None
+    rp = _new((T,), f32, dev, stream) if stats and w_post is not None else None
+    wdt, kind, (wn, wp, g) = _norm_weights(T, H, dev, w_next=w_next, w_post=w_post, gate=gate)
+    args = (_arg(x, "x", x.dtype, (T, H), dev), _out_dtype(x.dtype),
+            None if y is None else _arg(y, "y", y.dtype, (T, H), dev), MOE_F32 if y is None else _out_dtype(y.dtype), wn, wp,
+            g, wdt, kind, scale, eps, T, H, None if x_out is None else _arg(x_out, "x_out", x.dtype, (T, H), dev),
+            None if n is None else _arg(n, "n", x.dtype, (T, H), dev), None if rn is None else rn.data_ptr(),
+            None if rp is None else rp.data_ptr())
+    with _On(dev) as on:
+        _check("moe_block_norm", lib().moe_block_norm(*args, on.stream(stream)))
+    return x_out, n, rn, rp
+
+
+def moe_block_norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(lib().moe_block_norm_backward_workspace_size(T, H))
+
+
+def moe_block_norm_backward(x_out: torch.Tensor, w_next: Optional[torch.Tensor] = None,
+                            rstd_next: Optional[torch.Tensor] = None, dn: Optional[torch.Tensor] = None,
+                            dx_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                            w_post: Optional[torch.Tensor] = None, rstd_post: Optional[torch.Tensor] = None,
+                            gate: Optional[torch.Tensor] = None, scale: float = 1.0, dx: Optional[torch.Tensor] = None,
+                            dy: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            stream=None) -> dict:
+    """Gradient of moe_block_norm -> dict(dx, dy, dw_next, dw_post, dgate), None for what the call had not.
+
+    ``x_out`` is the sum that the forward call gave (without ``y``: x), ``rstd_next`` and ``rstd_post`` its reciprocal
+    roots; ``dn`` and ``dx_out`` the gradients of its results, either may be missing.  dw_next, dw_post and dgate are
+    fp32.  ``dx`` may be ``dx_out`` or ``dn`` itself."""
+    T, H = x_out.shape
+    dev, f32 = x_out.device, torch.float32
+    if dx is None:
+        dx = _new((T, H), x_out.dtype, dev, stream)
+    if y is not None and dy is None:
+        dy = _new((T, H), y.dtype, dev, stream)
+    dwn = _new((H,), f32, dev, stream) if w_next is not None else None
+    dwp = _new((H,), f32, dev, stream) if w_post is not None else None
+    dg = _new(gate.shape, f32, dev, stream) if gate is not None else None
+    ws, nws, workspace = _space(workspace, int(lib().moe_block_norm_backward_workspace_size(T, H)), dev, stream)
+    wdt, kind, (wn, wp, g) = _norm_weights(T, H, dev, w_next=w_next, w_post=w_post, gate=gate)
+
+    def at(t, name, dtype, shape):
+        return None if t is None else _arg(t, name, dtype, shape, dev)
+
+    xdt = x_out.dtype
+    args = (_arg(x_out, "x_out", xdt, (T, H), dev), _out_dtype(xdt), at(y, "y", y.dtype if y is not None else f32, (T, H)),
+            MOE_F32 if y is None else _out_dtype(y.dtype), wn, wp, g, wdt, kind, scale,
+            at(rstd_next, "rstd_next", f32, (T,)), at(rstd_post, "rstd_post", f32, (T,)), at(dx_out, "dx_out", xdt, (T, H)),
+            at(dn, "dn", xdt, (T, H)), T, H, _arg(dx, "dx", xdt, (T, H), dev),
+            at(dy, "dy", y.dtype if y is not None else f32, (T, H)), None if dwn is None else dwn.data_ptr(),
+            None if dwp is None else dwp.data_ptr(), None if dg is None else dg.data_ptr(), ws, nws)
+    with _On(dev) as on:
+        _check("moe_block_norm_backward", lib().moe_block_norm_backward(*args, on.stream(stream)))
+    return {"dx": dx, "dy": dy, "dw_next": dwn, "dw_post": dwp, "dgate": dg}

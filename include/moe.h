@@ -14,7 +14,9 @@
  * launch), moe_decode_layer (all four of a decode batch in one launch), moe_shared_expert (an always-active expert added to y), the W8A8
  * MXFP8 variant of the expert FFN (moe_quantize_mx, moe_grouped_ffn_mx), MXFP4
  * experts (moe_quantize_mx4, moe_dequantize_mx, moe_pack_mx4, moe_grouped_ffn_mx4,
- * and moe_decode_layer_mx4, a few tokens' whole layer in two launches) and
+ * and moe_decode_layer_mx4, a few tokens' whole layer in two launches), the calls
+ * that train a block (moe_grouped_mm, moe_grouped_wgrad, moe_swiglu,
+ * moe_route_backward, moe_block_norm and their gradients) and
  * moe_pack_weights / moe_pack_router (one-time reorderings of resident expert
  * and router weights for faster reads), and moe_grouped_ffn_noalloc (the expert
  * FFN for callers that cannot allocate a workspace).
@@ -620,6 +622,163 @@ size_t moe_shared_workspace_size(int T, int I_s, int x_dtype);
 int moe_shared_expert(const void *x, int x_dtype, int T, int H, int I_s, const void *w_gate_up, const void *w_down,
                       int w_dtype, const float *s_gate_up, const float *s_down, float *y, void *workspace,
                       size_t workspace_bytes, unsigned flags, void *stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Training a MoE block: the expert products in their three directions, the gated activation between
+ * them, the router's gradient, and the residual with the norms around the block.  The forward pass of a
+ * block in these calls: moe_block_norm, moe_route, moe_permute, moe_grouped_mm (gate/up, rows gathered),
+ * moe_swiglu, moe_grouped_mm (down, fp32 rows), moe_combine with weights of one (the gates are in h),
+ * moe_block_norm; the Python package has both passes in train.py.
+ *
+ * Rows behind the last expert's, offsets[E_loc] .. R_cap - 1, are neither read nor written, and no row from
+ * R_cap on is touched whatever the offsets say.  Buffers that a call writes may not overlap those it reads
+ * or each other (MOE_ERR_SHAPE), apart from the exceptions named below.
+ * ------------------------------------------------------------------------------------------------ */
+
+/* moe_grouped_mm flags */
+#define MOE_MM_TRANSPOSED 1u /* w is [E_loc, K, N], contracted along its first axis */
+
+/*
+ * moe_grouped_mm - rows grouped by expert times their expert's matrix.
+ *
+ *   out[r, n] = sum over k < K of a[src(r), k] * w[e][n, k]     for the rows r of expert e (see moe_permute)
+ *   out[r, n] = sum over k < K of a[src(r), k] * w[e][k, n]     with MOE_MM_TRANSPOSED
+ *   src(r) = row_index != NULL ? row_index[r] : r
+ *
+ * With w a projection's weight, [E_loc, out features, in features], the plain form is the projection and
+ * MOE_MM_TRANSPOSED the gradient of its input.  a [a_rows, K] and w of type ``dtype`` (MOE_BF16 or MOE_F32),
+ * out [R_cap, N] of type out_dtype (MOE_BF16 or MOE_F32; MOE_F32 with MOE_F32 operands); products are summed in
+ * fp32 and rounded once.  row_index [R_cap] holds rows of a (others are taken as the nearest row there is);
+ * without it a_rows >= R_cap.  One matrix has fewer than 2^29 values, E_loc <= 1024, R_cap < 2^28.
+ * Errors: MOE_ERR_SHAPE (sizes, an unknown flag, out overlapping an input), MOE_ERR_DTYPE, MOE_ERR_NULL,
+ * MOE_ERR_ALIGN (a, w and out 16 bytes), MOE_ERR_HIP.  R_cap == 0 enqueues nothing.
+ */
+int moe_grouped_mm(const void *a, const int32_t *row_index, int a_rows, const void *w, int dtype, const int32_t *offsets,
+                   int E_loc, int R_cap, int N, int K, void *out, int out_dtype, unsigned flags, void *stream);
+
+/* moe_grouped_wgrad flags */
+#define MOE_WGRAD_ADD 1u /* add to dw instead of overwriting it */
+
+/* Bytes of workspace moe_grouped_wgrad needs (partial sums where few tiles share many rows; else 0). */
+size_t moe_grouped_wgrad_workspace_size(int E_loc, int R_cap, int M, int N, int dtype);
+
+/*
+ * moe_grouped_wgrad - the weight gradient of a grouped product.
+ *
+ *   dw[e][m, n] = (MOE_WGRAD_ADD ? dw[e][m, n] : 0) + sum over the rows r of expert e of a[ia(r), m] * b[ib(r), n]
+ *   ia(r) = a_index != NULL ? a_index[r] : r, and b likewise
+ *
+ * For a projection out = W a: a is the gradient of its output, b its input.  a [a_rows, M] and b [b_rows, N] of
+ * type ``dtype`` (MOE_BF16 or MOE_F32), dw [E_loc, M, N] of type dw_dtype (MOE_BF16 or MOE_F32; MOE_F32 with MOE_F32
+ * operands).  Products are summed in fp32, in an order that the sizes alone fix; with MOE_WGRAD_ADD dw is added in
+ * fp32 and the sum rounded once.  Every matrix is written, those of experts without a row with zeros (or left as
+ * they are with MOE_WGRAD_ADD).  Index and size rules as in moe_grouped_mm.  workspace: at least
+ * moe_grouped_wgrad_workspace_size(...) bytes, 256-byte aligned, contents free before and after.
+ */
+int moe_grouped_wgrad(const void *a, const int32_t *a_index, int a_rows, const void *b, const int32_t *b_index, int b_rows,
+                      int dtype, const int32_t *offsets, int E_loc, int R_cap, int M, int N, void *dw, int dw_dtype,
+                      void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
+ * moe_swiglu - the gated activation between the grouped products, weighted by the row's gate.
+ *
+ *   h[r, i] = row_w[r] * silu(gu[r, i]) * gu[r, I + i],  silu(z) = z / (1 + exp(-z));  row_w NULL: 1
+ *
+ * The gate may multiply h because the down projection is linear: the sum of the unweighted expert outputs is then
+ * the combined output.  gu [R_cap, 2I] (gate, then up) and h [R_cap, I] of type ``dtype`` (MOE_BF16 or MOE_F32), row_w
+ * [R_cap] fp32; computed in fp32, rounded once.  offsets [E_loc + 1] gives the rows there are; NULL: all R_cap
+ * (E_loc is then not read).  Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN (16 bytes), MOE_ERR_HIP.
+ */
+int moe_swiglu(const void *gu, int dtype, const int32_t *offsets, const float *row_w, int E_loc, int R_cap, int I, void *h,
+               void *stream);
+
+/*
+ * moe_swiglu_backward - the gradient of moe_swiglu, with s = 1 / (1 + exp(-g)), g and u the halves of a row of gu:
+ *
+ *   dgu[r, i]     = row_w[r] dh[r, i] u s (1 + g (1 - s))
+ *   dgu[r, I + i] = row_w[r] dh[r, i] g s
+ *   d_row_w[r]    = sum over i of dh[r, i] g s u              (if d_row_w is not NULL)
+ *   h             as moe_swiglu gives it, for the weight gradient of the down projection (if h is not NULL)
+ *
+ * dgu may be gu itself and h may be dh itself.
+ */
+int moe_swiglu_backward(const void *gu, const void *dh, int dtype, const int32_t *offsets, const float *row_w, int E_loc,
+                        int R_cap, int I, void *dgu, void *h, float *d_row_w, void *stream);
+
+/* Bytes of workspace moe_route_backward needs for dw_router or d_bias. */
+size_t moe_route_backward_workspace_size(int T, int k, int H, int E);
+
+/*
+ * moe_route_backward - from the gradient of the gates to those of the router and of the layer's input.
+ *
+ * With g = topk_w[t, :] the softmax over the k selected logits (moe_route) and d = d_topk_w[t, :]:
+ *   dl[t, j]       = g_j (d_j - sum over i of g_i d_i)
+ *   dw_router[e,:] = sum over (t, j) with topk_ids[t, j] == e of dl[t, j] x[t, :]          fp32 [E, H]
+ *   d_bias[e]      = sum over the same of dl[t, j]                                         fp32 [E]
+ *   dx[t, :]       = sum over j of dl[t, j] w_router[topk_ids[t, j], :] + sum over j with rows_at[t, j] >= 0 of
+ *                    rows[rows_at[t, j], :]
+ * ``rows`` [R_cap, H] are the input gradients of the experts' rows (rows_dtype), rows_at [T, k] the token_row of the
+ * local experts' moe_permute; rows NULL: none.  offsets [E + 1], row_token [T*k] and token_row [T, k] are those of
+ * moe_permute over all E experts (e_begin 0, e_end E); a layer that holds them all passes the same maps twice.  They
+ * are read for dw_router and d_bias only.  Outputs that are NULL are not computed.  x [T, H] and w_router [E, H]
+ * of type ``dtype``, dx [T, H] of type dx_dtype (MOE_BF16 or MOE_F32).  Sums in fp32, in an order that the routing
+ * alone fixes.  Gates that other ranks' experts contribute to must be summed over the ranks first.  workspace
+ * (for dw_router or d_bias): at least moe_route_backward_workspace_size(...) bytes, 256-byte aligned, contents free.
+ * T == 0 writes zeros to dw_router and d_bias.
+ * Errors: MOE_ERR_SHAPE (E <= 1024, 1 <= k <= min(E, 32), H <= 2^20, T*k < 2^28, overlapping buffers),
+ * MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_WORKSPACE, MOE_ERR_ALIGN (16 bytes), MOE_ERR_HIP.
+ */
+int moe_route_backward(const int32_t *topk_ids, const float *topk_w, const float *d_topk_w, int T, int k, int E, int H,
+                       const void *x, const void *w_router, int dtype, const int32_t *offsets, const int32_t *row_token,
+                       const int32_t *token_row, const void *rows, int rows_dtype, const int32_t *rows_at, int R_cap,
+                       void *dx, int dx_dtype, float *dw_router, float *d_bias, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* gate_kind of the block norms */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1 /* gate [H] */
+#define MOE_GATE_TOKEN 2   /* gate [T] */
+
+/*
+ * moe_block_norm - the residual around a block, with the RMS norms after it and before the next one.
+ *
+ *   u     = w_post != NULL ? y * rstd_post * w_post : y,        rstd_post = 1 / sqrt(mean(y^2) + eps)
+ *   sum   = scale * x + gate * u                                (gate NULL: 1; y NULL: sum = x)
+ *   x_out = sum,  n = sum * rstd_next * w_next,                 rstd_next = 1 / sqrt(mean(sum^2) + eps)
+ *
+ * x, x_out and n [T, H] of type x_dtype, y [T, H] of type y_dtype (MOE_BF16 or MOE_F32 each; the layer's y is fp32).
+ * w_next [H], w_post [H] and gate ([H] or [T], by gate_kind) of type w_dtype.  Computed in fp32; n is taken from the
+ * sum before that is rounded.  x_out may be NULL, or x itself; n is NULL exactly when w_next is; not both.  rstd_next
+ * and rstd_post [T] fp32 are written if not NULL (a backward pass needs them).  Without y there is no x_out, w_post,
+ * gate, rstd_post, and scale is 1: the norm of x alone.  1 <= H <= 16384, eps > 0.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN (16 bytes), MOE_ERR_HIP.  T == 0 enqueues nothing.
+ */
+int moe_block_norm(const void *x, int x_dtype, const void *y, int y_dtype, const void *w_next, const void *w_post,
+                   const void *gate, int w_dtype, int gate_kind, float scale, float eps, int T, int H, void *x_out, void *n,
+                   float *rstd_next, float *rstd_post, void *stream);
+
+/* Bytes of workspace moe_block_norm_backward needs for dw_next, dw_post and a channel gate's gradient. */
+size_t moe_block_norm_backward_workspace_size(int T, int H);
+
+/*
+ * moe_block_norm_backward - the gradient of moe_block_norm.
+ *
+ * With x_out the sum that the forward call gave (x without y), xh = x_out * rstd_next, yh = y * rstd_post:
+ *   D       = dx_out + rstd_next * (dn w_next - xh * mean(dn w_next xh))       (a NULL dx_out or dn: without its term)
+ *   dx      = scale * D
+ *   du      = gate * D,  dv = du * w_post,  dy = rstd_post * (dv - yh * mean(dv yh))   (w_post NULL: dy = du)
+ *   dw_next = sum over t of dn xh,  dw_post = sum over t of du yh                fp32 [H]
+ *   d_gate  = sum over t ([H]) or over the row ([T]) of D u                      fp32
+ * dx of type x_dtype, dy of type y_dtype.  Outputs that are NULL are not computed.  dx may be dx_out or dn itself.
+ * dx_out and dn are of type x_dtype; not both NULL.  workspace (for dw_next, dw_post and a channel gate): at least
+ * moe_block_norm_backward_workspace_size(T, H) bytes, 256-byte aligned, contents free.  The sums over t have an order
+ * that T alone fixes.  T == 0 writes zeros to dw_next, dw_post and a channel gate's gradient.
+ */
+int moe_block_norm_backward(const void *x_out, int x_dtype, const void *y, int y_dtype, const void *w_next,
+                            const void *w_post, const void *gate, int w_dtype, int gate_kind, float scale,
+                            const float *rstd_next, const float *rstd_post, const void *dx_out, const void *dn, int T, int H,
+                            void *dx, void *dy, float *dw_next, float *dw_post, float *d_gate, void *workspace,
+                            size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
