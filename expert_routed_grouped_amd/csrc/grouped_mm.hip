@@ -309,6 +309,7 @@ hipError_t launch_wgrad(const train::WgradArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t train::launch_grouped_mm(const MmArgs &a, hipStream_t s) {
+  if (a.R_cap > 32LL * a.El && mm_dma_fits(a)) return launch_mm_dma(a, s);
   if (!a.bf16) return pick_mm<float, float>(a, s);
   return a.out_bf16 ? pick_mm<uint16_t, uint16_t>(a, s) : pick_mm<uint16_t, float>(a, s);
 }
@@ -316,6 +317,7 @@ hipError_t train::launch_grouped_mm(const MmArgs &a, hipStream_t s) {
 size_t train::wgrad_ws_bytes(int El, int R_cap, int M, int N, int bf16) { return 0; }
 
 hipError_t train::launch_grouped_wgrad(const WgradArgs &a, hipStream_t s) {
+  if (wgrad_dma_fits(a)) return launch_wgrad_dma(a, s);
   if (!a.bf16) return a.out_bf16 ? hipErrorInvalidValue : launch_wgrad<float, float>(a, s);
   return a.out_bf16 ? launch_wgrad<uint16_t, uint16_t>(a, s) : launch_wgrad<uint16_t, float>(a, s);
 }

@@ -1,0 +1,410 @@
+// Products of rows grouped by expert on bf16 operands whose rows are whole 16-byte pieces: tiles that go from memory
+// straight to LDS (moe_grouped_mm, moe_grouped_wgrad).
+//
+// One kernel for three products, by how an operand lies in memory.  A "k-major" operand has its contraction along its
+// rows (activations; weights of a projection): its tile keeps rows of 64 values in LDS, 16-byte chunk c of row r in slot
+// c ^ (r / 2 % 8), and a fragment of v_mfma_f32_32x32x16_bf16 is one 16-byte LDS read.  An "mn-major" operand has an output
+// axis along its rows (weights for an input gradient; both operands of a weight gradient): its tile keeps whole k rows,
+// and a fragment is two transposing 8-byte LDS reads, each four k rows of 16 columns.  The 32-byte pieces p of k row r lie
+// at p ^ (2 (r % 4) + r / 8 % 2), so that the four rows of two neighbouring pieces, which half a wave reads at once,
+// meet all 64 banks.
+//
+// Tiles of 256 x 256 outputs, eight waves of 128 x 64, 64 values of the contraction a step; the second operand, whose
+// first touch comes from memory, is fetched two steps ahead through three slots, the first one step ahead through two
+// (160 KB of LDS).
+#include "ffn_common.h"
+#include "train.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace {
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
+constexpr uint32_t kRsrcWord3 = 0x00020000;  // raw buffer, 32-bit data format
+constexpr uint32_t kNowhere = 0x80000000u;   // byte offset behind every buffer: such a load gives zeros
+
+__device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::: "memory"); }
+
+// Rows (output axis) and waves of a tile, slots of the two operands.
+template <int BM_, int BN_, int BK_, int WM_, int WN_, int SA_, int SB_>
+struct Cfg {
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, SA = SA_, SB = SB_;
+  static constexpr int NW = WM * WN, NTHR = 64 * NW;
+  static constexpr int MB = BM / WM / 32, NB = BN / WN / 32;       // 32-row blocks of a wave
+  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
+  static constexpr int NA = A_BYTES / 1024 / NW, NBL = B_BYTES / 1024 / NW;  // loads of a wave and step
+  static constexpr int LDS = SA * A_BYTES + SB * B_BYTES;
+  static_assert(NA >= 1 && NBL >= 1 && LDS <= 160 * 1024, "whole loads, one compute unit's LDS");
+};
+
+// What a wave loads of an operand: byte offsets of its N segments of 1 KB at step 0, and their advance.
+template <int N, int NW>
+struct Source {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t off[N];
+  uint32_t step;    // bytes from one step to the next
+  uint32_t last;    // or-ed into a lane's offset in the last step: kNowhere where that is past the contraction's end
+  __device__ __forceinline__ void ahead(int, int) {}
+  __device__ __forceinline__ void load(char *to, int wave, int, int kt, bool is_last) {
+    const uint32_t so = (uint32_t)kt * step, m = is_last ? last : 0u;
+#pragma unroll
+    for (int u = 0; u < N; u++)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + (wave + NW * u) * 1024), 16, off[u] | m, so, 0, 0);
+  }
+  // k-major tile, BK = 64: segment s holds rows 8s .. 8s + 7.  ``row`` maps a tile row to its byte offset.
+  template <typename F>
+  __device__ __forceinline__ void k_major(int wave, int lane, int K, F row) {
+    static_assert(NW % 2 == 0, "a lane's chunk is the same in all of its segments");
+    int chunk = 0;
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      const int t = (wave + NW * u) * 8 + (lane >> 3);
+      chunk = (lane & 7) ^ ((t >> 1) & 7);
+      off[u] = row(t) + (uint32_t)chunk * 16u;
+    }
+    step = 128;
+    last = (K & 63) != 0 && chunk * 8 >= (K & 63) ? kNowhere : 0u;
+  }
+  // mn-major tile of R columns from byte ``col`` of rows that lie ``ld`` bytes apart, BK k rows a step.
+  template <int R, int BK>
+  __device__ __forceinline__ void mn_major(int wave, int lane, uint32_t ld, uint32_t col) {
+#pragma unroll
+    for (int u = 0; u < N; u++) off[u] = (uint32_t)k_row<R>(wave + NW * u, lane) * ld + col + in_row<R>(wave + NW * u, lane);
+    step = BK * ld;
+    last = 0;
+  }
+  // A segment of an mn-major tile holds 512 / R k rows; a lane's k row, and its byte of it.
+  template <int R>
+  static __device__ __forceinline__ int k_row(int seg, int lane) {
+    return seg * (512 / R) + lane / (R / 8);
+  }
+  template <int R>
+  static __device__ __forceinline__ uint32_t in_row(int seg, int lane) {
+    const int k = k_row<R>(seg, lane), slot = lane % (R / 8);
+    return (uint32_t)((slot >> 1) ^ (2 * (k & 3) + ((k >> 3) & 1))) * 32u + (uint32_t)(slot & 1) * 16u;
+  }
+};
+
+// The same for an mn-major operand whose k rows are gathered, 32 a step: a lane holds the source of one of the next
+// step's rows, loaded a step before it is used, and the rows' byte offsets go round by a shuffle.
+template <int N, int NW>
+struct Gathered {
+  using S = Source<N, NW>;
+  __amdgpu_buffer_rsrc_t r;
+  const int32_t *index;
+  int rows, limit;
+  uint32_t ld, at[N];
+  int k[N], next;
+  template <int R>
+  __device__ __forceinline__ void mn_major(int wave, int lane, uint32_t ld_, uint32_t col) {
+    ld = ld_;
+#pragma unroll
+    for (int u = 0; u < N; u++) k[u] = S::template k_row<R>(wave + NW * u, lane), at[u] = col + S::template in_row<R>(wave + NW * u, lane);
+  }
+  __device__ __forceinline__ void ahead(int lane, int kt) {
+    const int t = kt * 32 + (lane & 31);
+    next = index[min(t, rows - 1)];
+  }
+  __device__ __forceinline__ void load(char *to, int wave, int lane, int kt, bool) {
+    const int t = kt * 32 + (lane & 31);
+    const uint32_t row = t < rows ? (uint32_t)min(max(next, 0), limit - 1) * ld : kNowhere;
+#pragma unroll
+    for (int u = 0; u < N; u++)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + (wave + NW * u) * 1024), 16, __shfl(row, k[u], 64) + at[u], 0,
+                                               0, 0);
+  }
+};
+
+// LDS bytes of a lane's fragments of blocks of 32 rows from row r0 on: of block b in slice kk of 16 values.
+template <bool MN, int R, int B>
+struct Frag {
+  uint32_t base[MN ? B : 4];
+  __device__ __forceinline__ Frag(int r0, int lane) {
+    if constexpr (MN) {
+      const int i = lane & 15, h = (lane >> 4) & 1, g = lane >> 5;
+#pragma unroll
+      for (int b = 0; b < B; b++)
+        base[b] = (uint32_t)(8 * g + (i >> 2)) * (R * 2) + (uint32_t)((r0 / 16 + 2 * b + h) ^ (2 * (i >> 2) + g)) * 32u +
+                  (uint32_t)(i & 3) * 8u;
+    } else {
+      const int n = lane & 31, g = lane >> 5;
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++) base[kk] = (uint32_t)(r0 + n) * 128u + (uint32_t)((2 * kk + g) ^ ((n >> 1) & 7)) * 16u;
+    }
+  }
+  __device__ __forceinline__ bf16x8_t get(const char *slot, int kk, int b) const {
+    if constexpr (MN) {
+      const char *p = slot + base[b] + kk * 16 * (R * 2);
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * (R * 2)));
+      const uint2 x = __builtin_bit_cast(uint2, lo), y = __builtin_bit_cast(uint2, hi);
+      return __builtin_bit_cast(bf16x8_t, u32x4_t{x.x, x.y, y.x, y.y});
+    } else {
+      return *(const bf16x8_t *)(slot + base[kk] + b * 4096);
+    }
+  }
+};
+
+// The contraction of one tile.  MB: 32-row blocks of A that hold rows (0: this wave only loads).
+template <typename C, bool AMN, bool BMN, int MB, typename SrcA, typename SrcB, typename Acc>
+__device__ __forceinline__ void contract(SrcA &sa, SrcB &sb, int KT, int wave, int lane, int m0, int n0, char *lds,
+                                         Acc &acc) {
+  constexpr int M1 = MB > 0 ? MB : 1, U = C::SA * C::SB, KK = C::BK / 16;
+  const Frag<AMN, C::BM, M1> fa(m0, lane);
+  const Frag<BMN, C::BN, C::NB> fb(n0, lane);
+  char *const la = lds, *const lb = lds + C::SA * C::A_BYTES;
+#pragma unroll
+  for (int i = 0; i < M1; i++)
+#pragma unroll
+    for (int j = 0; j < C::NB; j++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
+  // Steps before the loop, the oldest first; within a step A before B.  Once only the younger steps' loads are in flight,
+  // a step has landed.
+#pragma unroll
+  for (int t = 0; t < C::SB - 1; t++) {
+    if (t >= KT) break;
+    if (t < C::SA - 1) {
+      sa.ahead(lane, t);
+      sa.load(la + t * C::A_BYTES, wave, lane, t, t == KT - 1);
+    }
+    sb.ahead(lane, t);
+    sb.load(lb + t * C::B_BYTES, wave, lane, t, t == KT - 1);
+  }
+  sa.ahead(lane, C::SA - 1);
+  sb.ahead(lane, C::SB - 1);
+  constexpr int YOUNG = C::NA * (C::SA - 2) + C::NBL * (C::SB - 2);
+  static_assert(C::SA <= 3 && C::SB == 3, "the wait below counts one younger step");
+  auto step = [&](auto PC, int kt) __attribute__((always_inline)) {
+    constexpr int P = decltype(PC)::value, A0 = P % C::SA, B0 = P % C::SB;
+    constexpr int A1 = (P + C::SA - 1) % C::SA, B1 = (P + C::SB - 1) % C::SB;
+    if (kt >= KT) return;
+    if (kt + 1 < KT) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(YOUNG) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    barrier_no_fence();
+    const int na = kt + C::SA - 1, nb = kt + C::SB - 1;
+    auto load_a = [&]() __attribute__((always_inline)) {
+      if (na < KT) sa.load(la + A1 * C::A_BYTES, wave, lane, na, na == KT - 1);
+      sa.ahead(lane, na + 1);
+    };
+    auto load_b = [&]() __attribute__((always_inline)) {
+      if (nb < KT) sb.load(lb + B1 * C::B_BYTES, wave, lane, nb, nb == KT - 1);
+      sb.ahead(lane, nb + 1);
+    };
+    const char *a = la + A0 * C::A_BYTES, *b = lb + B0 * C::B_BYTES;
+    bf16x8_t af[2][M1], bf[2][C::NB];
+    auto frags = [&](int kk) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < C::NB; j++) bf[kk & 1][j] = fb.get(b, kk, j);
+#pragma unroll
+      for (int i = 0; i < M1; i++) af[kk & 1][i] = fa.get(a, kk, i);
+    };
+    if constexpr (MB > 0) frags(0);
+#pragma unroll
+    for (int kk = 0; kk < KK; kk++) {
+      if constexpr (MB > 0) {
+        if (kk + 1 < KK) frags(kk + 1);
+      }
+      if (kk == 0) load_a();
+      if (kk == KK / 2) load_b();
+      if constexpr (MB > 0) {
+#pragma unroll
+        for (int i = 0; i < MB; i++)
+#pragma unroll
+          for (int j = 0; j < C::NB; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[kk & 1][i], bf[kk & 1][j], acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+  constexpr int L = C::SA == C::SB ? C::SA : U;  // steps until the slots repeat
+  for (int kt = 0; kt < KT; kt += L) {
+    step(std::integral_constant<int, 0>{}, kt);
+    step(std::integral_constant<int, 1>{}, kt + 1);
+    step(std::integral_constant<int, 2>{}, kt + 2);
+    if constexpr (L > 3) {
+      step(std::integral_constant<int, 3>{}, kt + 3);
+      step(std::integral_constant<int, 4>{}, kt + 4);
+      step(std::integral_constant<int, 5>{}, kt + 5);
+    }
+  }
+}
+
+// acc[i][j][r] at lane l: tile row m0 + 32 i + 8 (r / 4) + 4 (l / 32) + r % 4, column n0 + 32 j + l % 32.
+template <int MB, int NB, typename TO>
+__device__ __forceinline__ void store(const f32x16_t (&acc)[MB][NB], TO *out, size_t ld, int m0, int n0, int rows, int cols,
+                                      int lane, bool add) {
+#pragma unroll
+  for (int j = 0; j < NB; j++) {
+    const int n = n0 + 32 * j + (lane & 31);
+    if (n >= cols) continue;
+#pragma unroll
+    for (int i = 0; i < MB; i++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) {
+        const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        if (m < rows) {
+          TO *o = out + (size_t)m * ld + n;
+          train::put(o, add ? train::to_f32(*o) + acc[i][j][r] : acc[i][j][r]);
+        }
+      }
+  }
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *p, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, (int)(uint32_t)bytes, kRsrcWord3);
+}
+
+using Mm = Cfg<256, 256, 64, 2, 4, 2, 3>;
+
+template <bool KN, bool GATHER, typename TO>
+__global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) void mm_dma_kernel(train::MmArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone
+  using C = Mm;
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  ffn::TileParams tp{};
+  tp.offsets = p.offsets;
+  tp.El = p.El;
+  tp.R_cap = p.R_cap;
+  int e, nt, mt, mtiles;
+  if (!ffn::locate_tile<C::BM>(tp, (p.N + C::BN - 1) / C::BN, e, nt, mt, mtiles)) return;
+  e = __builtin_amdgcn_readfirstlane(e);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  mtiles = __builtin_amdgcn_readfirstlane(mtiles);
+  // an expert's rows split evenly over its tiles, rounded up to 64
+  const int beg = p.offsets[e], cnt = p.offsets[e + 1] - beg;
+  const int trows = __builtin_amdgcn_readfirstlane(min(C::BM, (((cnt + mtiles - 1) / mtiles) + 63) & ~63));
+  const int r0 = beg + mt * trows, rows = min(trows, min(beg + cnt, p.R_cap) - r0);
+  if (rows <= 0 || r0 < 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = trows >> 1, wm = wave / C::WN, wn = wave % C::WN, valid = rows - wm * half;
+  const int mb = __builtin_amdgcn_readfirstlane(valid <= 0 ? 0 : min(half >> 5, (valid + 31) >> 5));
+  const int K = p.K, KT = (K + C::BK - 1) / C::BK;
+
+  Source<C::NA, C::NW> sa;
+  const size_t lda = (size_t)K * 2;
+  if constexpr (GATHER) sa.r = resource(p.a, (size_t)p.a_rows * lda);
+  else sa.r = resource((const char *)p.a + r0 * lda, (size_t)rows * lda);
+  sa.k_major(wave, lane, K, [&](int r) {
+    const int at = min(r, rows - 1);  // rows past the end repeat the last one; nothing of them is stored
+    return (uint32_t)(GATHER ? min(max(p.a_index[r0 + at], 0), p.a_rows - 1) : at) * (uint32_t)lda;
+  });
+  Source<C::NBL, C::NW> sb;
+  sb.r = resource((const char *)p.w + (size_t)e * p.N * K * 2, (size_t)p.N * K * 2);
+  if constexpr (KN) {
+    sb.template mn_major<C::BN, C::BK>(wave, lane, (uint32_t)p.N * 2u, nt * C::BN * 2u);
+  } else {
+    sb.k_major(wave, lane, K, [&](int r) { return (uint32_t)min(nt * C::BN + r, p.N - 1) * (uint32_t)lda; });
+  }
+  const int m0 = wm * half, n0 = wn * (C::NB * 32);
+  TO *out = (TO *)p.out + (size_t)r0 * p.N + nt * C::BN;
+  auto body = [&](auto MC) __attribute__((always_inline)) {
+    constexpr int MB = decltype(MC)::value;
+    f32x16_t acc[MB > 0 ? MB : 1][C::NB];
+    contract<C, false, KN, MB>(sa, sb, KT, wave, lane, m0, n0, lds, acc);
+    if constexpr (MB > 0) store(acc, out, p.N, m0, n0, rows, p.N - nt * C::BN, lane, false);
+  };
+  switch (mb) {
+    case 0: body(std::integral_constant<int, 0>{}); break;
+    case 1: body(std::integral_constant<int, 1>{}); break;
+    case 2: body(std::integral_constant<int, 2>{}); break;
+    case 3: body(std::integral_constant<int, 3>{}); break;
+    default: body(std::integral_constant<int, 4>{}); break;
+  }
+#endif
+}
+
+template <bool KN, bool GATHER, typename TO>
+hipError_t launch(const train::MmArgs &a, hipStream_t s) {
+  const long long mt = std::min(((long long)a.R_cap + (long long)a.El * (Mm::BM - 1)) / Mm::BM, (long long)a.R_cap);
+  hipLaunchKernelGGL((mm_dma_kernel<KN, GATHER, TO>), dim3((unsigned)(mt * ceil_div_i(a.N, Mm::BN))), dim3(Mm::NTHR), 0, s, a);
+  return hipGetLastError();
+}
+template <bool KN, bool GATHER>
+hipError_t by_out(const train::MmArgs &a, hipStream_t s) {
+  return a.out_bf16 ? launch<KN, GATHER, uint16_t>(a, s) : launch<KN, GATHER, float>(a, s);
+}
+template <bool KN>
+hipError_t by_index(const train::MmArgs &a, hipStream_t s) {
+  return a.a_index ? by_out<KN, true>(a, s) : by_out<KN, false>(a, s);
+}
+
+using Wg = Cfg<256, 128, 32, 2, 2, 3, 3>;
+
+template <bool GA, bool GB, typename TO>
+__global__ __launch_bounds__(Wg::NTHR, 2) __attribute__((amdgpu_waves_per_eu(2, 2))) void wgrad_dma_kernel(train::WgradArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using C = Wg;
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  const int MT = (p.M + C::BM - 1) / C::BM, NT = (p.N + C::BN - 1) / C::BN;
+  // Workgroups go round-robin over the 8 XCDs; runs of 32 neighbouring tiles, which share operands, go to one XCD.
+  const int j = blockIdx.x >> 3, t = ((j >> 5) * 8 + (blockIdx.x & 7)) * 32 + (j & 31);
+  if (t >= p.El * MT * NT) return;
+  const int e = t / (MT * NT), mt = t / NT % MT, nt = t % NT;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r0 = max(p.offsets[e], 0), rows = max(min(p.offsets[e + 1], p.R_cap) - r0, 0);
+  const int KT = (rows + C::BK - 1) / C::BK;
+  std::conditional_t<GA, Gathered<C::NA, C::NW>, Source<C::NA, C::NW>> sa;
+  std::conditional_t<GB, Gathered<C::NBL, C::NW>, Source<C::NBL, C::NW>> sb;
+  auto place = [&](auto &s, auto RC, const void *base, const int32_t *index, int have, uint32_t ld, int col)
+                   __attribute__((always_inline)) {
+    constexpr int R = decltype(RC)::value;
+    if constexpr (std::is_same_v<std::decay_t<decltype(s)>, Gathered<R == C::BM ? C::NA : C::NBL, C::NW>>) {
+      s.r = resource(base, (size_t)have * ld);
+      s.index = index + r0;
+      s.rows = rows;
+      s.limit = have;
+      s.template mn_major<R>(wave, lane, ld, (uint32_t)col * 2u);
+    } else {
+      s.r = resource((const char *)base + (size_t)r0 * ld, (size_t)rows * ld);
+      s.template mn_major<R, C::BK>(wave, lane, ld, (uint32_t)col * 2u);
+    }
+  };
+  place(sa, std::integral_constant<int, C::BM>{}, p.a, p.a_index, p.a_rows, (uint32_t)p.M * 2u, mt * C::BM);
+  place(sb, std::integral_constant<int, C::BN>{}, p.b, p.b_index, p.b_rows, (uint32_t)p.N * 2u, nt * C::BN);
+  const int m0 = wave / C::WN * (C::MB * 32), n0 = wave % C::WN * (C::NB * 32);
+  f32x16_t acc[C::MB][C::NB];
+  if (KT > 0) contract<C, true, true, C::MB>(sa, sb, KT, wave, lane, m0, n0, lds, acc);
+  else {
+#pragma unroll
+    for (int i = 0; i < C::MB; i++)
+#pragma unroll
+      for (int jj = 0; jj < C::NB; jj++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) acc[i][jj][r] = 0.0f;
+  }
+  TO *out = (TO *)p.dw + ((size_t)e * p.M + mt * C::BM) * p.N + nt * C::BN;
+  store(acc, out, p.N, m0, n0, p.M - mt * C::BM, p.N - nt * C::BN, lane, p.add);
+#endif
+}
+
+}  // namespace
+
+// bf16 rows of whole 16-byte pieces, every 32-bit byte offset below kNowhere.
+bool train::mm_dma_fits(const MmArgs &a) {
+  const long long lim = 1LL << 31;
+  return a.bf16 && a.K % 8 == 0 && (!a.kn || a.N % 8 == 0) && (long long)a.N * a.K * 2 < lim &&
+         (a.a_index ? (long long)a.a_rows * a.K * 2 < lim : 256LL * a.K * 2 < lim);
+}
+template <bool GA, bool GB>
+static hipError_t wgrad_by_out(const train::WgradArgs &a, hipStream_t s) {
+  const long long tiles = (long long)a.El * ceil_div_i(a.M, Wg::BM) * ceil_div_i(a.N, Wg::BN);
+  const dim3 grid((unsigned)((tiles + 255) / 256 * 256)), block(Wg::NTHR);
+  if (a.out_bf16) hipLaunchKernelGGL((wgrad_dma_kernel<GA, GB, uint16_t>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((wgrad_dma_kernel<GA, GB, float>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+bool train::wgrad_dma_fits(const WgradArgs &a) {
+  const long long lim = 1LL << 31;
+  return a.bf16 && a.M % 8 == 0 && a.N % 8 == 0 && a.M >= 128 && a.N >= 64 &&
+         (long long)(a.a_index ? a.a_rows : a.R_cap) * a.M * 2 < lim && (long long)(a.b_index ? a.b_rows : a.R_cap) * a.N * 2 < lim;
+}
+hipError_t train::launch_wgrad_dma(const WgradArgs &a, hipStream_t s) {
+  if (a.a_index) return a.b_index ? wgrad_by_out<true, true>(a, s) : wgrad_by_out<true, false>(a, s);
+  return a.b_index ? wgrad_by_out<false, true>(a, s) : wgrad_by_out<false, false>(a, s);
+}
+
+hipError_t train::launch_mm_dma(const MmArgs &a, hipStream_t s) { return a.kn ? by_index<true>(a, s) : by_index<false>(a, s); }

@@ -17,6 +17,8 @@ struct MmArgs {
   int bf16, out_bf16, kn;
 };
 hipError_t launch_grouped_mm(const MmArgs &a, hipStream_t s);
+bool mm_dma_fits(const MmArgs &a);  // grouped_mm_dma.hip
+hipError_t launch_mm_dma(const MmArgs &a, hipStream_t s);
 
 // dw[e] = sum over e's rows of a_r b_r^T (+ dw[e] with add).
 struct WgradArgs {
@@ -31,6 +33,8 @@ struct WgradArgs {
 };
 size_t wgrad_ws_bytes(int El, int R_cap, int M, int N, int bf16);
 hipError_t launch_grouped_wgrad(const WgradArgs &a, hipStream_t s);
+bool wgrad_dma_fits(const WgradArgs &a);  // grouped_mm_dma.hip
+hipError_t launch_wgrad_dma(const WgradArgs &a, hipStream_t s);
 
 // h = row_w silu(gate) up; offsets NULL: every one of the R_cap rows.
 struct SwigluArgs {
