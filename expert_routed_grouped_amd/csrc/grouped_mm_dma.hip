@@ -28,6 +28,31 @@ constexpr uint32_t kNowhere = 0x80000000u;   // byte offset behind every buffer:
 
 __device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::: "memory"); }
 
+// Sixteen bytes a lane from memory to 1 KB of LDS at byte ``to``.  In assembly, because the compiler waits for every load to
+// LDS that it knows of before a transposing LDS read (vmcnt(0) twice a step); nothing comes back in registers, and the waits
+// for LDS are the kernel's own.  M0 is written one wait state before its use.
+typedef uint32_t rsrc_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void dma(rsrc_t r, uint32_t to, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff), "s"(r), "s"(soff)
+               : "m0");
+}
+// The same for four bytes a lane.
+__device__ __forceinline__ void dma_words(rsrc_t r, uint32_t to, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(voff), "s"(r) : "m0");
+}
+// A buffer of ``bytes`` bytes.  The words come out of vector registers: five wait states before a load may read them.
+__device__ __forceinline__ rsrc_t resource(const void *p, size_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  rsrc_t r;
+  r.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  r.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xffffu);
+  r.z = __builtin_amdgcn_readfirstlane((uint32_t)bytes);
+  r.w = kRsrcWord3;
+  asm volatile("s_nop 7" : "+s"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_at(const char *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
+
 // Rows (output axis) and waves of a tile, slots of the two operands.
 template <int BM_, int BN_, int BK_, int WM_, int WN_, int SA_, int SB_>
 struct Cfg {
@@ -37,22 +62,24 @@ struct Cfg {
   static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
   static constexpr int NA = A_BYTES / 1024 / NW, NBL = B_BYTES / 1024 / NW;  // loads of a wave and step
   static constexpr int LDS = SA * A_BYTES + SB * B_BYTES;
+  static constexpr int OUT = 32 * (NB * 32 * 4 + 16);              // a wave's 32 rows of outputs, up to fp32
+  static_assert(NW * OUT <= LDS, "the outputs go through the operands' LDS");
   static_assert(NA >= 1 && NBL >= 1 && LDS <= 160 * 1024, "whole loads, one compute unit's LDS");
 };
 
 // What a wave loads of an operand: byte offsets of its N segments of 1 KB at step 0, and their advance.
 template <int N, int NW>
 struct Source {
-  __amdgpu_buffer_rsrc_t r;
+  static constexpr int LOADS = N;  // loads of a step
+  rsrc_t r;
   uint32_t off[N];
   uint32_t step;    // bytes from one step to the next
   uint32_t last;    // or-ed into a lane's offset in the last step: kNowhere where that is past the contraction's end
-  __device__ __forceinline__ void ahead(int, int) {}
-  __device__ __forceinline__ void load(char *to, int wave, int, int kt, bool is_last) {
+  __device__ __forceinline__ void start(int) {}
+  __device__ __forceinline__ void load(uint32_t to, int wave, int, int kt, bool is_last) {
     const uint32_t so = (uint32_t)kt * step, m = is_last ? last : 0u;
 #pragma unroll
-    for (int u = 0; u < N; u++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + (wave + NW * u) * 1024), 16, off[u] | m, so, 0, 0);
+    for (int u = 0; u < N; u++) dma(r, to + (wave + NW * u) * 1024, off[u] | m, so);
   }
   // k-major tile, BK = 64: segment s holds rows 8s .. 8s + 7.  ``row`` maps a tile row to its byte offset.
   template <typename F>
@@ -88,16 +115,16 @@ struct Source {
   }
 };
 
-// The same for an mn-major operand whose k rows are gathered, 32 a step: a lane holds the source of one of the next
-// step's rows, loaded a step before it is used, and the rows' byte offsets go round by a shuffle.
+// The same for an mn-major operand whose k rows are gathered, 32 a step.  The indexes of a step's rows go to LDS too, two
+// steps before its rows do: a register load would have to be waited for with everything that is younger.
 template <int N, int NW>
 struct Gathered {
   using S = Source<N, NW>;
-  __amdgpu_buffer_rsrc_t r;
-  const int32_t *index;
+  static constexpr int LOADS = N + 1;
+  rsrc_t r, ri;
   int rows, limit;
-  uint32_t ld, at[N];
-  int k[N], next;
+  uint32_t ld, at[N], words;  // words: LDS of this wave's indexes, two steps of 256 bytes
+  int k[N];
   template <int R>
   __device__ __forceinline__ void mn_major(int wave, int lane, uint32_t ld_, uint32_t col) {
     ld = ld_;
@@ -105,16 +132,21 @@ struct Gathered {
     for (int u = 0; u < N; u++) k[u] = S::template k_row<R>(wave + NW * u, lane), at[u] = col + S::template in_row<R>(wave + NW * u, lane);
   }
   __device__ __forceinline__ void ahead(int lane, int kt) {
-    const int t = kt * 32 + (lane & 31);
-    next = index[min(t, rows - 1)];
+    dma_words(ri, words + (kt & 1) * 256, (uint32_t)min(kt * 32 + (lane & 31), rows - 1) * 4u);
   }
-  __device__ __forceinline__ void load(char *to, int wave, int lane, int kt, bool) {
-    const int t = kt * 32 + (lane & 31);
-    const uint32_t row = t < rows ? (uint32_t)min(max(next, 0), limit - 1) * ld : kNowhere;
+  __device__ __forceinline__ void start(int lane) {
+    ahead(lane, 0);
+    ahead(lane, 1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  __device__ __forceinline__ void load(uint32_t to, int wave, int lane, int kt, bool) {
+    const __attribute__((address_space(3))) int *const w = (const __attribute__((address_space(3))) int *)(uintptr_t)(words + (kt & 1) * 256);
+    uint32_t row[N];
 #pragma unroll
-    for (int u = 0; u < N; u++)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + (wave + NW * u) * 1024), 16, __shfl(row, k[u], 64) + at[u], 0,
-                                               0, 0);
+    for (int u = 0; u < N; u++) row[u] = kt * 32 + k[u] < rows ? (uint32_t)min(max(w[k[u]], 0), limit - 1) * ld : kNowhere;
+#pragma unroll
+    for (int u = 0; u < N; u++) dma(r, to + (wave + NW * u) * 1024, row[u] + at[u], 0);
+    ahead(lane, kt + 2);  // into the words that were just used
   }
 };
 
@@ -156,44 +188,34 @@ __device__ __forceinline__ void contract(SrcA &sa, SrcB &sb, int KT, int wave, i
   const Frag<AMN, C::BM, M1> fa(m0, lane);
   const Frag<BMN, C::BN, C::NB> fb(n0, lane);
   char *const la = lds, *const lb = lds + C::SA * C::A_BYTES;
+  const uint32_t ta = lds_at(la), tb = lds_at(lb);
 #pragma unroll
   for (int i = 0; i < M1; i++)
 #pragma unroll
     for (int j = 0; j < C::NB; j++)
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
-  // Steps before the loop, the oldest first; within a step A before B.  Once only the younger steps' loads are in flight,
-  // a step has landed.
+  // Steps before the loop, the oldest first; within a step A before B.  Once only the younger step's loads are in flight,
+  // a step has landed, and so have the indexes that were asked for with it.
+  sa.start(lane);
+  sb.start(lane);
 #pragma unroll
   for (int t = 0; t < C::SB - 1; t++) {
     if (t >= KT) break;
-    if (t < C::SA - 1) {
-      sa.ahead(lane, t);
-      sa.load(la + t * C::A_BYTES, wave, lane, t, t == KT - 1);
-    }
-    sb.ahead(lane, t);
-    sb.load(lb + t * C::B_BYTES, wave, lane, t, t == KT - 1);
+    if (t < C::SA - 1) sa.load(ta + t * C::A_BYTES, wave, lane, t, t == KT - 1);
+    sb.load(tb + t * C::B_BYTES, wave, lane, t, t == KT - 1);
   }
-  sa.ahead(lane, C::SA - 1);
-  sb.ahead(lane, C::SB - 1);
-  constexpr int YOUNG = C::NA * (C::SA - 2) + C::NBL * (C::SB - 2);
-  static_assert(C::SA <= 3 && C::SB == 3, "the wait below counts one younger step");
+  constexpr int YOUNG = SrcA::LOADS * (C::SA - 2) + SrcB::LOADS * (C::SB - 2);
+  static_assert((C::SA == 2 || C::SA == 3) && C::SB == 3, "the wait below counts one younger step");
   auto step = [&](auto PC, int kt) __attribute__((always_inline)) {
     constexpr int P = decltype(PC)::value, A0 = P % C::SA, B0 = P % C::SB;
     constexpr int A1 = (P + C::SA - 1) % C::SA, B1 = (P + C::SB - 1) % C::SB;
     if (kt >= KT) return;
-    if (kt + 1 < KT) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(YOUNG) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // this wave's loads of the step have landed, and it has read its last fragments of the step before
+    if (kt + 1 < KT) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNG) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     barrier_no_fence();
     const int na = kt + C::SA - 1, nb = kt + C::SB - 1;
-    auto load_a = [&]() __attribute__((always_inline)) {
-      if (na < KT) sa.load(la + A1 * C::A_BYTES, wave, lane, na, na == KT - 1);
-      sa.ahead(lane, na + 1);
-    };
-    auto load_b = [&]() __attribute__((always_inline)) {
-      if (nb < KT) sb.load(lb + B1 * C::B_BYTES, wave, lane, nb, nb == KT - 1);
-      sb.ahead(lane, nb + 1);
-    };
     const char *a = la + A0 * C::A_BYTES, *b = lb + B0 * C::B_BYTES;
     bf16x8_t af[2][M1], bf[2][C::NB];
     auto frags = [&](int kk) __attribute__((always_inline)) {
@@ -208,14 +230,14 @@ __device__ __forceinline__ void contract(SrcA &sa, SrcB &sb, int KT, int wave, i
       if constexpr (MB > 0) {
         if (kk + 1 < KK) frags(kk + 1);
       }
-      if (kk == 0) load_a();
-      if (kk == KK / 2) load_b();
+      if (kk == 0 && na < KT) sa.load(ta + A1 * C::A_BYTES, wave, lane, na, na == KT - 1);
+      if (kk == KK / 2 && nb < KT) sb.load(tb + B1 * C::B_BYTES, wave, lane, nb, nb == KT - 1);
       if constexpr (MB > 0) {
 #pragma unroll
         for (int i = 0; i < MB; i++)
 #pragma unroll
           for (int j = 0; j < C::NB; j++)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[kk & 1][i], bf[kk & 1][j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[kk & 1][j], af[kk & 1][i], acc[i][j], 0, 0, 0);
       }
     }
   };
@@ -232,29 +254,46 @@ __device__ __forceinline__ void contract(SrcA &sa, SrcB &sb, int KT, int wave, i
   }
 }
 
-// acc[i][j][r] at lane l: tile row m0 + 32 i + 8 (r / 4) + 4 (l / 32) + r % 4, column n0 + 32 j + l % 32.
-template <int MB, int NB, typename TO>
-__device__ __forceinline__ void store(const f32x16_t (&acc)[MB][NB], TO *out, size_t ld, int m0, int n0, int rows, int cols,
-                                      int lane, bool add) {
+// A wave's outputs, 32 rows at a time through LDS of its own, so that a store writes whole rows of the wave's columns:
+// acc[i][j][r] at lane l is tile row m0 + 32 i + l % 32, column n0 + 32 j + 8 (r / 4) + 4 (l / 32) + r % 4.  Two-byte stores
+// straight from the accumulators cost 440 of 1144 us of a weight gradient.  ADD: to what is there, in fp32.  ``cols`` is a
+// multiple of 8.
+template <int MB, int NB, bool ADD, typename TO>
+__device__ __forceinline__ void store(const f32x16_t (&acc)[MB][NB], char *lds, TO *out, size_t ld, int m0, int n0, int rows,
+                                      int cols, int lane) {
+  using TS = std::conditional_t<ADD, float, TO>;  // a sum that is added to is not rounded before
+  constexpr int V = 16 / sizeof(TO), LR = NB * 32 / V, PITCH = NB * 32 * sizeof(TS) + 16;  // lanes of a row; bytes between rows
+  char *const w = lds + (lane & 31) * PITCH + 4 * (lane >> 5) * (int)sizeof(TS);
+  const char *const rd = lds + lane / LR * PITCH + lane % LR * V * (int)sizeof(TS);
+  const int n = n0 + lane % LR * V;
 #pragma unroll
-  for (int j = 0; j < NB; j++) {
-    const int n = n0 + 32 * j + (lane & 31);
-    if (n >= cols) continue;
+  for (int i = 0; i < MB; i++) {
 #pragma unroll
-    for (int i = 0; i < MB; i++)
+    for (int j = 0; j < NB; j++)
 #pragma unroll
-      for (int r = 0; r < 16; r++) {
-        const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        if (m < rows) {
-          TO *o = out + (size_t)m * ld + n;
-          train::put(o, add ? train::to_f32(*o) + acc[i][j][r] : acc[i][j][r]);
-        }
+      for (int q = 0; q < 4; q++) {
+        const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        train::store_n<4>((TS *)(w + (32 * j + 8 * q) * (int)sizeof(TS)), v);
       }
+    asm volatile("" ::: "memory");  // other lanes' values are read: the order of a wave's LDS accesses is the program's
+#pragma unroll
+    for (int u = 0; u < 32 * LR / 64; u++) {
+      const int m = m0 + 32 * i + u * (64 / LR) + lane / LR;
+      const char *const at = rd + u * (64 / LR) * PITCH;
+      TO *const o = out + (size_t)m * ld + n;
+      if (m < rows && n < cols) {
+        if constexpr (ADD) {
+          float x[V], y[V];
+          train::load_n<V>((const float *)at, x);
+          train::load_n<V>(o, y);
+#pragma unroll
+          for (int k = 0; k < V; k++) x[k] += y[k];
+          train::store_n<V>(o, x);
+        } else *(u32x4_t *)o = *(const u32x4_t *)at;
+      }
+    }
+    asm volatile("" ::: "memory");
   }
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *p, size_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, (int)(uint32_t)bytes, kRsrcWord3);
 }
 
 using Mm = Cfg<256, 256, 64, 2, 4, 2, 3>;
@@ -305,7 +344,8 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
     constexpr int MB = decltype(MC)::value;
     f32x16_t acc[MB > 0 ? MB : 1][C::NB];
     contract<C, false, KN, MB>(sa, sb, KT, wave, lane, m0, n0, lds, acc);
-    if constexpr (MB > 0) store(acc, out, p.N, m0, n0, rows, p.N - nt * C::BN, lane, false);
+    barrier_no_fence();  // every wave has read its last fragments
+    if constexpr (MB > 0) store<MB, C::NB, false>(acc, lds + wave * C::OUT, out, p.N, m0, n0, rows, p.N - nt * C::BN, lane);
   };
   switch (mb) {
     case 0: body(std::integral_constant<int, 0>{}); break;
@@ -334,11 +374,11 @@ hipError_t by_index(const train::MmArgs &a, hipStream_t s) {
 
 using Wg = Cfg<256, 128, 32, 2, 2, 3, 3>;
 
-template <bool GA, bool GB, typename TO>
+template <bool GA, bool GB, bool ADD, typename TO>
 __global__ __launch_bounds__(Wg::NTHR, 2) __attribute__((amdgpu_waves_per_eu(2, 2))) void wgrad_dma_kernel(train::WgradArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   using C = Wg;
-  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS + (GA + GB) * C::NW * 512];
   const int MT = (p.M + C::BM - 1) / C::BM, NT = (p.N + C::BN - 1) / C::BN;
   // Workgroups go round-robin over the 8 XCDs; runs of 32 neighbouring tiles, which share operands, go to one XCD.
   const int j = blockIdx.x >> 3, t = ((j >> 5) * 8 + (blockIdx.x & 7)) * 32 + (j & 31);
@@ -354,7 +394,8 @@ __global__ __launch_bounds__(Wg::NTHR, 2) __attribute__((amdgpu_waves_per_eu(2, 
     constexpr int R = decltype(RC)::value;
     if constexpr (std::is_same_v<std::decay_t<decltype(s)>, Gathered<R == C::BM ? C::NA : C::NBL, C::NW>>) {
       s.r = resource(base, (size_t)have * ld);
-      s.index = index + r0;
+      s.ri = resource(index + r0, (size_t)rows * 4);
+      s.words = lds_at(lds) + C::LDS + ((R == C::BM || !GA ? 0 : C::NW) + wave) * 512;
       s.rows = rows;
       s.limit = have;
       s.template mn_major<R>(wave, lane, ld, (uint32_t)col * 2u);
@@ -377,7 +418,8 @@ __global__ __launch_bounds__(Wg::NTHR, 2) __attribute__((amdgpu_waves_per_eu(2, 
         for (int r = 0; r < 16; r++) acc[i][jj][r] = 0.0f;
   }
   TO *out = (TO *)p.dw + ((size_t)e * p.M + mt * C::BM) * p.N + nt * C::BN;
-  store(acc, out, p.N, m0, n0, p.M - mt * C::BM, p.N - nt * C::BN, lane, p.add);
+  barrier_no_fence();  // every wave has read its last fragments
+  store<C::MB, C::NB, ADD>(acc, lds + wave * C::OUT, out, p.N, m0, n0, p.M - mt * C::BM, p.N - nt * C::BN, lane);
 #endif
 }
 
@@ -386,16 +428,20 @@ __global__ __launch_bounds__(Wg::NTHR, 2) __attribute__((amdgpu_waves_per_eu(2, 
 // bf16 rows of whole 16-byte pieces, every 32-bit byte offset below kNowhere.
 bool train::mm_dma_fits(const MmArgs &a) {
   const long long lim = 1LL << 31;
-  return a.bf16 && a.K % 8 == 0 && (!a.kn || a.N % 8 == 0) && (long long)a.N * a.K * 2 < lim &&
+  return a.bf16 && a.K % 8 == 0 && a.N % 8 == 0 && (long long)a.N * a.K * 2 < lim &&
          (a.a_index ? (long long)a.a_rows * a.K * 2 < lim : 256LL * a.K * 2 < lim);
 }
-template <bool GA, bool GB>
+template <bool GA, bool GB, bool ADD>
 static hipError_t wgrad_by_out(const train::WgradArgs &a, hipStream_t s) {
   const long long tiles = (long long)a.El * ceil_div_i(a.M, Wg::BM) * ceil_div_i(a.N, Wg::BN);
   const dim3 grid((unsigned)((tiles + 255) / 256 * 256)), block(Wg::NTHR);
-  if (a.out_bf16) hipLaunchKernelGGL((wgrad_dma_kernel<GA, GB, uint16_t>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((wgrad_dma_kernel<GA, GB, float>), grid, block, 0, s, a);
+  if (a.out_bf16) hipLaunchKernelGGL((wgrad_dma_kernel<GA, GB, ADD, uint16_t>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((wgrad_dma_kernel<GA, GB, ADD, float>), grid, block, 0, s, a);
   return hipGetLastError();
+}
+template <bool GA, bool GB>
+static hipError_t wgrad_by_add(const train::WgradArgs &a, hipStream_t s) {
+  return a.add ? wgrad_by_out<GA, GB, true>(a, s) : wgrad_by_out<GA, GB, false>(a, s);
 }
 bool train::wgrad_dma_fits(const WgradArgs &a) {
   const long long lim = 1LL << 31;
@@ -403,8 +449,8 @@ bool train::wgrad_dma_fits(const WgradArgs &a) {
          (long long)(a.a_index ? a.a_rows : a.R_cap) * a.M * 2 < lim && (long long)(a.b_index ? a.b_rows : a.R_cap) * a.N * 2 < lim;
 }
 hipError_t train::launch_wgrad_dma(const WgradArgs &a, hipStream_t s) {
-  if (a.a_index) return a.b_index ? wgrad_by_out<true, true>(a, s) : wgrad_by_out<true, false>(a, s);
-  return a.b_index ? wgrad_by_out<false, true>(a, s) : wgrad_by_out<false, false>(a, s);
+  if (a.a_index) return a.b_index ? wgrad_by_add<true, true>(a, s) : wgrad_by_add<true, false>(a, s);
+  return a.b_index ? wgrad_by_add<false, true>(a, s) : wgrad_by_add<false, false>(a, s);
 }
 
 hipError_t train::launch_mm_dma(const MmArgs &a, hipStream_t s) { return a.kn ? by_index<true>(a, s) : by_index<false>(a, s); }
