@@ -30,17 +30,18 @@ __device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::
 
 // Sixteen bytes a lane from memory to 1 KB of LDS at byte ``to``.  In assembly, because the compiler waits for every load to
 // LDS that it knows of before a transposing LDS read (vmcnt(0) twice a step); nothing comes back in registers, and the waits
-// for LDS are the kernel's own.  M0 is written one wait state before its use.
+// for LDS are the kernel's own.  The five wait states are those between a scalar register that a vector instruction wrote (a
+// spilled one, say) and a load that reads it, which the compiler does not see in here; M0 needs one.
 typedef uint32_t rsrc_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void dma(rsrc_t r, uint32_t to, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff), "s"(r), "s"(soff)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff), "s"(r), "s"(soff)
                : "m0");
 }
 // The same for four bytes a lane.
 __device__ __forceinline__ void dma_words(rsrc_t r, uint32_t to, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(voff), "s"(r) : "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to), "v"(voff), "s"(r) : "m0");
 }
-// A buffer of ``bytes`` bytes.  The words come out of vector registers: five wait states before a load may read them.
+// A buffer of ``bytes`` bytes.
 __device__ __forceinline__ rsrc_t resource(const void *p, size_t bytes) {
   const uint64_t a = (uint64_t)(uintptr_t)p;
   rsrc_t r;
@@ -48,7 +49,6 @@ __device__ __forceinline__ rsrc_t resource(const void *p, size_t bytes) {
   r.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xffffu);
   r.z = __builtin_amdgcn_readfirstlane((uint32_t)bytes);
   r.w = kRsrcWord3;
-  asm volatile("s_nop 7" : "+s"(r));
   return r;
 }
 __device__ __forceinline__ uint32_t lds_at(const char *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
@@ -62,8 +62,6 @@ struct Cfg {
   static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
   static constexpr int NA = A_BYTES / 1024 / NW, NBL = B_BYTES / 1024 / NW;  // loads of a wave and step
   static constexpr int LDS = SA * A_BYTES + SB * B_BYTES;
-  static constexpr int OUT = 32 * (NB * 32 * 4 + 16);              // a wave's 32 rows of outputs, up to fp32
-  static_assert(NW * OUT <= LDS, "the outputs go through the operands' LDS");
   static_assert(NA >= 1 && NBL >= 1 && LDS <= 160 * 1024, "whole loads, one compute unit's LDS");
 };
 
@@ -137,7 +135,6 @@ struct Gathered {
   __device__ __forceinline__ void start(int lane) {
     ahead(lane, 0);
     ahead(lane, 1);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
   __device__ __forceinline__ void load(uint32_t to, int wave, int lane, int kt, bool) {
     const __attribute__((address_space(3))) int *const w = (const __attribute__((address_space(3))) int *)(uintptr_t)(words + (kt & 1) * 256);
@@ -197,8 +194,6 @@ __device__ __forceinline__ void contract(SrcA &sa, SrcB &sb, int KT, int wave, i
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
   // Steps before the loop, the oldest first; within a step A before B.  Once only the younger step's loads are in flight,
   // a step has landed, and so have the indexes that were asked for with it.
-  sa.start(lane);
-  sb.start(lane);
 #pragma unroll
   for (int t = 0; t < C::SB - 1; t++) {
     if (t >= KT) break;
@@ -254,47 +249,61 @@ __device__ __forceinline__ void contract(SrcA &sa, SrcB &sb, int KT, int wave, i
   }
 }
 
-// A wave's outputs, 32 rows at a time through LDS of its own, so that a store writes whole rows of the wave's columns:
-// acc[i][j][r] at lane l is tile row m0 + 32 i + l % 32, column n0 + 32 j + 8 (r / 4) + 4 (l / 32) + r % 4.  Two-byte stores
-// straight from the accumulators cost 440 of 1144 us of a weight gradient.  ADD: to what is there, in fp32.  ``cols`` is a
+// A wave's outputs, 32 rows of 128 bytes of LDS at a time, so that a store writes whole lines of a row: acc[i][j][r] at lane l
+// is tile row m0 + 32 i + l % 32, column n0 + 32 j + 8 (r / 4) + 4 (l / 32) + r % 4.  Two-byte stores straight from the
+// accumulators cost 440 of 1144 us of a weight gradient.  ADD: to what is there, in fp32.  ONCE: results that nobody reads
+// soon, past the caches.  FULL: the tile lies inside the matrix; the stores are then as many as STORES says.  ``cols`` is a
 // multiple of 8.
-template <int MB, int NB, bool ADD, typename TO>
+constexpr int kOutPitch = 144, kOutBytes = 32 * kOutPitch;
+template <int MB, int NB, bool ADD, bool ONCE, bool FULL, typename TO>
 __device__ __forceinline__ void store(const f32x16_t (&acc)[MB][NB], char *lds, TO *out, size_t ld, int m0, int n0, int rows,
                                       int cols, int lane) {
   using TS = std::conditional_t<ADD, float, TO>;  // a sum that is added to is not rounded before
-  constexpr int V = 16 / sizeof(TO), LR = NB * 32 / V, PITCH = NB * 32 * sizeof(TS) + 16;  // lanes of a row; bytes between rows
-  char *const w = lds + (lane & 31) * PITCH + 4 * (lane >> 5) * (int)sizeof(TS);
-  const char *const rd = lds + lane / LR * PITCH + lane % LR * V * (int)sizeof(TS);
-  const int n = n0 + lane % LR * V;
+  constexpr int JB = 4 / sizeof(TS), V = 16 / sizeof(TO), LR = JB * 32 / V;  // column blocks of a pass; lanes of a row
+  static_assert(NB % JB == 0, "whole passes");
+  char *const w = lds + (lane & 31) * kOutPitch + 4 * (lane >> 5) * (int)sizeof(TS);
+  const char *const rd = lds + lane / LR * kOutPitch + lane % LR * V * (int)sizeof(TS);
+  const uint32_t at_lane = ((uint32_t)(lane / LR) * (uint32_t)ld + (uint32_t)(lane % LR * V)) * (uint32_t)sizeof(TO);
 #pragma unroll
-  for (int i = 0; i < MB; i++) {
+  for (int i = 0; i < MB; i++)
 #pragma unroll
-    for (int j = 0; j < NB; j++)
+    for (int j0 = 0; j0 < NB; j0 += JB) {
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        train::store_n<4>((TS *)(w + (32 * j + 8 * q) * (int)sizeof(TS)), v);
+      for (int j = 0; j < JB; j++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const f32x16_t &c = acc[i][j0 + j];
+          const float v[4] = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+          train::store_n<4>((TS *)(w + (32 * j + 8 * q) * (int)sizeof(TS)), v);
+        }
+      asm volatile("" ::: "memory");  // other lanes' values are read: the order of a wave's LDS accesses is the program's
+      const int n = n0 + 32 * j0 + lane % LR * V;
+#pragma unroll
+      for (int u = 0; u < 32 * LR / 64; u++) {
+        const int m = m0 + 32 * i + u * (64 / LR) + lane / LR;
+        const char *const at = rd + u * (64 / LR) * kOutPitch;
+        // a wave's own address and a lane's offset from it
+        TO *const o = (TO *)((char *)(out + (size_t)(m0 + 32 * i + u * (64 / LR)) * ld + n0 + 32 * j0) + at_lane);
+        if (FULL || (m < rows && n < cols)) {
+          if constexpr (ADD) {
+            float x[V], y[V];
+            train::load_n<V>((const float *)at, x);
+            train::load_n<V>(o, y);
+#pragma unroll
+            for (int k = 0; k < V; k++) x[k] += y[k];
+            train::store_n<V>(o, x);
+          } else {
+            const u32x4_t v = *(const u32x4_t *)at;
+            if constexpr (ONCE) __builtin_nontemporal_store(v, (u32x4_t *)o);
+            else *(u32x4_t *)o = v;
+          }
+        }
       }
-    asm volatile("" ::: "memory");  // other lanes' values are read: the order of a wave's LDS accesses is the program's
-#pragma unroll
-    for (int u = 0; u < 32 * LR / 64; u++) {
-      const int m = m0 + 32 * i + u * (64 / LR) + lane / LR;
-      const char *const at = rd + u * (64 / LR) * PITCH;
-      TO *const o = out + (size_t)m * ld + n;
-      if (m < rows && n < cols) {
-        if constexpr (ADD) {
-          float x[V], y[V];
-          train::load_n<V>((const float *)at, x);
-          train::load_n<V>(o, y);
-#pragma unroll
-          for (int k = 0; k < V; k++) x[k] += y[k];
-          train::store_n<V>(o, x);
-        } else *(u32x4_t *)o = *(const u32x4_t *)at;
-      }
+      asm volatile("" ::: "memory");
     }
-    asm volatile("" ::: "memory");
-  }
 }
+template <int MB, int NB, typename TO>
+constexpr int STORES = MB * NB * 32 * 32 * sizeof(TO) / 1024;
 
 using Mm = Cfg<256, 256, 64, 2, 4, 2, 3>;
 
@@ -345,7 +354,7 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
     f32x16_t acc[MB > 0 ? MB : 1][C::NB];
     contract<C, false, KN, MB>(sa, sb, KT, wave, lane, m0, n0, lds, acc);
     barrier_no_fence();  // every wave has read its last fragments
-    if constexpr (MB > 0) store<MB, C::NB, false>(acc, lds + wave * C::OUT, out, p.N, m0, n0, rows, p.N - nt * C::BN, lane);
+    if constexpr (MB > 0) store<MB, C::NB, false, false, false>(acc, lds + wave * kOutBytes, out, p.N, m0, n0, rows, p.N - nt * C::BN, lane);
   };
   switch (mb) {
     case 0: body(std::integral_constant<int, 0>{}); break;
@@ -372,54 +381,152 @@ hipError_t by_index(const train::MmArgs &a, hipStream_t s) {
   return a.a_index ? by_out<KN, true>(a, s) : by_out<KN, false>(a, s);
 }
 
-using Wg = Cfg<256, 128, 32, 2, 2, 3, 3>;
+// Two workgroups of four waves on a compute unit, so that one multiplies while the other stores, took 809 us of the weight
+// gradient's 748 (6000 tokens, 4096 x 1536): they load half as much again.  Without its stores it takes 556 us, 1.09 PFLOP/s.
+using Wg = Cfg<256, 256, 32, 2, 4, 3, 3>;
+constexpr int kWorkers = 256;  // one workgroup per compute unit
 
+// Weight gradients: the contraction is short (an expert's rows, 375 of 6000 tokens), so a workgroup works through a list
+// of tiles and loads the next one's first two steps before it stores a tile.
 template <bool GA, bool GB, bool ADD, typename TO>
-__global__ __launch_bounds__(Wg::NTHR, 2) __attribute__((amdgpu_waves_per_eu(2, 2))) void wgrad_dma_kernel(train::WgradArgs p) {
+__global__ __launch_bounds__(Wg::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) void wgrad_dma_kernel(train::WgradArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   using C = Wg;
-  __shared__ __attribute__((aligned(1024))) char lds[C::LDS + (GA + GB) * C::NW * 512];
-  const int MT = (p.M + C::BM - 1) / C::BM, NT = (p.N + C::BN - 1) / C::BN;
-  // Workgroups go round-robin over the 8 XCDs; runs of 32 neighbouring tiles, which share operands, go to one XCD.
-  const int j = blockIdx.x >> 3, t = ((j >> 5) * 8 + (blockIdx.x & 7)) * 32 + (j & 31);
-  if (t >= p.El * MT * NT) return;
-  const int e = t / (MT * NT), mt = t / NT % MT, nt = t % NT;
+  using SrcA = std::conditional_t<GA, Gathered<C::NA, C::NW>, Source<C::NA, C::NW>>;
+  using SrcB = std::conditional_t<GB, Gathered<C::NBL, C::NW>, Source<C::NBL, C::NW>>;
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS + C::NW * kOutBytes + (GA + GB) * C::NW * 512];
+  const int MT = (p.M + C::BM - 1) / C::BM, NT = (p.N + C::BN - 1) / C::BN, per = MT * NT, total = p.El * per;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r0 = max(p.offsets[e], 0), rows = max(min(p.offsets[e + 1], p.R_cap) - r0, 0);
-  const int KT = (rows + C::BK - 1) / C::BK;
-  std::conditional_t<GA, Gathered<C::NA, C::NW>, Source<C::NA, C::NW>> sa;
-  std::conditional_t<GB, Gathered<C::NBL, C::NW>, Source<C::NBL, C::NW>> sb;
-  auto place = [&](auto &s, auto RC, const void *base, const int32_t *index, int have, uint32_t ld, int col)
-                   __attribute__((always_inline)) {
-    constexpr int R = decltype(RC)::value;
-    if constexpr (std::is_same_v<std::decay_t<decltype(s)>, Gathered<R == C::BM ? C::NA : C::NBL, C::NW>>) {
-      s.r = resource(base, (size_t)have * ld);
-      s.ri = resource(index + r0, (size_t)rows * 4);
-      s.words = lds_at(lds) + C::LDS + ((R == C::BM || !GA ? 0 : C::NW) + wave) * 512;
-      s.rows = rows;
-      s.limit = have;
-      s.template mn_major<R>(wave, lane, ld, (uint32_t)col * 2u);
+  const int m0 = wave / C::WN * (C::MB * 32), n0 = wave % C::WN * (C::NB * 32);
+  // Workgroups go round-robin over the 8 XCDs: 32 neighbouring tiles, which share operands, run on one XCD at a time.
+  int t = (blockIdx.x & 7) * (kWorkers / 8) + (blockIdx.x >> 3);
+  if (t >= total) return;
+  const auto *const off = (const __attribute__((address_space(4))) int *)(uintptr_t)p.offsets;  // scalar loads
+  struct Tile {
+    int e, mt, nt, r0, rows, KT;
+  };
+  auto tile = [&](int at) __attribute__((always_inline)) {
+    Tile d;
+    d.e = at / per;
+    d.mt = (at - d.e * per) / NT;
+    d.nt = at - d.e * per - d.mt * NT;
+    d.r0 = max(off[d.e], 0);
+    d.rows = max(min(off[d.e + 1], p.R_cap) - d.r0, 0);
+    d.KT = (d.rows + C::BK - 1) / C::BK;
+    return d;
+  };
+  SrcA sa;
+  SrcB sb;
+  char *const la = lds, *const lb = lds + C::SA * C::A_BYTES, *const stage = lds + C::LDS + wave * kOutBytes;
+  const uint32_t ta = lds_at(la), tb = lds_at(lb);
+  auto place = [&](const Tile &d) __attribute__((always_inline)) {
+    const uint32_t lda = (uint32_t)p.M * 2u, ldb = (uint32_t)p.N * 2u, words = lds_at(lds) + C::LDS + C::NW * kOutBytes;
+    if constexpr (GA) {
+      sa.r = resource(p.a, (size_t)p.a_rows * lda);
+      sa.ri = resource(p.a_index + d.r0, (size_t)d.rows * 4);
+      sa.words = words + wave * 512;
+      sa.rows = d.rows;
+      sa.limit = p.a_rows;
+      sa.template mn_major<C::BM>(wave, lane, lda, d.mt * C::BM * 2u);
     } else {
-      s.r = resource((const char *)base + (size_t)r0 * ld, (size_t)rows * ld);
-      s.template mn_major<R, C::BK>(wave, lane, ld, (uint32_t)col * 2u);
+      sa.r = resource((const char *)p.a + (size_t)d.r0 * lda, (size_t)d.rows * lda);
+      sa.template mn_major<C::BM, C::BK>(wave, lane, lda, d.mt * C::BM * 2u);
+    }
+    if constexpr (GB) {
+      sb.r = resource(p.b, (size_t)p.b_rows * ldb);
+      sb.ri = resource(p.b_index + d.r0, (size_t)d.rows * 4);
+      sb.words = words + (GA * C::NW + wave) * 512;
+      sb.rows = d.rows;
+      sb.limit = p.b_rows;
+      sb.template mn_major<C::BN>(wave, lane, ldb, d.nt * C::BN * 2u);
+    } else {
+      sb.r = resource((const char *)p.b + (size_t)d.r0 * ldb, (size_t)d.rows * ldb);
+      sb.template mn_major<C::BN, C::BK>(wave, lane, ldb, d.nt * C::BN * 2u);
     }
   };
-  place(sa, std::integral_constant<int, C::BM>{}, p.a, p.a_index, p.a_rows, (uint32_t)p.M * 2u, mt * C::BM);
-  place(sb, std::integral_constant<int, C::BN>{}, p.b, p.b_index, p.b_rows, (uint32_t)p.N * 2u, nt * C::BN);
-  const int m0 = wave / C::WN * (C::MB * 32), n0 = wave % C::WN * (C::NB * 32);
+  auto first = [&](int KT) __attribute__((always_inline)) {  // the loads of a tile's first two steps
+    if (KT == 0) return;
+    sa.start(lane);
+    sb.start(lane);
+    if constexpr (GA || GB) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    sa.load(ta, wave, lane, 0, KT == 1);
+    sb.load(tb, wave, lane, 0, KT == 1);
+    if (KT > 1) {
+      sa.load(ta + C::A_BYTES, wave, lane, 1, KT == 2);
+      sb.load(tb + C::B_BYTES, wave, lane, 1, KT == 2);
+    }
+  };
+  const Frag<true, C::BM, C::MB> fa(m0, lane);
+  const Frag<true, C::BN, C::NB> fb(n0, lane);
   f32x16_t acc[C::MB][C::NB];
-  if (KT > 0) contract<C, true, true, C::MB>(sa, sb, KT, wave, lane, m0, n0, lds, acc);
-  else {
+  constexpr int YOUNG = SrcA::LOADS + SrcB::LOADS, LATER = STORES<C::MB, C::NB, TO>;
+  static_assert(C::SA == 3 && C::SB == 3 && YOUNG + LATER < 64, "two steps ahead; counts that a wait can name");
+
+  Tile d = tile(t);
+  place(d);
+  first(d.KT);
+  bool stored = false;  // exactly LATER stores are younger than the loads of this tile's first two steps
+  for (;;) {
+    const int tn = t + kWorkers;
+    const bool more = tn < total;
+    const Tile dn = tile(more ? tn : t);
+    const int KT = d.KT;
 #pragma unroll
     for (int i = 0; i < C::MB; i++)
 #pragma unroll
-      for (int jj = 0; jj < C::NB; jj++)
+      for (int j = 0; j < C::NB; j++)
 #pragma unroll
-        for (int r = 0; r < 16; r++) acc[i][jj][r] = 0.0f;
+        for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
+    auto step = [&](auto PC, int kt) __attribute__((always_inline)) {
+      constexpr int P = decltype(PC)::value, P2 = (P + 2) % 3;
+      if (kt >= KT) return;
+      // this wave's loads of the step have landed, and it has read its last fragments of the step before
+      if (kt + 1 >= KT) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else if (P < 2 && kt < 2 && stored) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNG + LATER) : "memory");
+      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNG) : "memory");
+      barrier_no_fence();
+      const char *a = la + P * C::A_BYTES, *b = lb + P * C::B_BYTES;
+      bf16x8_t af[2][C::MB], bf[2][C::NB];
+      auto frags = [&](int kk) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < C::NB; j++) bf[kk & 1][j] = fb.get(b, kk, j);
+#pragma unroll
+        for (int i = 0; i < C::MB; i++) af[kk & 1][i] = fa.get(a, kk, i);
+      };
+      frags(0);
+#pragma unroll
+      for (int kk = 0; kk < C::BK / 16; kk++) {
+        if (kk + 1 < C::BK / 16) frags(kk + 1);
+        if (kk == 0 && kt + 2 < KT) sa.load(ta + P2 * C::A_BYTES, wave, lane, kt + 2, kt + 3 == KT);
+        if (kk == 1 && kt + 2 < KT) sb.load(tb + P2 * C::B_BYTES, wave, lane, kt + 2, kt + 3 == KT);
+#pragma unroll
+        for (int i = 0; i < C::MB; i++)
+#pragma unroll
+          for (int j = 0; j < C::NB; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[kk & 1][j], af[kk & 1][i], acc[i][j], 0, 0, 0);
+      }
+    };
+    for (int kt = 0; kt < KT; kt += 3) {
+      step(std::integral_constant<int, 0>{}, kt);
+      step(std::integral_constant<int, 1>{}, kt + 1);
+      step(std::integral_constant<int, 2>{}, kt + 2);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every wave has read its last fragments
+    if (more) {
+      place(dn);
+      first(dn.KT);
+    }
+    TO *out = (TO *)p.dw + ((size_t)d.e * p.M + d.mt * C::BM) * p.N + d.nt * C::BN;
+    const int ms = p.M - d.mt * C::BM, ns = p.N - d.nt * C::BN;
+    const bool full = ms >= C::BM && ns >= C::BN;
+    if (ADD && KT == 0) {
+    } else if (full) store<C::MB, C::NB, ADD, true, true>(acc, stage, out, p.N, m0, n0, ms, ns, lane);
+    else store<C::MB, C::NB, ADD, true, false>(acc, stage, out, p.N, m0, n0, ms, ns, lane);
+    if (!more) break;
+    stored = !ADD && full;
+    t = tn;
+    d = dn;
   }
-  TO *out = (TO *)p.dw + ((size_t)e * p.M + mt * C::BM) * p.N + nt * C::BN;
-  barrier_no_fence();  // every wave has read its last fragments
-  store<C::MB, C::NB, ADD>(acc, lds + wave * C::OUT, out, p.N, m0, n0, p.M - mt * C::BM, p.N - nt * C::BN, lane);
 #endif
 }
 
@@ -433,8 +540,7 @@ bool train::mm_dma_fits(const MmArgs &a) {
 }
 template <bool GA, bool GB, bool ADD>
 static hipError_t wgrad_by_out(const train::WgradArgs &a, hipStream_t s) {
-  const long long tiles = (long long)a.El * ceil_div_i(a.M, Wg::BM) * ceil_div_i(a.N, Wg::BN);
-  const dim3 grid((unsigned)((tiles + 255) / 256 * 256)), block(Wg::NTHR);
+  const dim3 grid(kWorkers), block(Wg::NTHR);
   if (a.out_bf16) hipLaunchKernelGGL((wgrad_dma_kernel<GA, GB, ADD, uint16_t>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((wgrad_dma_kernel<GA, GB, ADD, float>), grid, block, 0, s, a);
   return hipGetLastError();
