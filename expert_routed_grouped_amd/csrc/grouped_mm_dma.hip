@@ -74,12 +74,15 @@ struct Source {
   uint32_t step;    // bytes from one step to the next
   uint32_t last;    // or-ed into a lane's offset in the last step: kNowhere where that is past the contraction's end
   __device__ __forceinline__ void start(int) {}
+  // The first COUNT segments of step kt.
+  template <int COUNT = N>
   __device__ __forceinline__ void load(uint32_t to, int wave, int, int kt, bool is_last) {
     const uint32_t so = (uint32_t)kt * step, m = is_last ? last : 0u;
 #pragma unroll
-    for (int u = 0; u < N; u++) dma(r, to + (wave + NW * u) * 1024, off[u] | m, so);
+    for (int u = 0; u < COUNT; u++) dma(r, to + (wave + NW * u) * 1024, off[u] | m, so);
   }
-  // k-major tile, BK = 64: segment s holds rows 8s .. 8s + 7.  ``row`` maps a tile row to its byte offset.
+  // k-major tile, BK = 64: segment s holds rows 8s .. 8s + 7.  ``row`` gives the byte offset of
+  // segment u's tile row.
   template <typename F>
   __device__ __forceinline__ void k_major(int wave, int lane, int K, F row) {
     static_assert(NW % 2 == 0, "a lane's chunk is the same in all of its segments");
@@ -88,7 +91,7 @@ struct Source {
     for (int u = 0; u < N; u++) {
       const int t = (wave + NW * u) * 8 + (lane >> 3);
       chunk = (lane & 7) ^ ((t >> 1) & 7);
-      off[u] = row(t) + (uint32_t)chunk * 16u;
+      off[u] = row(u, t) + (uint32_t)chunk * 16u;
     }
     step = 128;
     last = (K & 63) != 0 && chunk * 8 >= (K & 63) ? kNowhere : 0u;
@@ -177,86 +180,14 @@ struct Frag {
   }
 };
 
-// The contraction of one tile.  MB: 32-row blocks of A that hold rows (0: this wave only loads).
-template <typename C, bool AMN, bool BMN, int MB, typename SrcA, typename SrcB, typename Acc>
-__device__ __forceinline__ void contract(SrcA &sa, SrcB &sb, int KT, int wave, int lane, int m0, int n0, char *lds,
-                                         Acc &acc) {
-  constexpr int M1 = MB > 0 ? MB : 1, U = C::SA * C::SB, KK = C::BK / 16;
-  const Frag<AMN, C::BM, M1> fa(m0, lane);
-  const Frag<BMN, C::BN, C::NB> fb(n0, lane);
-  char *const la = lds, *const lb = lds + C::SA * C::A_BYTES;
-  const uint32_t ta = lds_at(la), tb = lds_at(lb);
-#pragma unroll
-  for (int i = 0; i < M1; i++)
-#pragma unroll
-    for (int j = 0; j < C::NB; j++)
-#pragma unroll
-      for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
-  // Steps before the loop, the oldest first; within a step A before B.  Once only the younger step's loads are in flight,
-  // a step has landed, and so have the indexes that were asked for with it.
-#pragma unroll
-  for (int t = 0; t < C::SB - 1; t++) {
-    if (t >= KT) break;
-    if (t < C::SA - 1) sa.load(ta + t * C::A_BYTES, wave, lane, t, t == KT - 1);
-    sb.load(tb + t * C::B_BYTES, wave, lane, t, t == KT - 1);
-  }
-  constexpr int YOUNG = SrcA::LOADS * (C::SA - 2) + SrcB::LOADS * (C::SB - 2);
-  static_assert((C::SA == 2 || C::SA == 3) && C::SB == 3, "the wait below counts one younger step");
-  auto step = [&](auto PC, int kt) __attribute__((always_inline)) {
-    constexpr int P = decltype(PC)::value, A0 = P % C::SA, B0 = P % C::SB;
-    constexpr int A1 = (P + C::SA - 1) % C::SA, B1 = (P + C::SB - 1) % C::SB;
-    if (kt >= KT) return;
-    // this wave's loads of the step have landed, and it has read its last fragments of the step before
-    if (kt + 1 < KT) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(YOUNG) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    barrier_no_fence();
-    const int na = kt + C::SA - 1, nb = kt + C::SB - 1;
-    const char *a = la + A0 * C::A_BYTES, *b = lb + B0 * C::B_BYTES;
-    bf16x8_t af[2][M1], bf[2][C::NB];
-    auto frags = [&](int kk) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < C::NB; j++) bf[kk & 1][j] = fb.get(b, kk, j);
-#pragma unroll
-      for (int i = 0; i < M1; i++) af[kk & 1][i] = fa.get(a, kk, i);
-    };
-    if constexpr (MB > 0) frags(0);
-#pragma unroll
-    for (int kk = 0; kk < KK; kk++) {
-      if constexpr (MB > 0) {
-        if (kk + 1 < KK) frags(kk + 1);
-      }
-      if (kk == 0 && na < KT) sa.load(ta + A1 * C::A_BYTES, wave, lane, na, na == KT - 1);
-      if (kk == KK / 2 && nb < KT) sb.load(tb + B1 * C::B_BYTES, wave, lane, nb, nb == KT - 1);
-      if constexpr (MB > 0) {
-#pragma unroll
-        for (int i = 0; i < MB; i++)
-#pragma unroll
-          for (int j = 0; j < C::NB; j++)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[kk & 1][j], af[kk & 1][i], acc[i][j], 0, 0, 0);
-      }
-    }
-  };
-  constexpr int L = C::SA == C::SB ? C::SA : U;  // steps until the slots repeat
-  for (int kt = 0; kt < KT; kt += L) {
-    step(std::integral_constant<int, 0>{}, kt);
-    step(std::integral_constant<int, 1>{}, kt + 1);
-    step(std::integral_constant<int, 2>{}, kt + 2);
-    if constexpr (L > 3) {
-      step(std::integral_constant<int, 3>{}, kt + 3);
-      step(std::integral_constant<int, 4>{}, kt + 4);
-      step(std::integral_constant<int, 5>{}, kt + 5);
-    }
-  }
-}
-
 // A wave's outputs, 32 rows of 128 bytes of LDS at a time, so that a store writes whole lines of a row: acc[i][j][r] at lane l
 // is tile row m0 + 32 i + l % 32, column n0 + 32 j + 8 (r / 4) + 4 (l / 32) + r % 4.  Two-byte stores straight from the
 // accumulators cost 440 of 1144 us of a weight gradient.  ADD: to what is there, in fp32.  ONCE: results that nobody reads
 // soon, past the caches.  FULL: the tile lies inside the matrix; the stores are then as many as STORES says.  ``cols`` is a
 // multiple of 8.
 constexpr int kOutPitch = 144, kOutBytes = 32 * kOutPitch;
-template <int MB, int NB, bool ADD, bool ONCE, bool FULL, typename TO>
-__device__ __forceinline__ void store(const f32x16_t (&acc)[MB][NB], char *lds, TO *out, size_t ld, int m0, int n0, int rows,
+template <int MB, int NB, bool ADD, bool ONCE, bool FULL, typename TO, int MA>
+__device__ __forceinline__ void store(const f32x16_t (&acc)[MA][NB], char *lds, TO *out, size_t ld, int m0, int n0, int rows,
                                       int cols, int lane) {
   using TS = std::conditional_t<ADD, float, TO>;  // a sum that is added to is not rounded before
   constexpr int JB = 4 / sizeof(TS), V = 16 / sizeof(TO), LR = JB * 32 / V;  // column blocks of a pass; lanes of a row
@@ -305,71 +236,203 @@ __device__ __forceinline__ void store(const f32x16_t (&acc)[MB][NB], char *lds, 
 template <int MB, int NB, typename TO>
 constexpr int STORES = MB * NB * 32 * 32 * sizeof(TO) / 1024;
 
+constexpr int kWorkers = 256;  // one workgroup per compute unit, 32 to an XCD
+
+// Rows times matrix.  The second operand, whose first touch comes from memory, is loaded two steps ahead through three
+// slots, the rows one step ahead through two (160 KB of LDS).
 using Mm = Cfg<256, 256, 64, 2, 4, 2, 3>;
+
+// The tiles of a product: expert e has ceil(c_e / BM) tiles of rows, its c_e rows split evenly over them (rounded up to 64), times
+// NT tiles of columns, numbered expert by expert, then by columns, then by rows.  A lane holds how many tiles the experts
+// up to its group of G have, so that a tile is found with one ballot and at most G scalar loads.
+struct MmTile {
+  int nt, r0, rows, trows;
+  const void *w;
+};
+template <typename C>
+struct MmTiles {
+  const __attribute__((address_space(4))) int *off;
+  int El, R_cap, NT, G, upto, total;
+  // Rows of an expert that lie in the buffers, whatever the offsets say.
+  static __device__ __forceinline__ int rows_in(int a, int b, int R_cap) { return max(min(b, R_cap) - max(a, 0), 0); }
+  __device__ __forceinline__ int of(int e) const {
+    return (rows_in(off[e], off[e + 1], R_cap) + C::BM - 1) / C::BM * NT;
+  }
+  __device__ __forceinline__ MmTiles(const train::MmArgs &p, int lane) {
+    off = (const __attribute__((address_space(4))) int *)(uintptr_t)p.offsets;
+    El = p.El;
+    R_cap = p.R_cap;
+    NT = (p.N + C::BN - 1) / C::BN;
+    G = (El + 63) / 64;
+    int n = 0;
+    for (int i = 0; i < G; i++) {
+      const int e = lane * G + i;
+      if (e < El) n += (rows_in(p.offsets[e], p.offsets[e + 1], R_cap) + C::BM - 1) / C::BM * NT;
+    }
+    upto = ffn::wave_incl_scan_i(n, lane);
+    total = __builtin_amdgcn_readlane(upto, 63);
+  }
+  // Tile L < total.
+  __device__ __forceinline__ MmTile at(int L, const train::MmArgs &p) const {
+    const int g = __ffsll((long long)__ballot(upto > L)) - 1;
+    int before = g == 0 ? 0 : __builtin_amdgcn_readlane(upto, g - 1), e = g * G;
+    for (int n = of(e); L >= before + n; n = of(e)) before += n, e++;
+    const int beg = max(off[e], 0), cnt = rows_in(beg, off[e + 1], R_cap), mtiles = (cnt + C::BM - 1) / C::BM, rr = L - before;
+    MmTile t;
+    t.nt = rr / mtiles;
+    t.trows = min(C::BM, ((cnt + mtiles - 1) / mtiles + 63) & ~63);
+    t.r0 = beg + (rr - t.nt * mtiles) * t.trows;
+    t.rows = min(t.trows, beg + cnt - t.r0);
+    t.w = (const char *)p.w + (size_t)e * p.N * p.K * 2;
+    return t;
+  }
+};
 
 template <bool KN, bool GATHER, typename TO>
 __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 2))) void mm_dma_kernel(train::MmArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone
   using C = Mm;
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
-  ffn::TileParams tp{};
-  tp.offsets = p.offsets;
-  tp.El = p.El;
-  tp.R_cap = p.R_cap;
-  int e, nt, mt, mtiles;
-  if (!ffn::locate_tile<C::BM>(tp, (p.N + C::BN - 1) / C::BN, e, nt, mt, mtiles)) return;
-  e = __builtin_amdgcn_readfirstlane(e);
-  nt = __builtin_amdgcn_readfirstlane(nt);
-  mt = __builtin_amdgcn_readfirstlane(mt);
-  mtiles = __builtin_amdgcn_readfirstlane(mtiles);
-  // an expert's rows split evenly over its tiles, rounded up to 64
-  const int beg = p.offsets[e], cnt = p.offsets[e + 1] - beg;
-  const int trows = __builtin_amdgcn_readfirstlane(min(C::BM, (((cnt + mtiles - 1) / mtiles) + 63) & ~63));
-  const int r0 = beg + mt * trows, rows = min(trows, min(beg + cnt, p.R_cap) - r0);
-  if (rows <= 0 || r0 < 0) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int half = trows >> 1, wm = wave / C::WN, wn = wave % C::WN, valid = rows - wm * half;
-  const int mb = __builtin_amdgcn_readfirstlane(valid <= 0 ? 0 : min(half >> 5, (valid + 31) >> 5));
-  const int K = p.K, KT = (K + C::BK - 1) / C::BK;
+  const int wm = wave / C::WN, n0 = wave % C::WN * (C::NB * 32), K = p.K, KT = (K + C::BK - 1) / C::BK;
+  const MmTiles<C> tiles(p, lane);
+  // Workgroups go round-robin over the 8 XCDs: XCD x takes the x-th eighth of the tiles, its workgroups in turn, so that
+  // the tiles of an expert, which share operands, meet in one L2.
+  const int xcd = blockIdx.x & 7, q = tiles.total >> 3, rem = tiles.total & 7;
+  const int end = xcd * q + min(xcd, rem) + q + (xcd < rem ? 1 : 0);
+  int L = xcd * q + min(xcd, rem) + (blockIdx.x >> 3);
+  if (L >= end) return;
+  char *const la = lds, *const lb = lds + C::SA * C::A_BYTES;
+  const uint32_t ta = lds_at(la), tb = lds_at(lb);
+  // Outputs go through the slots that the next tile's first loads leave free: the third of B, the second of A.
+  constexpr int IN_B = C::B_BYTES / kOutBytes;
+  static_assert(IN_B + C::A_BYTES / kOutBytes >= C::NW, "every wave's outputs fit");
+  char *const stage = wave < IN_B ? lb + 2 * C::B_BYTES + wave * kOutBytes : la + C::A_BYTES + (wave - IN_B) * kOutBytes;
 
   Source<C::NA, C::NW> sa;
-  const size_t lda = (size_t)K * 2;
-  if constexpr (GATHER) sa.r = resource(p.a, (size_t)p.a_rows * lda);
-  else sa.r = resource((const char *)p.a + r0 * lda, (size_t)rows * lda);
-  sa.k_major(wave, lane, K, [&](int r) {
-    const int at = min(r, rows - 1);  // rows past the end repeat the last one; nothing of them is stored
-    return (uint32_t)(GATHER ? min(max(p.a_index[r0 + at], 0), p.a_rows - 1) : at) * (uint32_t)lda;
-  });
   Source<C::NBL, C::NW> sb;
-  sb.r = resource((const char *)p.w + (size_t)e * p.N * K * 2, (size_t)p.N * K * 2);
-  if constexpr (KN) {
-    sb.template mn_major<C::BN, C::BK>(wave, lane, (uint32_t)p.N * 2u, nt * C::BN * 2u);
-  } else {
-    sb.k_major(wave, lane, K, [&](int r) { return (uint32_t)min(nt * C::BN + r, p.N - 1) * (uint32_t)lda; });
-  }
-  const int m0 = wm * half, n0 = wn * (C::NB * 32);
-  TO *out = (TO *)p.out + (size_t)r0 * p.N + nt * C::BN;
-  auto body = [&](auto MC) __attribute__((always_inline)) {
-    constexpr int MB = decltype(MC)::value;
-    f32x16_t acc[MB > 0 ? MB : 1][C::NB];
-    contract<C, false, KN, MB>(sa, sb, KT, wave, lane, m0, n0, lds, acc);
-    barrier_no_fence();  // every wave has read its last fragments
-    if constexpr (MB > 0) store<MB, C::NB, false, false, false>(acc, lds + wave * kOutBytes, out, p.N, m0, n0, rows, p.N - nt * C::BN, lane);
+  const uint32_t lda = (uint32_t)K * 2u;
+  int src[C::NA];  // gathered: the tensor's rows of this lane's segments
+  auto rows_of = [&](const MmTile &t) __attribute__((always_inline)) {
+    if constexpr (GATHER) {
+#pragma unroll
+      for (int u = 0; u < C::NA; u++)  // rows past the end repeat the last one; nothing of them is stored
+        src[u] = p.a_index[t.r0 + min((wave + C::NW * u) * 8 + (lane >> 3), t.rows - 1)];
+    }
   };
-  switch (mb) {
-    case 0: body(std::integral_constant<int, 0>{}); break;
-    case 1: body(std::integral_constant<int, 1>{}); break;
-    case 2: body(std::integral_constant<int, 2>{}); break;
-    case 3: body(std::integral_constant<int, 3>{}); break;
-    default: body(std::integral_constant<int, 4>{}); break;
+  auto place = [&](const MmTile &t) __attribute__((always_inline)) {
+    if constexpr (GATHER) sa.r = resource(p.a, (size_t)p.a_rows * lda);
+    else sa.r = resource((const char *)p.a + (size_t)t.r0 * lda, (size_t)t.rows * lda);
+    sa.k_major(wave, lane, K, [&](int u, int r) {
+      if constexpr (GATHER) return (uint32_t)min(max(src[u], 0), p.a_rows - 1) * lda;
+      else return (uint32_t)min(r, t.rows - 1) * lda;
+    });
+    sb.r = resource(t.w, (size_t)p.N * K * 2);
+    if constexpr (KN) sb.template mn_major<C::BN, C::BK>(wave, lane, (uint32_t)p.N * 2u, t.nt * C::BN * 2u);
+    else sb.k_major(wave, lane, K, [&](int, int r) { return (uint32_t)min(t.nt * C::BN + r, p.N - 1) * lda; });
+  };
+  auto first = [&](int trows) __attribute__((always_inline)) {  // the loads that run ahead of a tile
+    if (trows > 192) sa.template load<4>(ta, wave, lane, 0, KT == 1);
+    else if (trows > 128) sa.template load<3>(ta, wave, lane, 0, KT == 1);
+    else if (trows > 64) sa.template load<2>(ta, wave, lane, 0, KT == 1);
+    else sa.template load<1>(ta, wave, lane, 0, KT == 1);
+    sb.load(tb, wave, lane, 0, KT == 1);
+    if (KT > 1) sb.load(tb + C::B_BYTES, wave, lane, 1, KT == 2);
+  };
+  const Frag<KN, C::BN, C::NB> fb(n0, lane);
+  f32x16_t acc[C::MB][C::NB];
+  bool stored = false;  // exactly the stores of a whole tile are younger than the loads of this tile's first step
+
+  // One tile of MB blocks of 32 rows for either half of the waves; the outputs are the caller's to store.
+  auto contract = [&](auto MC, int m0) __attribute__((always_inline)) {
+    constexpr int MB = decltype(MC)::value;
+    const Frag<false, C::BM, MB> fa(m0, lane);
+#pragma unroll
+    for (int i = 0; i < MB; i++)
+#pragma unroll
+      for (int j = 0; j < C::NB; j++)
+#pragma unroll
+        for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
+    auto step = [&](auto PC, int kt) __attribute__((always_inline)) {
+      constexpr int P = decltype(PC)::value, A0 = P % 2, B0 = P % 3, A1 = (P + 1) % 2, B2 = (P + 2) % 3;
+      if (kt >= KT) return;
+      // This wave's loads of the step have landed (within a step those of A are issued before those of B, one step younger),
+      // and it has read its last fragments of the step before.
+      if (kt + 1 >= KT) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      else if (P == 0 && kt == 0 && stored)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C::NBL + STORES<MB, C::NB, TO>) : "memory");
+      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C::NBL) : "memory");
+      barrier_no_fence();
+      const char *a = la + A0 * C::A_BYTES, *b = lb + B0 * C::B_BYTES;
+      bf16x8_t af[2][MB], bf[2][C::NB];
+      auto frags = [&](int kk) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < C::NB; j++) bf[kk & 1][j] = fb.get(b, kk, j);
+#pragma unroll
+        for (int i = 0; i < MB; i++) af[kk & 1][i] = fa.get(a, kk, i);
+      };
+      frags(0);
+#pragma unroll
+      for (int kk = 0; kk < 4; kk++) {
+        if (kk < 3) frags(kk + 1);
+        if (kk == 0 && kt + 1 < KT) sa.template load<MB>(ta + A1 * C::A_BYTES, wave, lane, kt + 1, kt + 2 == KT);
+        if (kk == 2 && kt + 2 < KT) sb.load(tb + B2 * C::B_BYTES, wave, lane, kt + 2, kt + 3 == KT);
+#pragma unroll
+        for (int i = 0; i < MB; i++)
+#pragma unroll
+          for (int j = 0; j < C::NB; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[kk & 1][j], af[kk & 1][i], acc[i][j], 0, 0, 0);
+      }
+    };
+    for (int kt = 0; kt < KT; kt += 6) {
+      step(std::integral_constant<int, 0>{}, kt);
+      step(std::integral_constant<int, 1>{}, kt + 1);
+      step(std::integral_constant<int, 2>{}, kt + 2);
+      step(std::integral_constant<int, 3>{}, kt + 3);
+      step(std::integral_constant<int, 4>{}, kt + 4);
+      step(std::integral_constant<int, 5>{}, kt + 5);
+    }
+  };
+
+  MmTile t = tiles.at(L, p);
+  rows_of(t);
+  place(t);
+  first(t.trows);
+  for (;;) {
+    const bool more = L + kWorkers / 8 < end;
+    const MmTile tn = tiles.at(more ? L + kWorkers / 8 : L, p);
+    rows_of(tn);
+    const int m0 = wm * (t.trows >> 1), cols = p.N - t.nt * C::BN;
+    TO *const out = (TO *)p.out + (size_t)t.r0 * p.N + t.nt * C::BN;
+    const bool full = t.rows == t.trows && cols >= C::BN;
+    auto body = [&](auto MC) __attribute__((always_inline)) {
+      constexpr int MB = decltype(MC)::value;
+      contract(MC, m0);
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every wave has read its last fragments
+      if (more) {
+        place(tn);
+        first(tn.trows);
+      }
+      if (full) store<MB, C::NB, false, false, true>(acc, stage, out, p.N, m0, n0, t.rows, cols, lane);
+      else store<MB, C::NB, false, false, false>(acc, stage, out, p.N, m0, n0, t.rows, cols, lane);
+    };
+    switch (t.trows >> 6) {
+      case 1: body(std::integral_constant<int, 1>{}); break;
+      case 2: body(std::integral_constant<int, 2>{}); break;
+      case 3: body(std::integral_constant<int, 3>{}); break;
+      default: body(std::integral_constant<int, 4>{}); break;
+    }
+    if (!more) break;
+    stored = full && tn.trows == t.trows;
+    L += kWorkers / 8;
+    t = tn;
   }
 #endif
 }
 
 template <bool KN, bool GATHER, typename TO>
 hipError_t launch(const train::MmArgs &a, hipStream_t s) {
-  const long long mt = std::min(((long long)a.R_cap + (long long)a.El * (Mm::BM - 1)) / Mm::BM, (long long)a.R_cap);
-  hipLaunchKernelGGL((mm_dma_kernel<KN, GATHER, TO>), dim3((unsigned)(mt * ceil_div_i(a.N, Mm::BN))), dim3(Mm::NTHR), 0, s, a);
+  hipLaunchKernelGGL((mm_dma_kernel<KN, GATHER, TO>), dim3(kWorkers), dim3(Mm::NTHR), 0, s, a);
   return hipGetLastError();
 }
 template <bool KN, bool GATHER>
@@ -384,7 +447,6 @@ hipError_t by_index(const train::MmArgs &a, hipStream_t s) {
 // Two workgroups of four waves on a compute unit, so that one multiplies while the other stores, took 809 us of the weight
 // gradient's 748 (6000 tokens, 4096 x 1536): they load half as much again.  Without its stores it takes 556 us, 1.09 PFLOP/s.
 using Wg = Cfg<256, 256, 32, 2, 4, 3, 3>;
-constexpr int kWorkers = 256;  // one workgroup per compute unit
 
 // Weight gradients: the contraction is short (an expert's rows, 375 of 6000 tokens), so a workgroup works through a list
 // of tiles and loads the next one's first two steps before it stores a tile.
