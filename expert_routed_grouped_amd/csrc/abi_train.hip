@@ -168,16 +168,10 @@ int moe_swiglu_backward(const void *gu, const void *dh, int dtype, const int32_t
   return hip_status(train::launch_swiglu_backward(s, (hipStream_t)stream));
 }
 
-size_t moe_route_backward_workspace_size(int T, int k, int H, int E) {
-  if (T < 0 || k < 1 || k > 32 || E < 1 || E > 1024 || k > E || H < 1 || (long long)T * k >= kMaxRows) return 0;
-  return train::route_grad_ws_bytes(T, k, E, H);
-}
-
 int moe_route_backward(const int32_t *topk_ids, const float *topk_w, const float *d_topk_w, int T, int k, int E, int H,
                        const void *x, const void *w_router, int dtype, const int32_t *offsets, const int32_t *row_token,
-                       const int32_t *token_row, const void *rows, int rows_dtype, const int32_t *rows_at, int R_cap,
-                       void *dx, int dx_dtype, float *dw_router, float *d_bias, void *workspace, size_t workspace_bytes,
-                       void *stream) {
+                       const void *rows, int rows_dtype, const int32_t *rows_at, int R_cap, void *dx, int dx_dtype,
+                       float *dw_router, float *d_bias, void *stream) {
   if (T < 0 || k < 1 || k > 32 || E < 1 || E > 1024 || k > E || H < 1 || H > (1 << 20) || (long long)T * k >= kMaxRows ||
       R_cap < 0 || R_cap >= kMaxRows)
     return MOE_ERR_SHAPE;
@@ -185,23 +179,20 @@ int moe_route_backward(const int32_t *topk_ids, const float *topk_w, const float
   const bool weights = dw_router || d_bias;
   if (!dx && !weights) return MOE_ERR_NULL;
   if (T > 0 && (!topk_ids || !topk_w || !d_topk_w || (dx && !w_router) || (dw_router && !x))) return MOE_ERR_NULL;
-  if (weights && (!offsets || (T > 0 && (!row_token || !token_row)))) return MOE_ERR_NULL;
+  if (weights && (!offsets || (T > 0 && !row_token))) return MOE_ERR_NULL;
   if (rows && dx && T > 0 && !rows_at) return MOE_ERR_NULL;
-  const size_t need = moe_route_backward_workspace_size(T, k, H, E);
-  if (weights && need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
   if (!aligned(x, 16) || !aligned(w_router, 16) || !aligned(rows, 16) || !aligned(dx, 16) || !aligned(dw_router, 16) ||
-      (weights && !aligned(workspace, 256)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(d_topk_w, 4) ||
-      !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(token_row, 4) || !aligned(rows_at, 4) ||
-      !aligned(d_bias, 4))
+      !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(d_topk_w, 4) ||
+      !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(rows_at, 4) || !aligned(d_bias, 4))
     return MOE_ERR_ALIGN;
   const size_t A = (size_t)T * k * 4, e = esize(dtype);
-  const void *outs[] = {dx, dw_router, d_bias, weights ? workspace : nullptr};
-  const size_t ob[] = {(size_t)T * H * esize(dx_dtype), (size_t)E * H * 4, (size_t)E * 4, need};
-  const void *ins[] = {topk_ids, topk_w, d_topk_w, x, w_router, offsets, row_token, token_row, rows, rows_at};
-  const size_t ib[] = {A, A, A, (size_t)T * H * e, (size_t)E * H * e, (size_t)(E + 1) * 4, A, A,
+  const void *outs[] = {dx, dw_router, d_bias};
+  const size_t ob[] = {(size_t)T * H * esize(dx_dtype), (size_t)E * H * 4, (size_t)E * 4};
+  const void *ins[] = {topk_ids, topk_w, d_topk_w, x, w_router, offsets, row_token, rows, rows_at};
+  const size_t ib[] = {A, A, A, (size_t)T * H * e, (size_t)E * H * e, (size_t)(E + 1) * 4, A,
                        (size_t)R_cap * H * esize(rows_dtype), A};
-  for (int i = 0; i < 4; i++) {
-    for (int j = 0; j < 10; j++)
+  for (int i = 0; i < 3; i++) {
+    for (int j = 0; j < 9; j++)
       if (overlap(outs[i], ob[i], ins[j], ib[j])) return MOE_ERR_SHAPE;
     for (int j = 0; j < i; j++)
       if (overlap(outs[i], ob[i], outs[j], ob[j])) return MOE_ERR_SHAPE;
@@ -220,7 +211,6 @@ int moe_route_backward(const int32_t *topk_ids, const float *topk_w, const float
   r.bf16 = dtype == MOE_BF16;
   r.offsets = offsets;
   r.row_token = row_token;
-  r.token_row = token_row;
   r.rows = rows;
   r.rows_bf16 = rows_dtype == MOE_BF16;
   r.rows_at = rows_at;
@@ -229,7 +219,6 @@ int moe_route_backward(const int32_t *topk_ids, const float *topk_w, const float
   r.dx_bf16 = dx_dtype == MOE_BF16;
   r.dwr = dw_router;
   r.dbias = d_bias;
-  r.ws = workspace;
   return hip_status(train::launch_route_grad(r, (hipStream_t)stream));
 }
 
@@ -301,11 +290,11 @@ int moe_block_norm_backward(const void *x_out, int x_dtype, const void *y, int y
   if (!aligned(x_out, 16) || !aligned(y, 16) || !aligned(w_next, 16) || !aligned(w_post, 16) || !aligned(gate, 16) ||
       !aligned(dx_out, 16) || !aligned(dn, 16) || !aligned(dx, 16) || !aligned(dy, 16) || !aligned(dw_next, 16) ||
       !aligned(dw_post, 16) || !aligned(d_gate, 16) || !aligned(rstd_next, 4) || !aligned(rstd_post, 4) ||
-      (columns && !aligned(workspace, 256)))
+      (columns && need > 0 && !aligned(workspace, 256)))
     return MOE_ERR_ALIGN;
   const size_t nx = (size_t)T * H * esize(x_dtype), ny = (size_t)T * H * esize(y_dtype), w = esize(w_dtype);
   const size_t ng = gate_kind == 2 ? T : H;
-  const void *outs[] = {dx, dy, dw_next, dw_post, d_gate, columns ? workspace : nullptr};
+  const void *outs[] = {dx, dy, dw_next, dw_post, d_gate, columns && need > 0 ? workspace : nullptr};
   const size_t ob[] = {nx, ny, (size_t)H * 4, (size_t)H * 4, ng * 4, need};
   const void *ins[] = {x_out, y, w_next, w_post, gate, rstd_next, rstd_post, dx_out, dn};
   const size_t ib[] = {nx, ny, H * w, H * w, ng * w, (size_t)T * 4, (size_t)T * 4, nx, nx};

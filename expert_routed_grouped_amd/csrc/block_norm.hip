@@ -218,14 +218,15 @@ __global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(NormArgs a)
       }
     }
   }
-  float *ws = (float *)a.ws + (size_t)blockIdx.x * 3 * H;
+  float *const ws = (float *)a.ws + (size_t)blockIdx.x * 3 * H;
+  const bool alone = gridDim.x == 1;  // the sums are the results
 #pragma unroll
   for (int v = 0; v < NV; v++) {
     const int h = (v * W * 64 + tid) * N;
     if (h < H) {
-      if (a.dw_next) store_n<N>(ws + h, dwn[v]);
-      if (a.dw_post) store_n<N>(ws + H + h, dwp[v]);
-      if (a.d_gate && channel) store_n<N>(ws + 2 * (size_t)H + h, dgc[v]);
+      if (a.dw_next) store_n<N>((alone ? a.dw_next : ws) + h, dwn[v]);
+      if (a.dw_post) store_n<N>((alone ? a.dw_post : ws + H) + h, dwp[v]);
+      if (a.d_gate && channel) store_n<N>((alone ? a.d_gate : ws + 2 * (size_t)H) + h, dgc[v]);
     }
   }
 }
@@ -254,6 +255,8 @@ __global__ __launch_bounds__(kSumWaves * 64) void column_sum_kernel(const float 
 }
 
 constexpr int kMaxBlocks = 512;
+// Workgroups of a backward pass.  Up to four rows one takes them all: a row takes about 1.5 us, a second launch 4.5.
+int blocks(int T) { return T <= 4 ? (T > 0 ? 1 : 0) : (T < kMaxBlocks ? T : kMaxBlocks); }
 
 template <typename TX, typename TY, int W, int NV, int N>
 hipError_t launch(const NormArgs &a, bool backward, hipStream_t s) {
@@ -261,11 +264,11 @@ hipError_t launch(const NormArgs &a, bool backward, hipStream_t s) {
     hipLaunchKernelGGL((block_norm_kernel<TX, TY, W, NV, N>), dim3(a.T), dim3(W * 64), 0, s, a);
     return hipGetLastError();
   }
-  const int G = a.T < kMaxBlocks ? a.T : kMaxBlocks;
+  const int G = blocks(a.T);
   if (G > 0) hipLaunchKernelGGL((block_norm_backward_kernel<TX, TY, W, NV, N>), dim3(G), dim3(W * 64), 0, s, a);
   hipError_t err = hipGetLastError();
   float *gate = a.gate_kind == train::kGateChannel ? a.d_gate : nullptr;
-  if (err != hipSuccess || (!a.dw_next && !a.dw_post && !gate)) return err;
+  if (err != hipSuccess || G == 1 || (!a.dw_next && !a.dw_post && !gate)) return err;
   hipLaunchKernelGGL(column_sum_kernel, dim3(ceil_div_i(a.H, 64), 3), dim3(kSumWaves * 64), 0, s, (const float *)a.ws, G, a.H,
                      a.dw_next, a.dw_post, gate);
   return hipGetLastError();
@@ -294,7 +297,8 @@ hipError_t by_type(const NormArgs &a, bool backward, hipStream_t s) {
 }  // namespace
 
 size_t train::norm_grad_ws_bytes(int T, int H) {
-  return align_up((size_t)(T < kMaxBlocks ? T : kMaxBlocks) * 3 * H * sizeof(float), 256);
+  const int G = blocks(T);
+  return G <= 1 ? 0 : align_up((size_t)G * 3 * H * sizeof(float), 256);
 }
 hipError_t train::launch_block_norm(const NormArgs &a, hipStream_t s) { return by_type(a, false, s); }
 hipError_t train::launch_block_norm_backward(const NormArgs &a, hipStream_t s) { return by_type(a, true, s); }

@@ -54,7 +54,7 @@ struct RouteGradArgs {
   int T, k, E, H;
   const void *x, *wr;         // [T, H], [E, H]
   int bf16;
-  const int32_t *offsets, *row_token, *token_row;  // grouping over all E experts: [E + 1], [T * k], [T, k]
+  const int32_t *offsets, *row_token;  // grouping over all E experts: [E + 1], [T * k]
   const void *rows;           // [R_cap, H] or NULL
   int rows_bf16;
   const int32_t *rows_at;     // [T, k]: row of an assignment in ``rows``, -1 none
@@ -62,9 +62,7 @@ struct RouteGradArgs {
   void *dx;
   int dx_bf16;
   float *dwr, *dbias;
-  void *ws;                   // route_grad_ws_bytes
 };
-size_t route_grad_ws_bytes(int T, int k, int E, int H);
 hipError_t launch_route_grad(const RouteGradArgs &a, hipStream_t s);
 
 enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };

@@ -32,7 +32,7 @@ EXPORTS = ("moe_version", "moe_status_str", "moe_route", "moe_permute", "moe_per
            "moe_dequantize_mx", "moe_mx4_packed_scale_bytes", "moe_pack_mx4", "moe_ffn_mx4_workspace_size",
            "moe_grouped_ffn_mx4", "moe_decode_layer_mx4_workspace_size", "moe_decode_layer_mx4", "moe_grouped_mm",
            "moe_grouped_wgrad_workspace_size", "moe_grouped_wgrad", "moe_swiglu", "moe_swiglu_backward",
-           "moe_route_backward_workspace_size", "moe_route_backward", "moe_block_norm",
+           "moe_route_backward", "moe_block_norm",
            "moe_block_norm_backward_workspace_size", "moe_block_norm_backward")
 MOE_MM_TRANSPOSED, MOE_WGRAD_ADD = 1, 1
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
@@ -130,10 +130,8 @@ def lib():
         L.moe_swiglu.argtypes = [P, I, P, P, I, I, I, P, P]
         L.moe_swiglu_backward.restype = I
         L.moe_swiglu_backward.argtypes = [P, P, I, P, P, I, I, I, P, P, P, P]
-        L.moe_route_backward_workspace_size.restype = Z
-        L.moe_route_backward_workspace_size.argtypes = [I, I, I, I]
         L.moe_route_backward.restype = I
-        L.moe_route_backward.argtypes = [P, P, P, I, I, I, I, P, P, I, P, P, P, P, I, P, I, P, I, P, P, P, Z, P]
+        L.moe_route_backward.argtypes = [P, P, P, I, I, I, I, P, P, I, P, P, P, I, P, I, P, I, P, P, P]
         L.moe_block_norm.restype = I
         L.moe_block_norm.argtypes = [P, I, P, I, P, P, P, I, I, F, F, I, I, P, P, P, P, P]
         L.moe_block_norm_backward_workspace_size.restype = Z
@@ -674,6 +672,11 @@ def _space(workspace: Optional[torch.Tensor], need: int, dev, stream):
     return _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.nbytes, workspace
 
 
+def _index(t: Optional[torch.Tensor], name: str, dev):
+    """Address of a row index of any length (None stays None)."""
+    return None if t is None else _arg(t, name, torch.int32, (t.shape[0],), dev)
+
+
 def moe_grouped_mm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, row_index: Optional[torch.Tensor] = None,
                    transposed: bool = False, out: Optional[torch.Tensor] = None, dtype=None, stream=None) -> torch.Tensor:
     """Rows grouped by expert times their expert's matrix -> out [R_cap, N] of ``dtype`` (default: a's).
@@ -694,7 +697,7 @@ def moe_grouped_mm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, row_
         _out_dtype(a.dtype if dtype is None else dtype)
         out = _new((R, N), a.dtype if dtype is None else dtype, dev, stream)
     args = (_arg(a, "a", a.dtype, (a.shape[0], K), dev),
-            None if row_index is None else _arg(row_index, "row_index", i32, (row_index.shape[0],), dev), a.shape[0],
+            _index(row_index, "row_index", dev), a.shape[0],
             _arg(w, "w", a.dtype, w.shape, dev), _out_dtype(a.dtype), _arg(offsets, "offsets", i32, (El + 1,), dev), El, R, N,
             K, _arg(out, "out", out.dtype, (R, N), dev), _out_dtype(out.dtype), MOE_MM_TRANSPOSED if transposed else 0)
     with _On(dev) as on:
@@ -725,9 +728,9 @@ def moe_grouped_wgrad(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, a
     dt = _out_dtype(a.dtype)
     ws, nws, workspace = _space(workspace, int(lib().moe_grouped_wgrad_workspace_size(El, R, M, N, dt)), dev, stream)
     args = (_arg(a, "a", a.dtype, a.shape, dev),
-            None if a_index is None else _arg(a_index, "a_index", i32, (a_index.shape[0],), dev), a.shape[0],
+            _index(a_index, "a_index", dev), a.shape[0],
             _arg(b, "b", a.dtype, b.shape, dev),
-            None if b_index is None else _arg(b_index, "b_index", i32, (b_index.shape[0],), dev), b.shape[0], dt,
+            _index(b_index, "b_index", dev), b.shape[0], dt,
             _arg(offsets, "offsets", i32, (El + 1,), dev), El, R, M, N, _arg(out, "out", out.dtype, (El, M, N), dev),
             _out_dtype(out.dtype), ws, nws, MOE_WGRAD_ADD if add else 0)
     with _On(dev) as on:
@@ -752,7 +755,7 @@ def moe_swiglu(gu: torch.Tensor, offsets: Optional[torch.Tensor] = None, row_w: 
         h = _new((R, I), gu.dtype, dev, stream)
     off, El = _rows_of(offsets, dev)
     args = (_arg(gu, "gu", gu.dtype, (R, 2 * I), dev), _out_dtype(gu.dtype), off,
-            None if row_w is None else _arg(row_w, "row_w", torch.float32, (R,), dev), El, R, I,
+            _arg(row_w, "row_w", torch.float32, (R,), dev), El, R, I,
             _arg(h, "h", gu.dtype, (R, I), dev))
     with _On(dev) as on:
         _check("moe_swiglu", lib().moe_swiglu(*args, on.stream(stream)))
@@ -774,23 +777,18 @@ def moe_swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, offsets: Optional[to
         d_row_w = _new((R,), f32, dev, stream)
     off, El = _rows_of(offsets, dev)
     args = (_arg(gu, "gu", gu.dtype, (R, 2 * I), dev), _arg(dh, "dh", gu.dtype, (R, I), dev), _out_dtype(gu.dtype), off,
-            None if row_w is None else _arg(row_w, "row_w", f32, (R,), dev), El, R, I,
+            _arg(row_w, "row_w", f32, (R,), dev), El, R, I,
             _arg(dgu, "dgu", gu.dtype, (R, 2 * I), dev), _arg(h, "h", gu.dtype, (R, I), dev),
-            None if d_row_w is None else _arg(d_row_w, "d_row_w", f32, (R,), dev))
+            _arg(d_row_w, "d_row_w", f32, (R,), dev))
     with _On(dev) as on:
         _check("moe_swiglu_backward", lib().moe_swiglu_backward(*args, on.stream(stream)))
     return dgu, h, d_row_w
 
 
-def moe_route_backward_workspace_size(T: int, k: int, H: int, E: int) -> int:
-    return int(lib().moe_route_backward_workspace_size(T, k, H, E))
-
-
 def moe_route_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor, d_topk_w: torch.Tensor, x: torch.Tensor,
                        w_router: torch.Tensor, perm: dict, rows: Optional[torch.Tensor] = None,
                        token_row: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None, dtype=None,
-                       dw_router: Optional[torch.Tensor] = None, d_bias: Optional[torch.Tensor] = None,
-                       workspace: Optional[torch.Tensor] = None, stream=None):
+                       dw_router: Optional[torch.Tensor] = None, d_bias: Optional[torch.Tensor] = None, stream=None):
     """Gradients of the router weight [E, H] and bias [E] (fp32) and of the layer's input [T, H] (``dtype``, default x's)
     from that of the gates -> (dx, dw_router, d_bias).
 
@@ -807,7 +805,6 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor, d_topk_w: t
         d_bias = _new((E,), f32, dev, stream)
     if rows is not None and token_row is None:
         token_row = perm["token_row"]
-    ws, nws, workspace = _space(workspace, int(lib().moe_route_backward_workspace_size(T, k, H, E)), dev, stream)
     row_token = perm["row_token"]
     if row_token.dim() != 1 or row_token.shape[0] < T * k:
         raise ValueError(f"perm must be over all experts: row_token needs T * k = {T * k} entries")
@@ -816,26 +813,26 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor, d_topk_w: t
             _arg(w_router, "w_router", x.dtype, (E, H), dev), _out_dtype(x.dtype),
             _arg(perm["offsets"], "perm offsets", i32, (E + 1,), dev),
             _arg(row_token, "perm row_token", i32, row_token.shape, dev),
-            _arg(perm["token_row"], "perm token_row", i32, (T, k), dev),
             None if rows is None else _arg(rows, "rows", rows.dtype, (rows.shape[0], H), dev),
             MOE_F32 if rows is None else _out_dtype(rows.dtype),
             None if rows is None else _arg(token_row, "token_row", i32, (T, k), dev),
             0 if rows is None else rows.shape[0], _arg(dx, "dx", dx.dtype, (T, H), dev), _out_dtype(dx.dtype),
-            _arg(dw_router, "dw_router", f32, (E, H), dev), _arg(d_bias, "d_bias", f32, (E,), dev), ws, nws)
+            _arg(dw_router, "dw_router", f32, (E, H), dev), _arg(d_bias, "d_bias", f32, (E,), dev))
     with _On(dev) as on:
         _check("moe_route_backward", lib().moe_route_backward(*args, on.stream(stream)))
     return dx, dw_router, d_bias
 
 
-def _norm_weights(T, H, dev, **named):
+def _norm_weights(T, H, dev, w_next, w_post, gate):
     """MOE_* type and gate kind of the norms' weights and gate, and their addresses; all of one type."""
-    given = [t for t in named.values() if t is not None]
-    dt = given[0].dtype if given else torch.float32
-    kind = MOE_GATE_NONE
-    if named["gate"] is not None:
-        kind = MOE_GATE_CHANNEL if named["gate"].dim() == 1 else MOE_GATE_TOKEN
-    shapes = {"gate": (H,) if kind == MOE_GATE_CHANNEL else (T, 1)}
-    return _out_dtype(dt), kind, [None if t is None else _arg(t, n, dt, shapes.get(n, (H,)), dev) for n, t in named.items()]
+    first = w_next if w_next is not None else w_post if w_post is not None else gate
+    if first is None:
+        return MOE_F32, MOE_GATE_NONE, None, None, None
+    dt, kind, row = first.dtype, MOE_GATE_NONE, (H,)
+    if gate is not None:
+        kind = MOE_GATE_CHANNEL if gate.dim() == 1 else MOE_GATE_TOKEN
+    return (_out_dtype(dt), kind, _arg(w_next, "w_next", dt, row, dev), _arg(w_post, "w_post", dt, row, dev),
+            _arg(gate, "gate", dt, row if kind == MOE_GATE_CHANNEL else (T, 1), dev))
 
 
 def moe_block_norm(x: torch.Tensor, w_next: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
@@ -857,11 +854,11 @@ def moe_block_norm(x: torch.Tensor, w_next: Optional[torch.Tensor] = None, y: Op
         n = _new((T, H), x.dtype, dev, stream)
     rn = _new((T,), f32, dev, stream) if stats and w_next is not None else None
     rp = _new((T,), f32, dev, stream) if stats and w_post is not None else None
-    wdt, kind, (wn, wp, g) = _norm_weights(T, H, dev, w_next=w_next, w_post=w_post, gate=gate)
-    args = (_arg(x, "x", x.dtype, (T, H), dev), _out_dtype(x.dtype),
-            None if y is None else _arg(y, "y", y.dtype, (T, H), dev), MOE_F32 if y is None else _out_dtype(y.dtype), wn, wp,
-            g, wdt, kind, scale, eps, T, H, None if x_out is None else _arg(x_out, "x_out", x.dtype, (T, H), dev),
-            None if n is None else _arg(n, "n", x.dtype, (T, H), dev), None if rn is None else rn.data_ptr(),
+    wdt, kind, wn, wp, g = _norm_weights(T, H, dev, w_next, w_post, gate)
+    xdt, all_ = x.dtype, (T, H)
+    yp, ydt = (None, MOE_F32) if y is None else (_arg(y, "y", y.dtype, all_, dev), _out_dtype(y.dtype))
+    args = (_arg(x, "x", xdt, all_, dev), _out_dtype(xdt), yp, ydt, wn, wp, g, wdt, kind, scale, eps, T, H,
+            _arg(x_out, "x_out", xdt, all_, dev), _arg(n, "n", xdt, all_, dev), None if rn is None else rn.data_ptr(),
             None if rp is None else rp.data_ptr())
     with _On(dev) as on:
         _check("moe_block_norm", lib().moe_block_norm(*args, on.stream(stream)))
@@ -894,18 +891,16 @@ def moe_block_norm_backward(x_out: torch.Tensor, w_next: Optional[torch.Tensor] 
     dwp = _new((H,), f32, dev, stream) if w_post is not None else None
     dg = _new(gate.shape, f32, dev, stream) if gate is not None else None
     ws, nws, workspace = _space(workspace, int(lib().moe_block_norm_backward_workspace_size(T, H)), dev, stream)
-    wdt, kind, (wn, wp, g) = _norm_weights(T, H, dev, w_next=w_next, w_post=w_post, gate=gate)
-
-    def at(t, name, dtype, shape):
-        return None if t is None else _arg(t, name, dtype, shape, dev)
-
-    xdt = x_out.dtype
-    args = (_arg(x_out, "x_out", xdt, (T, H), dev), _out_dtype(xdt), at(y, "y", y.dtype if y is not None else f32, (T, H)),
-            MOE_F32 if y is None else _out_dtype(y.dtype), wn, wp, g, wdt, kind, scale,
-            at(rstd_next, "rstd_next", f32, (T,)), at(rstd_post, "rstd_post", f32, (T,)), at(dx_out, "dx_out", xdt, (T, H)),
-            at(dn, "dn", xdt, (T, H)), T, H, _arg(dx, "dx", xdt, (T, H), dev),
-            at(dy, "dy", y.dtype if y is not None else f32, (T, H)), None if dwn is None else dwn.data_ptr(),
-            None if dwp is None else dwp.data_ptr(), None if dg is None else dg.data_ptr(), ws, nws)
+    wdt, kind, wn, wp, g = _norm_weights(T, H, dev, w_next, w_post, gate)
+    xdt, all_ = x_out.dtype, (T, H)
+    yp, dyp, ydt = None, None, MOE_F32
+    if y is not None:
+        yp, dyp, ydt = _arg(y, "y", y.dtype, all_, dev), _arg(dy, "dy", y.dtype, all_, dev), _out_dtype(y.dtype)
+    args = (_arg(x_out, "x_out", xdt, all_, dev), _out_dtype(xdt), yp, ydt, wn, wp, g, wdt, kind, scale,
+            _arg(rstd_next, "rstd_next", f32, (T,), dev), _arg(rstd_post, "rstd_post", f32, (T,), dev),
+            _arg(dx_out, "dx_out", xdt, all_, dev), _arg(dn, "dn", xdt, all_, dev), T, H, _arg(dx, "dx", xdt, all_, dev), dyp,
+            None if dwn is None else dwn.data_ptr(), None if dwp is None else dwp.data_ptr(),
+            None if dg is None else dg.data_ptr(), ws, nws)
     with _On(dev) as on:
         _check("moe_block_norm_backward", lib().moe_block_norm_backward(*args, on.stream(stream)))
     return {"dx": dx, "dy": dy, "dw_next": dwn, "dw_post": dwp, "dgate": dg}

@@ -705,9 +705,6 @@ int moe_swiglu(const void *gu, int dtype, const int32_t *offsets, const float *r
 int moe_swiglu_backward(const void *gu, const void *dh, int dtype, const int32_t *offsets, const float *row_w, int E_loc,
                         int R_cap, int I, void *dgu, void *h, float *d_row_w, void *stream);
 
-/* Bytes of workspace moe_route_backward needs for dw_router or d_bias. */
-size_t moe_route_backward_workspace_size(int T, int k, int H, int E);
-
 /*
  * moe_route_backward - from the gradient of the gates to those of the router and of the layer's input.
  *
@@ -718,21 +715,17 @@ size_t moe_route_backward_workspace_size(int T, int k, int H, int E);
  *   dx[t, :]       = sum over j of dl[t, j] w_router[topk_ids[t, j], :] + sum over j with rows_at[t, j] >= 0 of
  *                    rows[rows_at[t, j], :]
  * ``rows`` [R_cap, H] are the input gradients of the experts' rows (rows_dtype), rows_at [T, k] the token_row of the
- * local experts' moe_permute; rows NULL: none.  offsets [E + 1], row_token [T*k] and token_row [T, k] are those of
- * moe_permute over all E experts (e_begin 0, e_end E); a layer that holds them all passes the same maps twice.  They
- * are read for dw_router and d_bias only.  Outputs that are NULL are not computed.  x [T, H] and w_router [E, H]
+ * local experts' moe_permute; rows NULL: none.  offsets [E + 1] and row_token [T*k] are those of moe_permute over all
+ * E experts (e_begin 0, e_end E), whether this rank holds them or not.  They are read for dw_router and d_bias only.  Outputs that are NULL are not computed.  x [T, H] and w_router [E, H]
  * of type ``dtype``, dx [T, H] of type dx_dtype (MOE_BF16 or MOE_F32).  Sums in fp32, in an order that the routing
- * alone fixes.  Gates that other ranks' experts contribute to must be summed over the ranks first.  workspace
- * (for dw_router or d_bias): at least moe_route_backward_workspace_size(...) bytes, 256-byte aligned, contents free.
- * T == 0 writes zeros to dw_router and d_bias.
+ * alone fixes.  Gates that other ranks' experts contribute to must be summed over the ranks first.  T == 0 writes zeros to dw_router and d_bias.
  * Errors: MOE_ERR_SHAPE (E <= 1024, 1 <= k <= min(E, 32), H <= 2^20, T*k < 2^28, overlapping buffers),
- * MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_WORKSPACE, MOE_ERR_ALIGN (16 bytes), MOE_ERR_HIP.
+ * MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN (16 bytes), MOE_ERR_HIP.
  */
 int moe_route_backward(const int32_t *topk_ids, const float *topk_w, const float *d_topk_w, int T, int k, int E, int H,
                        const void *x, const void *w_router, int dtype, const int32_t *offsets, const int32_t *row_token,
-                       const int32_t *token_row, const void *rows, int rows_dtype, const int32_t *rows_at, int R_cap,
-                       void *dx, int dx_dtype, float *dw_router, float *d_bias, void *workspace, size_t workspace_bytes,
-                       void *stream);
+                       const void *rows, int rows_dtype, const int32_t *rows_at, int R_cap, void *dx, int dx_dtype,
+                       float *dw_router, float *d_bias, void *stream);
 
 /* gate_kind of the block norms */
 #define MOE_GATE_NONE 0
@@ -757,7 +750,7 @@ int moe_block_norm(const void *x, int x_dtype, const void *y, int y_dtype, const
                    const void *gate, int w_dtype, int gate_kind, float scale, float eps, int T, int H, void *x_out, void *n,
                    float *rstd_next, float *rstd_post, void *stream);
 
-/* Bytes of workspace moe_block_norm_backward needs for dw_next, dw_post and a channel gate's gradient. */
+/* Bytes of workspace moe_block_norm_backward needs for dw_next, dw_post and a channel gate's gradient (0 for few rows). */
 size_t moe_block_norm_backward_workspace_size(int T, int H);
 
 /*

@@ -97,29 +97,23 @@ def test_swiglu_backward(kw, code):
     assert backward(**kw) == code
 
 
-route = call("moe_route_backward", "ids g d T k E H x wr dt off rt tr rows rd at R dx xd dw db ws nws".split(),
-             dict(ids=A, g=B, d=C, T=8, k=2, E=4, H=64, x=D, wr=E_, dt=1, off=F, rt=G, tr=H_, rows=I_, rd=1, at=J, R=16, dx=K_, xd=0,
-                  dw=L_, db=M_, ws=N_, nws=1 << 20))
+route = call("moe_route_backward", "ids g d T k E H x wr dt off rt rows rd at R dx xd dw db".split(),
+             dict(ids=A, g=B, d=C, T=8, k=2, E=4, H=64, x=D, wr=E_, dt=1, off=F, rt=G, rows=I_, rd=1, at=J, R=16, dx=K_, xd=0,
+                  dw=L_, db=M_))
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), -2), (dict(k=0), -2), (dict(k=5), -2), (dict(k=33, E=64), -2), (dict(E=1025), -2), (dict(H=0), -2), (dict(H=(1 << 20) + 1), -2),
     (dict(T=1 << 27), -2), (dict(R=-1), -2), (dict(dt=2), -3), (dict(xd=2), -3), (dict(rd=2), -3),
     (dict(ids=None), -1), (dict(g=None), -1), (dict(d=None), -1), (dict(x=None), -1), (dict(wr=None), -1), (dict(off=None), -1),
-    (dict(rt=None), -1), (dict(tr=None), -1), (dict(at=None), -1), (dict(dx=None, dw=None, db=None), -1),
-    (dict(ws=None), -4), (dict(nws=8), -4), (dict(x=off(D, 8)), -6), (dict(wr=off(E_, 8)), -6), (dict(rows=off(I_, 8)), -6),
-    (dict(dx=off(K_, 8)), -6), (dict(dw=off(L_, 4)), -6), (dict(ws=off(N_, 16)), -6), (dict(ids=ODD.value and off(A, 2)), -6),
-    (dict(dx=D), -2), (dict(dx=I_), -2), (dict(dw=E_), -2), (dict(db=L_), -2), (dict(ws=K_), -2), (dict(db=B), -2),
+    (dict(rt=None), -1), (dict(at=None), -1), (dict(dx=None, dw=None, db=None), -1),
+    (dict(x=off(D, 8)), -6), (dict(wr=off(E_, 8)), -6), (dict(rows=off(I_, 8)), -6),
+    (dict(dx=off(K_, 8)), -6), (dict(dw=off(L_, 4)), -6), (dict(ids=ODD.value and off(A, 2)), -6),
+    (dict(dx=D), -2), (dict(dx=I_), -2), (dict(dw=E_), -2), (dict(db=L_), -2), (dict(db=B), -2),
     (dict(T=0, dw=None, db=None), 0),
 ])
 def test_route_backward(kw, code):
     assert route(**kw) == code
-
-
-def test_route_backward_workspace():
-    size = moe.moe_route_backward_workspace_size
-    assert size(8, 2, 64, 4) >= 64 and size(0, 2, 64, 4) >= 0
-    assert size(-1, 2, 64, 4) == size(8, 0, 64, 4) == size(8, 5, 64, 4) == size(8, 2, 64, 1025) == size(8, 2, 0, 4) == 0
 
 
 norm = call("moe_block_norm", "x xd y yd wn wp g wd gk sc eps T H xo n rn rp".split(),
@@ -162,14 +156,14 @@ T, E, K, H, I = 4, 4, 2, 64, 32
 bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
 i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
 f32 = lambda *s: torch.zeros(s)  # noqa: E731
-PERM = dict(offsets=i32(E + 1), row_token=i32(T * K), token_row=i32(T, K))
+PERM = dict(offsets=i32(E + 1), row_token=i32(T * K))
 CALLS = {  # name: (tensors it allocates, the call)
     "moe_grouped_mm": (1, lambda s: moe.moe_grouped_mm(bf(T, H), bf(E, I, H), i32(E + 1), row_index=i32(T * K), stream=s)),
     "moe_swiglu": (1, lambda s: moe.moe_swiglu(bf(T, 2 * I), stream=s)),
     "moe_swiglu_backward": (3, lambda s: moe.moe_swiglu_backward(bf(T, 2 * I), bf(T, I), row_w=f32(T), stream=s)),
-    "moe_route_backward": (4, lambda s: moe.moe_route_backward(i32(T, K), f32(T, K), f32(T, K), bf(T, H), bf(E, H), PERM, stream=s)),
+    "moe_route_backward": (3, lambda s: moe.moe_route_backward(i32(T, K), f32(T, K), f32(T, K), bf(T, H), bf(E, H), PERM, stream=s)),
     "moe_block_norm": (4, lambda s: moe.moe_block_norm(bf(T, H), f32(H), y=f32(T, H), w_post=f32(H), stats=True, stream=s)),
-    "moe_block_norm_backward": (6, lambda s: moe.moe_block_norm_backward(
+    "moe_block_norm_backward": (5, lambda s: moe.moe_block_norm_backward(
         bf(T, H), f32(H), f32(T), bf(T, H), y=f32(T, H), w_post=f32(H), rstd_post=f32(T), gate=f32(H), stream=s)),
 }
 
