@@ -309,7 +309,7 @@ hipError_t launch_wgrad(const train::WgradArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t train::launch_grouped_mm(const MmArgs &a, hipStream_t s) {
-  if (a.R_cap > 32LL * a.El && mm_dma_fits(a)) return launch_mm_dma(a, s);
+  if (mm_dma_fits(a)) return launch_mm_dma(a, s);
   if (!a.bf16) return pick_mm<float, float>(a, s);
   return a.out_bf16 ? pick_mm<uint16_t, uint16_t>(a, s) : pick_mm<uint16_t, float>(a, s);
 }

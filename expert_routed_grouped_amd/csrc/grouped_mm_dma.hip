@@ -5,9 +5,8 @@
 // rows (activations; weights of a projection): its tile keeps rows of 64 values in LDS, 16-byte chunk c of row r in slot
 // c ^ (r / 2 % 8), and a fragment of v_mfma_f32_32x32x16_bf16 is one 16-byte LDS read.  An "mn-major" operand has an output
 // axis along its rows (weights for an input gradient; both operands of a weight gradient): its tile keeps whole k rows,
-// and a fragment is two transposing 8-byte LDS reads, each four k rows of 16 columns.  The 32-byte pieces p of k row r lie
-// at p ^ (2 (r % 4) + r / 8 % 2), so that the four rows of two neighbouring pieces, which half a wave reads at once,
-// meet all 64 banks.
+// and a fragment is two transposing 8-byte LDS reads, each four k rows of 16 columns.  The 32-byte pieces of a k row
+// are turned (below), so that the four rows of two neighbouring pieces, which half a wave reads at once, meet all 64 banks.
 //
 // Tiles of 256 x 256 outputs, eight waves of 128 x 64, 64 values of the contraction a step; the second operand, whose
 // first touch comes from memory, is fetched two steps ahead through three slots, the first one step ahead through two
@@ -35,6 +34,12 @@ __device__ __forceinline__ void barrier_no_fence() { asm volatile("s_barrier" ::
 typedef uint32_t rsrc_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void dma(rsrc_t r, uint32_t to, uint32_t voff, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(to), "v"(voff), "s"(r), "s"(soff)
+               : "m0");
+}
+// The same for lines that are read once.
+__device__ __forceinline__ void dma_once(rsrc_t r, uint32_t to, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(to), "v"(voff), "s"(r),
+               "s"(soff)
                : "m0");
 }
 // The same for four bytes a lane.
@@ -65,6 +70,14 @@ struct Cfg {
   static_assert(NA >= 1 && NBL >= 1 && LDS <= 160 * 1024, "whole loads, one compute unit's LDS");
 };
 
+// Where an mn-major tile of R columns keeps the 32-byte piece p of k row k: at p ^ turn<R>(k).  Half a wave reads two
+// neighbouring pieces of k rows 4c .. 4c + 3 (bit 3 of k is the same in it): with R >= 128 a row starts at bank 0, with
+// R = 64 every other one does.
+template <int R>
+__device__ __forceinline__ constexpr int turn(int k) {
+  return R >= 128 ? 2 * (k & 3) + ((k >> 3) & 1) : k & 2;
+}
+
 // What a wave loads of an operand: byte offsets of its N segments of 1 KB at step 0, and their advance.
 template <int N, int NW>
 struct Source {
@@ -76,10 +89,15 @@ struct Source {
   __device__ __forceinline__ void start(int) {}
   // The first COUNT segments of step kt.
   template <int COUNT = N>
-  __device__ __forceinline__ void load(uint32_t to, int wave, int, int kt, bool is_last) {
+  __device__ __forceinline__ void load(uint32_t to, int wave, int, int kt, bool is_last, bool once = false) {
     const uint32_t so = (uint32_t)kt * step, m = is_last ? last : 0u;
+    if (once) {
 #pragma unroll
-    for (int u = 0; u < COUNT; u++) dma(r, to + (wave + NW * u) * 1024, off[u] | m, so);
+      for (int u = 0; u < COUNT; u++) dma_once(r, to + (wave + NW * u) * 1024, off[u] | m, so);
+    } else {
+#pragma unroll
+      for (int u = 0; u < COUNT; u++) dma(r, to + (wave + NW * u) * 1024, off[u] | m, so);
+    }
   }
   // k-major tile, BK = 64: segment s holds rows 8s .. 8s + 7.  ``row`` gives the byte offset of
   // segment u's tile row.
@@ -112,7 +130,7 @@ struct Source {
   template <int R>
   static __device__ __forceinline__ uint32_t in_row(int seg, int lane) {
     const int k = k_row<R>(seg, lane), slot = lane % (R / 8);
-    return (uint32_t)((slot >> 1) ^ (2 * (k & 3) + ((k >> 3) & 1))) * 32u + (uint32_t)(slot & 1) * 16u;
+    return (uint32_t)((slot >> 1) ^ turn<R>(k)) * 32u + (uint32_t)(slot & 1) * 16u;
   }
 };
 
@@ -159,12 +177,20 @@ struct Frag {
       const int i = lane & 15, h = (lane >> 4) & 1, g = lane >> 5;
 #pragma unroll
       for (int b = 0; b < B; b++)
-        base[b] = (uint32_t)(8 * g + (i >> 2)) * (R * 2) + (uint32_t)((r0 / 16 + 2 * b + h) ^ (2 * (i >> 2) + g)) * 32u +
+        base[b] = (uint32_t)(8 * g + (i >> 2)) * (R * 2) + (uint32_t)((r0 / 16 + 2 * b + h) ^ turn<R>(8 * g + (i >> 2))) * 32u +
                   (uint32_t)(i & 3) * 8u;
     } else {
       const int n = lane & 31, g = lane >> 5;
 #pragma unroll
       for (int kk = 0; kk < 4; kk++) base[kk] = (uint32_t)(r0 + n) * 128u + (uint32_t)((2 * kk + g) ^ ((n >> 1) & 7)) * 16u;
+    }
+  }
+  // The same with kk known at run time only.
+  __device__ __forceinline__ bf16x8_t at(const char *slot, int kk, int b) const {
+    if constexpr (MN) return get(slot + kk * 16 * (R * 2), 0, b);
+    else {
+      const uint32_t o = kk == 0 ? base[0] : kk == 1 ? base[1] : kk == 2 ? base[2] : base[3];
+      return *(const bf16x8_t *)(slot + o + b * 4096);
     }
   }
   __device__ __forceinline__ bf16x8_t get(const char *slot, int kk, int b) const {
@@ -247,6 +273,7 @@ using Mm = Cfg<256, 256, 64, 2, 4, 2, 3>;
 // up to its group of G have, so that a tile is found with one ballot and at most G scalar loads.
 struct MmTile {
   int nt, r0, rows, trows;
+  bool once;  // the expert's only tile of rows: its matrix is read once
   const void *w;
 };
 template <typename C>
@@ -282,6 +309,7 @@ struct MmTiles {
     t.nt = rr / mtiles;
     t.trows = min(C::BM, ((cnt + mtiles - 1) / mtiles + 63) & ~63);
     t.r0 = beg + (rr - t.nt * mtiles) * t.trows;
+    t.once = mtiles == 1;
     t.rows = min(t.trows, beg + cnt - t.r0);
     t.w = (const char *)p.w + (size_t)e * p.N * p.K * 2;
     return t;
@@ -331,20 +359,22 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
     if constexpr (KN) sb.template mn_major<C::BN, C::BK>(wave, lane, (uint32_t)p.N * 2u, t.nt * C::BN * 2u);
     else sb.k_major(wave, lane, K, [&](int, int r) { return (uint32_t)min(t.nt * C::BN + r, p.N - 1) * lda; });
   };
-  auto first = [&](int trows) __attribute__((always_inline)) {  // the loads that run ahead of a tile
+  // The loads that run ahead of a tile.  A matrix that one tile reads goes past the caches (512 tokens, 32 rows an expert: 308 us
+  // without, 288; transposed 289 and 259), one that two tiles share does not (6000 tokens: 656 us, 701 with).
+  auto first = [&](int trows, bool once) __attribute__((always_inline)) {
     if (trows > 192) sa.template load<4>(ta, wave, lane, 0, KT == 1);
     else if (trows > 128) sa.template load<3>(ta, wave, lane, 0, KT == 1);
     else if (trows > 64) sa.template load<2>(ta, wave, lane, 0, KT == 1);
     else sa.template load<1>(ta, wave, lane, 0, KT == 1);
-    sb.load(tb, wave, lane, 0, KT == 1);
-    if (KT > 1) sb.load(tb + C::B_BYTES, wave, lane, 1, KT == 2);
+    sb.load(tb, wave, lane, 0, KT == 1, once);
+    if (KT > 1) sb.load(tb + C::B_BYTES, wave, lane, 1, KT == 2, once);
   };
   const Frag<KN, C::BN, C::NB> fb(n0, lane);
   f32x16_t acc[C::MB][C::NB];
   bool stored = false;  // exactly the stores of a whole tile are younger than the loads of this tile's first step
 
   // One tile of MB blocks of 32 rows for either half of the waves; the outputs are the caller's to store.
-  auto contract = [&](auto MC, int m0) __attribute__((always_inline)) {
+  auto contract = [&](auto MC, int m0, bool once) __attribute__((always_inline)) {
     constexpr int MB = decltype(MC)::value;
     const Frag<false, C::BM, MB> fa(m0, lane);
 #pragma unroll
@@ -376,7 +406,7 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
       for (int kk = 0; kk < 4; kk++) {
         if (kk < 3) frags(kk + 1);
         if (kk == 0 && kt + 1 < KT) sa.template load<MB>(ta + A1 * C::A_BYTES, wave, lane, kt + 1, kt + 2 == KT);
-        if (kk == 2 && kt + 2 < KT) sb.load(tb + B2 * C::B_BYTES, wave, lane, kt + 2, kt + 3 == KT);
+        if (kk == 2 && kt + 2 < KT) sb.load(tb + B2 * C::B_BYTES, wave, lane, kt + 2, kt + 3 == KT, once);
 #pragma unroll
         for (int i = 0; i < MB; i++)
 #pragma unroll
@@ -397,7 +427,7 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
   MmTile t = tiles.at(L, p);
   rows_of(t);
   place(t);
-  first(t.trows);
+  first(t.trows, t.once);
   for (;;) {
     const bool more = L + kWorkers / 8 < end;
     const MmTile tn = tiles.at(more ? L + kWorkers / 8 : L, p);
@@ -407,11 +437,11 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
     const bool full = t.rows == t.trows && cols >= C::BN;
     auto body = [&](auto MC) __attribute__((always_inline)) {
       constexpr int MB = decltype(MC)::value;
-      contract(MC, m0);
+      contract(MC, m0, t.once);
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every wave has read its last fragments
       if (more) {
         place(tn);
-        first(tn.trows);
+        first(tn.trows, tn.once);
       }
       if (full) store<MB, C::NB, false, false, true>(acc, stage, out, p.N, m0, n0, t.rows, cols, lane);
       else store<MB, C::NB, false, false, false>(acc, stage, out, p.N, m0, n0, t.rows, cols, lane);
@@ -430,13 +460,116 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
 #endif
 }
 
+// Few rows an expert: the matrices are read once, so what counts is how much of them is under way.  Tiles of up to 32 rows
+// x 64 columns, 64 values of the contraction a step, six steps in LDS (72 KB, two workgroups on a compute unit); each of four
+// waves multiplies a quarter of every step, and the quarters are joined at the end.
+struct Few {
+  static constexpr int BM = 32, BN = 64, BK = 64, NW = 4, NTHR = 256, S = 6;
+  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, LDS = S * (A_BYTES + B_BYTES);
+  static constexpr int NA = A_BYTES / 1024 / NW, NBL = B_BYTES / 1024 / NW;
+  static constexpr int PITCH = BN * 4 + 16;  // bytes between the rows of a quarter's sums
+  static_assert(NW * BM * PITCH <= LDS, "the quarters fit");
+};
+
+template <bool KN, bool GATHER, typename TO>
+__global__ __launch_bounds__(Few::NTHR, 2) void mm_few_kernel(train::MmArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  using C = Few;
+  __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const MmTiles<C> tiles(p, lane);
+  if ((int)blockIdx.x >= tiles.total) return;
+  const int xcd = blockIdx.x & 7, q = tiles.total >> 3, rem = tiles.total & 7;  // runs of tiles to an XCD
+  const MmTile t = tiles.at(xcd * q + min(xcd, rem) + (blockIdx.x >> 3), p);
+  const int K = p.K, KT = (K + C::BK - 1) / C::BK, rows = t.rows;
+  const uint32_t lda = (uint32_t)K * 2u;
+  Source<C::NA, C::NW> sa;
+  Source<C::NBL, C::NW> sb;
+  if constexpr (GATHER) sa.r = resource(p.a, (size_t)p.a_rows * lda);
+  else sa.r = resource((const char *)p.a + (size_t)t.r0 * lda, (size_t)rows * lda);
+  sa.k_major(wave, lane, K, [&](int, int r) {
+    const int at = min(r, rows - 1);  // rows past the end repeat the last one; nothing of them is stored
+    return (uint32_t)(GATHER ? min(max(p.a_index[t.r0 + at], 0), p.a_rows - 1) : at) * lda;
+  });
+  sb.r = resource(t.w, (size_t)p.N * K * 2);
+  if constexpr (KN) sb.template mn_major<C::BN, C::BK>(wave, lane, (uint32_t)p.N * 2u, t.nt * C::BN * 2u);
+  else sb.k_major(wave, lane, K, [&](int, int r) { return (uint32_t)min(t.nt * C::BN + r, p.N - 1) * lda; });
+  const uint32_t to = lds_at(lds);
+  // Step kt into its slot.  Steps past the end load nothing (every lane's offset is nowhere), so that the count below holds.
+  int slot = 0;
+  auto load = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t m = kt < KT ? (kt == KT - 1 ? sa.last : 0u) : kNowhere, at = to + slot * (C::A_BYTES + C::B_BYTES);
+    const uint32_t mb = kt < KT ? (kt == KT - 1 ? sb.last : 0u) : kNowhere;
+    const int k = min(kt, KT - 1);
+#pragma unroll
+    for (int u = 0; u < C::NA; u++) dma(sa.r, at + (wave + C::NW * u) * 1024, sa.off[u] | m, (uint32_t)k * sa.step);
+#pragma unroll
+    for (int u = 0; u < C::NBL; u++) {
+      if (t.once) dma_once(sb.r, at + C::A_BYTES + (wave + C::NW * u) * 1024, sb.off[u] | mb, (uint32_t)k * sb.step);
+      else dma(sb.r, at + C::A_BYTES + (wave + C::NW * u) * 1024, sb.off[u] | mb, (uint32_t)k * sb.step);
+    }
+    slot = slot + 1 == C::S ? 0 : slot + 1;
+  };
+  for (int kt = 0; kt < C::S - 1; kt++) load(kt);
+  const Frag<false, C::BM, 1> fa(0, lane);
+  const Frag<KN, C::BN, 2> fb(0, lane);
+  f32x16_t acc[2];
+#pragma unroll
+  for (int j = 0; j < 2; j++)
+#pragma unroll
+    for (int r = 0; r < 16; r++) acc[j][r] = 0.0f;
+  int rd = 0;
+  for (int kt = 0; kt < KT; kt++) {
+    // the step's loads have landed; the slot that is filled next was read a step ago
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((C::NA + C::NBL) * (C::S - 2)) : "memory");
+    const char *a = lds + rd * (C::A_BYTES + C::B_BYTES), *b = a + C::A_BYTES;
+    const bf16x8_t af = fa.at(a, wave, 0), b0 = fb.at(b, wave, 0), b1 = fb.at(b, wave, 1);
+    load(kt + C::S - 1);
+    acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b0, af, acc[0], 0, 0, 0);
+    acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b1, af, acc[1], 0, 0, 0);
+    rd = rd + 1 == C::S ? 0 : rd + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  // acc[j][r] at lane l: row l % 32, column 32 j + 8 (r / 4) + 4 (l / 32) + r % 4
+  char *const mine = lds + (wave * C::BM + (lane & 31)) * C::PITCH + 16 * (lane >> 5);
+#pragma unroll
+  for (int j = 0; j < 2; j++)
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      *(float4 *)(mine + (32 * j + 8 * i) * 4) = make_float4(acc[j][4 * i], acc[j][4 * i + 1], acc[j][4 * i + 2], acc[j][4 * i + 3]);
+  __syncthreads();
+  const int cols = p.N - t.nt * C::BN, n = threadIdx.x % 16 * 4;
+  if (n >= cols) return;
+  TO *const out = (TO *)p.out + (size_t)t.r0 * p.N + t.nt * C::BN + n;
+  for (int m = threadIdx.x / 16; m < rows; m += C::NTHR / 16) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < C::NW; w++) {
+      const float4 v = *(const float4 *)(lds + (w * C::BM + m) * C::PITCH + n * 4);
+      s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+    }
+    train::store_n<4>(out + (size_t)m * p.N, s);
+  }
+#endif
+}
+
 template <bool KN, bool GATHER, typename TO>
 hipError_t launch(const train::MmArgs &a, hipStream_t s) {
   hipLaunchKernelGGL((mm_dma_kernel<KN, GATHER, TO>), dim3(kWorkers), dim3(Mm::NTHR), 0, s, a);
   return hipGetLastError();
 }
+template <bool KN, bool GATHER, typename TO>
+hipError_t launch_few(const train::MmArgs &a, hipStream_t s) {
+  const long long mt = std::min(((long long)a.R_cap + (long long)a.El * (Few::BM - 1)) / Few::BM, (long long)a.R_cap);
+  hipLaunchKernelGGL((mm_few_kernel<KN, GATHER, TO>), dim3((unsigned)(mt * ceil_div_i(a.N, Few::BN))), dim3(Few::NTHR), 0, s, a);
+  return hipGetLastError();
+}
 template <bool KN, bool GATHER>
 hipError_t by_out(const train::MmArgs &a, hipStream_t s) {
+  // Few rows an expert on average.  128 experts of 1536 x 4096, top 8, us with the tiles for few rows and with the large ones: 64
+  // tokens 231 and 245, 256 247 and 268, 384 263 and 283, 512 363 and 288; transposed 8 tokens 114 and 127, 24 200 and 206, 64
+  // 243 and 234, 512 376 and 259.
+  if (a.R_cap <= (KN ? 2LL : 24LL) * a.El) return a.out_bf16 ? launch_few<KN, GATHER, uint16_t>(a, s) : launch_few<KN, GATHER, float>(a, s);
   return a.out_bf16 ? launch<KN, GATHER, uint16_t>(a, s) : launch<KN, GATHER, float>(a, s);
 }
 template <bool KN>
