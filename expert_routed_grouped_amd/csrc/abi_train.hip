@@ -273,7 +273,7 @@ size_t moe_block_norm_backward_workspace_size(int T, int H) { return norm_sizes_
 int moe_block_norm_backward(const void *x_out, int x_dtype, const void *y, int y_dtype, const void *w_next,
                             const void *w_post, const void *gate, int w_dtype, int gate_kind, float scale,
                             const float *rstd_next, const float *rstd_post, const void *dx_out, const void *dn, int T, int H,
-                            void *dx, void *dy, float *dw_next, float *dw_post, float *d_gate, void *workspace,
+                            void *dx, void *dy, int dy_dtype, float *dw_next, float *dw_post, float *d_gate, void *workspace,
                             size_t workspace_bytes, void *stream) {
   if (!norm_sizes_ok(T, H) || gate_kind < 0 || gate_kind > 2) return MOE_ERR_SHAPE;
   if (T > 0 && ((gate != nullptr) != (gate_kind != 0) || (!y && (w_post || gate || dy || scale != 1.0f)) ||
@@ -282,6 +282,7 @@ int moe_block_norm_backward(const void *x_out, int x_dtype, const void *y, int y
   if ((dw_next && !w_next) || (dw_post && !w_post)) return MOE_ERR_SHAPE;
   if (!is_float(x_dtype) || (y && !is_float(y_dtype)) || ((w_next || w_post || gate) && !is_float(w_dtype)))
     return MOE_ERR_DTYPE;
+  if (dy && !is_float(dy_dtype)) return MOE_ERR_DTYPE;
   if (T > 0 && !dx && !dy && !dw_next && !dw_post && !d_gate) return MOE_ERR_NULL;
   if (T > 0 && ((!dn && !dx_out) || (dn && (!x_out || !w_next || !rstd_next)) || (w_post && !rstd_post))) return MOE_ERR_NULL;
   const bool columns = dw_next || dw_post || (d_gate && gate_kind == 1);
@@ -295,7 +296,7 @@ int moe_block_norm_backward(const void *x_out, int x_dtype, const void *y, int y
   const size_t nx = (size_t)T * H * esize(x_dtype), ny = (size_t)T * H * esize(y_dtype), w = esize(w_dtype);
   const size_t ng = gate_kind == 2 ? T : H;
   const void *outs[] = {dx, dy, dw_next, dw_post, d_gate, columns && need > 0 ? workspace : nullptr};
-  const size_t ob[] = {nx, ny, (size_t)H * 4, (size_t)H * 4, ng * 4, need};
+  const size_t ob[] = {nx, (size_t)T * H * esize(dy_dtype), (size_t)H * 4, (size_t)H * 4, ng * 4, need};
   const void *ins[] = {x_out, y, w_next, w_post, gate, rstd_next, rstd_post, dx_out, dn};
   const size_t ib[] = {nx, ny, H * w, H * w, ng * w, (size_t)T * 4, (size_t)T * 4, nx, nx};
   for (int i = 0; i < 6; i++) {
@@ -323,6 +324,7 @@ int moe_block_norm_backward(const void *x_out, int x_dtype, const void *y, int y
   a.dn = dn;
   a.dx = dx;
   a.dy = dy;
+  a.dy_bf16 = dy_dtype == MOE_BF16;
   a.dw_next = dw_next;
   a.dw_post = dw_post;
   a.d_gate = d_gate;

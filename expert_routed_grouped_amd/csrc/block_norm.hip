@@ -13,6 +13,8 @@
 // workgroup over its rows and joined by a second launch, in a fixed order.
 #include "train.h"
 
+#include <type_traits>
+
 namespace {
 
 using train::load_n;
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(W * 64) void block_norm_kernel(NormArgs a) {
 }
 
 // Partial column sums of one workgroup: dw_next, dw_post and a channel gate's, [3][H] each.
-template <typename TX, typename TY, int W, int NV, int N>
+template <typename TX, typename TY, typename TD, int W, int NV, int N>
 __global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(NormArgs a) {
   __shared__ float buf[2 * 3 * W];
   const int H = a.H, tid = threadIdx.x;
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(NormArgs a)
             dwp[v][i] = fmaf(du, yh[v][i], dwp[v][i]);
             o[i] = a.w_post ? rp * (du * w[i] - yh[v][i] * q) : du;
           }
-          if (a.dy) store_n<N>((TY *)a.dy + row + h, o);
+          if (a.dy) store_n<N>((TD *)a.dy + row + h, o);
         }
       }
     }
@@ -258,40 +260,46 @@ constexpr int kMaxBlocks = 512;
 // Workgroups of a backward pass.  Up to four rows one takes them all: a row takes about 1.5 us, a second launch 4.5.
 int blocks(int T) { return T <= 4 ? (T > 0 ? 1 : 0) : (T < kMaxBlocks ? T : kMaxBlocks); }
 
-template <typename TX, typename TY, int W, int NV, int N>
-hipError_t launch(const NormArgs &a, bool backward, hipStream_t s) {
-  if (!backward) {  // T >= 1
+// TD: type of dy, void for the forward pass.
+template <typename TX, typename TY, typename TD, int W, int NV, int N>
+hipError_t launch(const NormArgs &a, hipStream_t s) {
+  if constexpr (std::is_void_v<TD>) {  // T >= 1
     hipLaunchKernelGGL((block_norm_kernel<TX, TY, W, NV, N>), dim3(a.T), dim3(W * 64), 0, s, a);
     return hipGetLastError();
+  } else {
+    const int G = blocks(a.T);
+    if (G > 0) hipLaunchKernelGGL((block_norm_backward_kernel<TX, TY, TD, W, NV, N>), dim3(G), dim3(W * 64), 0, s, a);
+    hipError_t err = hipGetLastError();
+    float *gate = a.gate_kind == train::kGateChannel ? a.d_gate : nullptr;
+    if (err != hipSuccess || G == 1 || (!a.dw_next && !a.dw_post && !gate)) return err;
+    hipLaunchKernelGGL(column_sum_kernel, dim3(ceil_div_i(a.H, 64), 3), dim3(kSumWaves * 64), 0, s, (const float *)a.ws, G, a.H,
+                       a.dw_next, a.dw_post, gate);
+    return hipGetLastError();
   }
-  const int G = blocks(a.T);
-  if (G > 0) hipLaunchKernelGGL((block_norm_backward_kernel<TX, TY, W, NV, N>), dim3(G), dim3(W * 64), 0, s, a);
-  hipError_t err = hipGetLastError();
-  float *gate = a.gate_kind == train::kGateChannel ? a.d_gate : nullptr;
-  if (err != hipSuccess || G == 1 || (!a.dw_next && !a.dw_post && !gate)) return err;
-  hipLaunchKernelGGL(column_sum_kernel, dim3(ceil_div_i(a.H, 64), 3), dim3(kSumWaves * 64), 0, s, (const float *)a.ws, G, a.H,
-                     a.dw_next, a.dw_post, gate);
-  return hipGetLastError();
 }
 
-template <typename TX, typename TY>
-hipError_t pick(const NormArgs &a, bool backward, hipStream_t s) {
+template <typename TX, typename TY, typename TD>
+hipError_t pick(const NormArgs &a, hipStream_t s) {
   const int H = a.H;
   if (H % 8 == 0) {
-    if (H <= 512) return launch<TX, TY, 1, 1, 8>(a, backward, s);
-    if (H <= 2048) return launch<TX, TY, 4, 1, 8>(a, backward, s);
-    if (H <= 4096) return launch<TX, TY, 4, 2, 8>(a, backward, s);
-    if (H <= 8192) return launch<TX, TY, 8, 2, 8>(a, backward, s);
-    return launch<TX, TY, 16, 2, 8>(a, backward, s);
+    if (H <= 512) return launch<TX, TY, TD, 1, 1, 8>(a, s);
+    if (H <= 2048) return launch<TX, TY, TD, 4, 1, 8>(a, s);
+    if (H <= 4096) return launch<TX, TY, TD, 4, 2, 8>(a, s);
+    if (H <= 8192) return launch<TX, TY, TD, 8, 2, 8>(a, s);
+    return launch<TX, TY, TD, 16, 2, 8>(a, s);
   }
-  if (H <= 256) return launch<TX, TY, 1, 4, 1>(a, backward, s);
-  if (H <= 2048) return launch<TX, TY, 4, 8, 1>(a, backward, s);
-  return launch<TX, TY, 16, 16, 1>(a, backward, s);
+  if (H <= 256) return launch<TX, TY, TD, 1, 4, 1>(a, s);
+  if (H <= 2048) return launch<TX, TY, TD, 4, 8, 1>(a, s);
+  return launch<TX, TY, TD, 16, 16, 1>(a, s);
 }
 
-hipError_t by_type(const NormArgs &a, bool backward, hipStream_t s) {
-  if (a.x_bf16) return a.y_bf16 ? pick<uint16_t, uint16_t>(a, backward, s) : pick<uint16_t, float>(a, backward, s);
-  return a.y_bf16 ? pick<float, uint16_t>(a, backward, s) : pick<float, float>(a, backward, s);
+template <typename TX>
+hipError_t forward(const NormArgs &a, hipStream_t s) {
+  return a.y_bf16 ? pick<TX, uint16_t, void>(a, s) : pick<TX, float, void>(a, s);
+}
+template <typename TX, typename TY>
+hipError_t backward(const NormArgs &a, hipStream_t s) {
+  return a.dy_bf16 ? pick<TX, TY, uint16_t>(a, s) : pick<TX, TY, float>(a, s);
 }
 
 }  // namespace
@@ -300,5 +308,10 @@ size_t train::norm_grad_ws_bytes(int T, int H) {
   const int G = blocks(T);
   return G <= 1 ? 0 : align_up((size_t)G * 3 * H * sizeof(float), 256);
 }
-hipError_t train::launch_block_norm(const NormArgs &a, hipStream_t s) { return by_type(a, false, s); }
-hipError_t train::launch_block_norm_backward(const NormArgs &a, hipStream_t s) { return by_type(a, true, s); }
+hipError_t train::launch_block_norm(const NormArgs &a, hipStream_t s) {
+  return a.x_bf16 ? forward<uint16_t>(a, s) : forward<float>(a, s);
+}
+hipError_t train::launch_block_norm_backward(const NormArgs &a, hipStream_t s) {
+  if (a.x_bf16) return a.y_bf16 ? backward<uint16_t, uint16_t>(a, s) : backward<uint16_t, float>(a, s);
+  return a.y_bf16 ? backward<float, uint16_t>(a, s) : backward<float, float>(a, s);
+}

@@ -68,7 +68,7 @@ hipError_t launch_route_grad(const RouteGradArgs &a, hipStream_t s);
 enum { kGateNone = 0, kGateChannel = 1, kGateToken = 2 };
 struct NormArgs {
   const void *x, *y;          // x: the residual (forward) or the sum that it gave (backward)
-  int x_bf16, y_bf16;
+  int x_bf16, y_bf16, dy_bf16;
   const void *w_next, *w_post, *gate;
   int w_bf16, gate_kind;
   float scale, eps;

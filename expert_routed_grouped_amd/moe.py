@@ -137,7 +137,7 @@ def lib():
         L.moe_block_norm_backward_workspace_size.restype = Z
         L.moe_block_norm_backward_workspace_size.argtypes = [I, I]
         L.moe_block_norm_backward.restype = I
-        L.moe_block_norm_backward.argtypes = [P, I, P, I, P, P, P, I, I, F, P, P, P, P, I, I, P, P, P, P, P, P, Z, P]
+        L.moe_block_norm_backward.argtypes = [P, I, P, I, P, P, P, I, I, F, P, P, P, P, I, I, P, P, I, P, P, P, P, Z, P]
         _lib = L
     return _lib
 
@@ -874,31 +874,33 @@ def moe_block_norm_backward(x_out: torch.Tensor, w_next: Optional[torch.Tensor] 
                             dx_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                             w_post: Optional[torch.Tensor] = None, rstd_post: Optional[torch.Tensor] = None,
                             gate: Optional[torch.Tensor] = None, scale: float = 1.0, dx: Optional[torch.Tensor] = None,
-                            dy: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                            stream=None) -> dict:
+                            dy: Optional[torch.Tensor] = None, dy_dtype=None,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Gradient of moe_block_norm -> dict(dx, dy, dw_next, dw_post, dgate), None for what the call had not.
 
     ``x_out`` is the sum that the forward call gave (without ``y``: x), ``rstd_next`` and ``rstd_post`` its reciprocal
     roots; ``dn`` and ``dx_out`` the gradients of its results, either may be missing.  dw_next, dw_post and dgate are
-    fp32.  ``dx`` may be ``dx_out`` or ``dn`` itself."""
+    fp32, dy is of ``dy_dtype`` (default: y's).  ``dx`` may be ``dx_out`` or ``dn`` itself."""
     T, H = x_out.shape
     dev, f32 = x_out.device, torch.float32
     if dx is None:
         dx = _new((T, H), x_out.dtype, dev, stream)
     if y is not None and dy is None:
-        dy = _new((T, H), y.dtype, dev, stream)
+        _out_dtype(y.dtype if dy_dtype is None else dy_dtype)
+        dy = _new((T, H), y.dtype if dy_dtype is None else dy_dtype, dev, stream)
     dwn = _new((H,), f32, dev, stream) if w_next is not None else None
     dwp = _new((H,), f32, dev, stream) if w_post is not None else None
     dg = _new(gate.shape, f32, dev, stream) if gate is not None else None
     ws, nws, workspace = _space(workspace, int(lib().moe_block_norm_backward_workspace_size(T, H)), dev, stream)
     wdt, kind, wn, wp, g = _norm_weights(T, H, dev, w_next, w_post, gate)
     xdt, all_ = x_out.dtype, (T, H)
-    yp, dyp, ydt = None, None, MOE_F32
+    yp, dyp, ydt, dydt = None, None, MOE_F32, MOE_F32
     if y is not None:
-        yp, dyp, ydt = _arg(y, "y", y.dtype, all_, dev), _arg(dy, "dy", y.dtype, all_, dev), _out_dtype(y.dtype)
+        yp, dyp, ydt, dydt = (_arg(y, "y", y.dtype, all_, dev), _arg(dy, "dy", dy.dtype, all_, dev), _out_dtype(y.dtype),
+                              _out_dtype(dy.dtype))
     args = (_arg(x_out, "x_out", xdt, all_, dev), _out_dtype(xdt), yp, ydt, wn, wp, g, wdt, kind, scale,
             _arg(rstd_next, "rstd_next", f32, (T,), dev), _arg(rstd_post, "rstd_post", f32, (T,), dev),
-            _arg(dx_out, "dx_out", xdt, all_, dev), _arg(dn, "dn", xdt, all_, dev), T, H, _arg(dx, "dx", xdt, all_, dev), dyp,
+            _arg(dx_out, "dx_out", xdt, all_, dev), _arg(dn, "dn", xdt, all_, dev), T, H, _arg(dx, "dx", xdt, all_, dev), dyp, dydt,
             None if dwn is None else dwn.data_ptr(), None if dwp is None else dwp.data_ptr(),
             None if dg is None else dg.data_ptr(), ws, nws)
     with _On(dev) as on:

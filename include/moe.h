@@ -762,7 +762,7 @@ size_t moe_block_norm_backward_workspace_size(int T, int H);
  *   du      = gate * D,  dv = du * w_post,  dy = rstd_post * (dv - yh * mean(dv yh))   (w_post NULL: dy = du)
  *   dw_next = sum over t of dn xh,  dw_post = sum over t of du yh                fp32 [H]
  *   d_gate  = sum over t ([H]) or over the row ([T]) of D u                      fp32
- * dx of type x_dtype, dy of type y_dtype.  Outputs that are NULL are not computed.  dx may be dx_out or dn itself.
+ * dx of type x_dtype, dy of type dy_dtype (MOE_BF16 or MOE_F32).  Outputs that are NULL are not computed.  dx may be dx_out or dn itself.
  * dx_out and dn are of type x_dtype; not both NULL.  workspace (for dw_next, dw_post and a channel gate): at least
  * moe_block_norm_backward_workspace_size(T, H) bytes, 256-byte aligned, contents free.  The sums over t have an order
  * that T alone fixes.  T == 0 writes zeros to dw_next, dw_post and a channel gate's gradient.
@@ -770,7 +770,7 @@ size_t moe_block_norm_backward_workspace_size(int T, int H);
 int moe_block_norm_backward(const void *x_out, int x_dtype, const void *y, int y_dtype, const void *w_next,
                             const void *w_post, const void *gate, int w_dtype, int gate_kind, float scale,
                             const float *rstd_next, const float *rstd_post, const void *dx_out, const void *dn, int T, int H,
-                            void *dx, void *dy, float *dw_next, float *dw_post, float *d_gate, void *workspace,
+                            void *dx, void *dy, int dy_dtype, float *dw_next, float *dw_post, float *d_gate, void *workspace,
                             size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus

@@ -134,14 +134,14 @@ def test_block_norm(kw, code):
     assert norm(**kw) == code
 
 
-norm_back = call("moe_block_norm_backward", "xo xd y yd wn wp g wd gk sc rn rp dxo dn T H dx dy dwn dwp dg ws nws".split(),
-                 dict(xo=A, xd=1, y=B, yd=0, wn=C, wp=D, g=E_, wd=0, gk=1, sc=1.0, rn=F, rp=G, dxo=H_, dn=I_, T=8, H=64, dx=J, dy=K_,
+norm_back = call("moe_block_norm_backward", "xo xd y yd wn wp g wd gk sc rn rp dxo dn T H dx dy dyd dwn dwp dg ws nws".split(),
+                 dict(xo=A, xd=1, y=B, yd=0, wn=C, wp=D, g=E_, wd=0, gk=1, sc=1.0, rn=F, rp=G, dxo=H_, dn=I_, T=8, H=64, dx=J, dy=K_, dyd=0,
                       dwn=L_, dwp=M_, dg=N_, ws=O_, nws=1 << 20))
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), -2), (dict(H=0), -2), (dict(H=16385), -2), (dict(gk=3), -2), (dict(gk=0), -2), (dict(g=None, dg=None), -2), (dict(y=None), -2),
-    (dict(wn=None), -2), (dict(wp=None), -2), (dict(xd=2), -3), (dict(yd=5), -3), (dict(wd=2), -3), (dict(dn=None, dxo=None), -1),
+    (dict(wn=None), -2), (dict(wp=None), -2), (dict(xd=2), -3), (dict(yd=5), -3), (dict(dyd=2), -3), (dict(wd=2), -3), (dict(dn=None, dxo=None), -1),
     (dict(xo=None), -1), (dict(rn=None), -1), (dict(rp=None), -1), (dict(wn=None, dwn=None), -1), (dict(dx=None, dy=None, dwn=None, dwp=None, dg=None), -1),
     (dict(ws=None), -4), (dict(nws=16), -4), (dict(xo=off(A, 8)), -6), (dict(dx=off(J, 8)), -6), (dict(dwn=off(L_, 4)), -6), (dict(ws=off(O_, 16)), -6),
     (dict(dx=A), -2), (dict(dx=off(H_, 16)), -2), (dict(dy=B), -2), (dict(dy=J), -2), (dict(dwn=C), -2), (dict(dwp=L_), -2), (dict(ws=J), -2),

@@ -399,6 +399,9 @@ def test_block_norm_backward(T, H, has_y, post, gate_kind, types):
     else:
         assert got["dgate"] is None
     again = moe.moe_block_norm_backward(s, wn, rn, dn, dx_out=ds, y=y, w_post=wp, rstd_post=rp, gate=gate, scale=scale)
+    other = moe.moe_block_norm_backward(s, wn, rn, dn, dx_out=ds, y=y, w_post=wp, rstd_post=rp, gate=gate, scale=scale,
+                                        dy_dtype=BF if yt == F32 else F32)["dy"]
+    assert other.dtype != yt and torch.equal(other.to(BF), got["dy"].to(BF))
     for name in got:
         assert (got[name] is None) == (again[name] is None)
         assert got[name] is None or torch.equal(got[name], again[name])
