@@ -127,22 +127,82 @@ __global__ __launch_bounds__(W * 64) void block_norm_kernel(NormArgs a) {
   }
 }
 
-// Partial column sums of one workgroup: dw_next, dw_post and a channel gate's, [3][H] each.
+// N values as they lie in memory, loaded now and looked at later.
+template <typename T, int N>
+struct Raw {
+  static constexpr int Q = N == 1 ? 1 : N * (int)sizeof(T) / 16;
+  std::conditional_t<N == 1, T, u32x4_t> v[Q];
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (N == 1) v[0] = *p;
+    else {
+#pragma unroll
+      for (int i = 0; i < Q; i++) v[i] = ((const u32x4_t *)p)[i];
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+    if constexpr (N == 1) f[0] = train::to_f32(v[0]);
+    else {
+#pragma unroll
+      for (int i = 0; i < Q; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          if constexpr (sizeof(T) == 4) f[4 * i + j] = __uint_as_float(v[i][j]);
+          else f[8 * i + 2 * j] = bf16_lo(v[i][j]), f[8 * i + 2 * j + 1] = bf16_hi(v[i][j]);
+        }
+    }
+  }
+};
+
+// Partial column sums of one workgroup: dw_next, dw_post and a channel gate's, [3][H] each.  The next row's values are on
+// their way while a row is summed, and the weights stay in registers (6000 x 4096, bf16 and an fp32 y: 99 us without, 85), where a
+// thread has one piece of a row; with more there are not enough registers for it.
 template <typename TX, typename TY, typename TD, int W, int NV, int N>
 __global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(NormArgs a) {
   __shared__ float buf[2 * 3 * W];
   const int H = a.H, tid = threadIdx.x;
   const bool channel = a.gate_kind == train::kGateChannel;
-  float dwn[NV][N], dwp[NV][N], dgc[NV][N];
+  constexpr bool HOLD = NV * N <= 8;
+  float dwn[NV][N], dwp[NV][N], dgc[NV][N], wn[HOLD ? NV : 1][N], wp[HOLD ? NV : 1][N], gc[HOLD ? NV : 1][N];
+  auto weights = [&](int v, int h) __attribute__((always_inline)) {  // of piece v, into its place (or the one there is)
+    const int at = HOLD ? v : 0;
 #pragma unroll
-  for (int v = 0; v < NV; v++)
+    for (int i = 0; i < N; i++) wn[at][i] = wp[at][i] = gc[at][i] = 1.0f;
+    if (h < H) {
+      if (a.dn) load_w<N>(a.w_next, a.w_bf16, h, wn[at]);
+      if (a.w_post) load_w<N>(a.w_post, a.w_bf16, h, wp[at]);
+      if (channel) load_w<N>(a.gate, a.w_bf16, h, gc[at]);
+    }
+  };
+#pragma unroll
+  for (int v = 0; v < NV; v++) {
+    if constexpr (HOLD) weights(v, (v * W * 64 + tid) * N);
 #pragma unroll
     for (int i = 0; i < N; i++) dwn[v][i] = 0.0f, dwp[v][i] = 0.0f, dgc[v][i] = 0.0f;
-  int half = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, half ^= 1) {
+  }
+  Raw<TX, N> rx[NV], rdn[NV], rds[NV];
+  Raw<TY, N> ry[NV];
+  float rn = 0.0f, rp = 1.0f, gt = 1.0f;
+  auto fetch = [&](int t) __attribute__((always_inline)) {
     const size_t row = (size_t)t * H;
-    const float rn = a.dn ? a.rn[t] : 0.0f, rp = a.w_post ? a.rp[t] : 1.0f;
-    const float gt = a.gate_kind == train::kGateToken ? one_w(a.gate, a.w_bf16, t) : 1.0f;
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+      const int h = (v * W * 64 + tid) * N;
+      if (h < H) {
+        if (a.dx_out) rds[v].load((const TX *)a.dx_out + row + h);
+        if (a.dn) rx[v].load((const TX *)a.x + row + h), rdn[v].load((const TX *)a.dn + row + h);
+        if (a.y) ry[v].load((const TY *)a.y + row + h);
+      }
+    }
+    if (a.dn) rn = a.rn[t];
+    if (a.w_post) rp = a.rp[t];
+    if (a.gate_kind == train::kGateToken) gt = one_w(a.gate, a.w_bf16, t);
+  };
+  int half = 0;
+  if (HOLD && (int)blockIdx.x < a.T) fetch(blockIdx.x);
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, half ^= 1) {
+    if constexpr (!HOLD) fetch(t);
+    const size_t row = (size_t)t * H;
+    const float rnt = rn, rpt = rp, gtt = gt;
     float xh[NV][N], yh[NV][N], b[NV][N];  // b = dx' + r dn w_next
     float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -151,50 +211,45 @@ __global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(NormArgs a)
 #pragma unroll
       for (int i = 0; i < N; i++) xh[v][i] = 0.0f, yh[v][i] = 0.0f, b[v][i] = 0.0f;
       if (h < H) {
-        if (a.dx_out) load_n<N>((const TX *)a.dx_out + row + h, b[v]);
+        const int at = HOLD ? v : 0;
+        if constexpr (!HOLD) weights(v, h);
+        if (a.dx_out) rds[v].get(b[v]);
         if (a.dn) {
-          float dn[N], w[N];
-          load_n<N>((const TX *)a.x + row + h, xh[v]);
-          load_n<N>((const TX *)a.dn + row + h, dn);
-          load_w<N>(a.w_next, a.w_bf16, h, w);
+          float dn[N];
+          rx[v].get(xh[v]);
+          rdn[v].get(dn);
 #pragma unroll
           for (int i = 0; i < N; i++) {
-            xh[v][i] *= rn;
+            xh[v][i] *= rnt;
             dwn[v][i] = fmaf(dn[i], xh[v][i], dwn[v][i]);
-            dn[i] *= w[i];
+            dn[i] *= wn[at][i];
             s[0] = fmaf(dn[i], xh[v][i], s[0]);
-            b[v][i] = fmaf(rn, dn[i], b[v][i]);
+            b[v][i] = fmaf(rnt, dn[i], b[v][i]);
           }
         }
         if (a.y) {
-          load_n<N>((const TY *)a.y + row + h, yh[v]);
-          float f[N], w[N];
-#pragma unroll
-          for (int i = 0; i < N; i++) f[i] = 1.0f;
-          if (a.w_post) load_w<N>(a.w_post, a.w_bf16, h, f);
-          if (channel) {
-            load_w<N>(a.gate, a.w_bf16, h, w);
-#pragma unroll
-            for (int i = 0; i < N; i++) f[i] *= w[i];
-          }
+          ry[v].get(yh[v]);
 #pragma unroll
           for (int i = 0; i < N; i++) {
-            yh[v][i] *= rp;
-            const float q = f[i] * yh[v][i];
+            yh[v][i] *= rpt;
+            const float q = gc[at][i] * wp[at][i] * yh[v][i];
             s[1] = fmaf(q, b[v][i], s[1]);
             s[2] = fmaf(q, xh[v][i], s[2]);
           }
         }
       }
     }
+    if (HOLD && t + (int)gridDim.x < a.T) fetch(t + gridDim.x);  // this workgroup's own row: nothing that it writes here is read there
     block_sum<3, W>(s, buf, half);
-    const float c = rn * s[0] / (float)H;           // D = b - xh c
-    const float dot = s[1] - c * s[2], q = gt * dot / (float)H;  // sum of D u; mean of dv yh
+    const float c = rnt * s[0] / (float)H;           // D = b - xh c
+    const float dot = s[1] - c * s[2], q = gtt * dot / (float)H;  // sum of D u; mean of dv yh
     if (a.d_gate && !channel && tid == 0) a.d_gate[t] = dot;
 #pragma unroll
     for (int v = 0; v < NV; v++) {
       const int h = (v * W * 64 + tid) * N;
       if (h < H) {
+        const int at = HOLD ? v : 0;
+        if constexpr (!HOLD) weights(v, h);
         float D[N], o[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
@@ -203,17 +258,12 @@ __global__ __launch_bounds__(W * 64) void block_norm_backward_kernel(NormArgs a)
         }
         if (a.dx) store_n<N>((TX *)a.dx + row + h, o);
         if (a.y) {
-          float g[N], w[N];
-#pragma unroll
-          for (int i = 0; i < N; i++) g[i] = gt, w[i] = 1.0f;
-          if (channel) load_w<N>(a.gate, a.w_bf16, h, g);
-          if (a.w_post) load_w<N>(a.w_post, a.w_bf16, h, w);
 #pragma unroll
           for (int i = 0; i < N; i++) {
-            const float du = g[i] * D[i], u = yh[v][i] * w[i];
+            const float du = gtt * gc[at][i] * D[i], u = yh[v][i] * wp[at][i];
             if (channel) dgc[v][i] = fmaf(D[i], u, dgc[v][i]);
             dwp[v][i] = fmaf(du, yh[v][i], dwp[v][i]);
-            o[i] = a.w_post ? rp * (du * w[i] - yh[v][i] * q) : du;
+            o[i] = a.w_post ? rpt * (du * wp[at][i] - yh[v][i] * q) : du;
           }
           if (a.dy) store_n<N>((TD *)a.dy + row + h, o);
         }
@@ -256,9 +306,12 @@ __global__ __launch_bounds__(kSumWaves * 64) void column_sum_kernel(const float 
   }
 }
 
-constexpr int kMaxBlocks = 512;
-// Workgroups of a backward pass.  Up to four rows one takes them all: a row takes about 1.5 us, a second launch 4.5.
-int blocks(int T) { return T <= 4 ? (T > 0 ? 1 : 0) : (T < kMaxBlocks ? T : kMaxBlocks); }
+// Workgroups of a backward pass: one to a compute unit (6000 x 4096: 80 us, 85 with two, 90 with three), two of short rows.  Up to
+// four rows one workgroup takes them all: a row takes about 1.5 us, a second launch 4.5.
+int blocks(int T, int H) {
+  const int most = H > 512 ? 256 : 512;
+  return T <= 4 ? (T > 0 ? 1 : 0) : (T < most ? T : most);
+}
 
 // TD: type of dy, void for the forward pass.
 template <typename TX, typename TY, typename TD, int W, int NV, int N>
@@ -267,7 +320,7 @@ hipError_t launch(const NormArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((block_norm_kernel<TX, TY, W, NV, N>), dim3(a.T), dim3(W * 64), 0, s, a);
     return hipGetLastError();
   } else {
-    const int G = blocks(a.T);
+    const int G = blocks(a.T, a.H);
     if (G > 0) hipLaunchKernelGGL((block_norm_backward_kernel<TX, TY, TD, W, NV, N>), dim3(G), dim3(W * 64), 0, s, a);
     hipError_t err = hipGetLastError();
     float *gate = a.gate_kind == train::kGateChannel ? a.d_gate : nullptr;
@@ -284,12 +337,14 @@ hipError_t pick(const NormArgs &a, hipStream_t s) {
   if (H % 8 == 0) {
     if (H <= 512) return launch<TX, TY, TD, 1, 1, 8>(a, s);
     if (H <= 2048) return launch<TX, TY, TD, 4, 1, 8>(a, s);
-    if (H <= 4096) return launch<TX, TY, TD, 4, 2, 8>(a, s);
-    if (H <= 8192) return launch<TX, TY, TD, 8, 2, 8>(a, s);
+    if (H <= 4096) return launch<TX, TY, TD, 8, 1, 8>(a, s);
+    if (H <= 8192) return launch<TX, TY, TD, 16, 1, 8>(a, s);
     return launch<TX, TY, TD, 16, 2, 8>(a, s);
   }
   if (H <= 256) return launch<TX, TY, TD, 1, 4, 1>(a, s);
   if (H <= 2048) return launch<TX, TY, TD, 4, 8, 1>(a, s);
+  if (H <= 4096) return launch<TX, TY, TD, 16, 4, 1>(a, s);
+  if (H <= 8192) return launch<TX, TY, TD, 16, 8, 1>(a, s);
   return launch<TX, TY, TD, 16, 16, 1>(a, s);
 }
 
@@ -305,7 +360,7 @@ hipError_t backward(const NormArgs &a, hipStream_t s) {
 }  // namespace
 
 size_t train::norm_grad_ws_bytes(int T, int H) {
-  const int G = blocks(T);
+  const int G = blocks(T, H);
   return G <= 1 ? 0 : align_up((size_t)G * 3 * H * sizeof(float), 256);
 }
 hipError_t train::launch_block_norm(const NormArgs &a, hipStream_t s) {

@@ -42,24 +42,37 @@ struct Operand {
   int col0, cols;       // mn-major: first output column of the tile and columns of the matrix
   int K;                // k-major: length of the contraction
   u32x4_t reg[NP];
+  const T *src[MN ? 1 : NP];  // k-major: the rows of this thread's pieces, NULL past the last
 
   __device__ __forceinline__ const T *row(int r) const {
     if (index) r = min(max(index[r], 0), limit - 1);
     return base + (size_t)r * ld;
   }
-  // Piece p of a thread: element i of its row, or zero.
+  // The piece at p, of which the row has ``have`` elements.  Rows that are no whole pieces are loaded as whole ones too, at any
+  // alignment (global memory allows it), their last piece element by element.
   template <bool VEC>
   __device__ __forceinline__ u32x4_t piece(const T *p, int have) const {
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if constexpr (VEC) {
-      if (have > 0) v = *(const u32x4_t *)p;
-    } else {
-      T e[V];
+    if constexpr (VEC) return *(const u32x4_t *)p;
+    else {
+      u32x4_t v;
+      if (have >= V) __builtin_memcpy(&v, p, 16);
+      else {
+        T e[V];
 #pragma unroll
-      for (int i = 0; i < V; i++) e[i] = i < have ? p[i] : T(0);
-      v = __builtin_bit_cast(u32x4_t, e);
+        for (int i = 0; i < V; i++) e[i] = i < have ? p[i] : T(0);
+        v = __builtin_bit_cast(u32x4_t, e);
+      }
+      return v;
     }
-    return v;
+  }
+  __device__ __forceinline__ void start(int tid) {
+    if constexpr (!MN) {
+#pragma unroll
+      for (int u = 0; u < NP; u++) {
+        const int r = (tid + u * NTHR) / (KB / 16);
+        src[u] = r < rows ? row(row0 + r) : nullptr;
+      }
+    }
   }
   template <bool VEC>
   __device__ __forceinline__ void fetch(int k0, int tid) {
@@ -67,9 +80,9 @@ struct Operand {
     for (int u = 0; u < NP; u++) {
       const int c = tid + u * NTHR;
       if constexpr (!MN) {
-        const int r = c / (KB / 16), k = k0 + c % (KB / 16) * V;
-        const int have = r < rows ? K - k : 0;
-        reg[u] = have > 0 ? piece<VEC>(row(row0 + r) + k, have) : u32x4_t{0u, 0u, 0u, 0u};
+        const int k = k0 + c % (KB / 16) * V;
+        const int have = src[u] ? K - k : 0;
+        reg[u] = have > 0 ? piece<VEC>(src[u] + k, have) : u32x4_t{0u, 0u, 0u, 0u};
       } else {
         constexpr int PR = R / V;  // pieces of a k row
         const int r = k0 + c / PR, n = col0 + c % PR * V;
@@ -139,6 +152,8 @@ __device__ __forceinline__ void tile(Operand<T, AMN, BM> &A, Operand<T, BMN, BN>
     for (int j = 0; j < NB; j++)
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
+  A.start(tid);
+  B.start(tid);
   A.template fetch<VA>(0, tid);
   B.template fetch<VB>(0, tid);
   char *cur = lds, *nxt = lds + BUF;
@@ -182,11 +197,15 @@ __device__ __forceinline__ void each(const f32x16_t (&acc)[MB][NB], int m0, int 
 }
 
 template <int BM>
-struct Waves {  // BM = 128: 2 x 2 waves of 64 x 64 outputs; BM = 32: 1 x 4 of 32 x 32
-  static constexpr int MB = BM == 128 ? 2 : 1, NB = BM == 128 ? 2 : 1;
-  static __device__ __forceinline__ int m0(int w) { return BM == 128 ? (w >> 1) * 64 : 0; }
-  static __device__ __forceinline__ int n0(int w) { return BM == 128 ? (w & 1) * 64 : w * 32; }
+struct Waves {  // BM = 128: 2 x 2 waves of 64 x 64 outputs; 64: 2 x 2 of 32 x 64; 32: 1 x 4 of 32 x 32
+  static constexpr int MB = BM == 128 ? 2 : 1, NB = BM >= 64 ? 2 : 1;
+  static __device__ __forceinline__ int m0(int w) { return BM >= 64 ? (w >> 1) * (BM / 2) : 0; }
+  static __device__ __forceinline__ int n0(int w) { return BM >= 64 ? (w & 1) * 64 : w * 32; }
 };
+
+// Rows of a tile: fp32 products are slow enough that small tiles cost nothing, and they fill the chip more evenly.
+template <typename T>
+constexpr int kRows = sizeof(T) == 4 ? 64 : 128;
 
 template <typename T, typename TO, bool KN, int BM, bool VA, bool VB>
 __global__ __launch_bounds__(NTHR) void mm_kernel(train::MmArgs p) {
@@ -233,7 +252,7 @@ __global__ __launch_bounds__(NTHR) void mm_kernel(train::MmArgs p) {
 
 template <typename T, typename TO, bool VA, bool VB>
 __global__ __launch_bounds__(NTHR) void wgrad_kernel(train::WgradArgs p) {
-  constexpr int BM = 128;
+  constexpr int BM = kRows<T>;
   using OA = Operand<T, true, BM>;
   using OB = Operand<T, true, BN>;
   using Wv = Waves<BM>;
@@ -290,14 +309,14 @@ hipError_t launch_mm(const train::MmArgs &a, hipStream_t s) {
 template <typename T, typename TO>
 hipError_t pick_mm(const train::MmArgs &a, hipStream_t s) {
   const bool few = (long long)a.R_cap <= 32LL * a.El;
-  if (a.kn) return few ? launch_mm<T, TO, true, 32>(a, s) : launch_mm<T, TO, true, 128>(a, s);
-  return few ? launch_mm<T, TO, false, 32>(a, s) : launch_mm<T, TO, false, 128>(a, s);
+  if (a.kn) return few ? launch_mm<T, TO, true, 32>(a, s) : launch_mm<T, TO, true, kRows<T>>(a, s);
+  return few ? launch_mm<T, TO, false, 32>(a, s) : launch_mm<T, TO, false, kRows<T>>(a, s);
 }
 
 template <typename T, typename TO>
 hipError_t launch_wgrad(const train::WgradArgs &a, hipStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const dim3 grid((unsigned)((long long)a.El * ceil_div_i(a.M, 128) * ceil_div_i(a.N, BN)));
+  const dim3 grid((unsigned)((long long)a.El * ceil_div_i(a.M, kRows<T>) * ceil_div_i(a.N, BN)));
   const bool va = a.M % V == 0, vb = a.N % V == 0;
   if (va && vb) hipLaunchKernelGGL((wgrad_kernel<T, TO, true, true>), grid, dim3(NTHR), 0, s, a);
   else if (va) hipLaunchKernelGGL((wgrad_kernel<T, TO, true, false>), grid, dim3(NTHR), 0, s, a);
