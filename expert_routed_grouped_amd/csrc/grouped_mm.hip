@@ -258,8 +258,10 @@ __global__ __launch_bounds__(NTHR) void wgrad_kernel(train::WgradArgs p) {
   using Wv = Waves<BM>;
   __shared__ __attribute__((aligned(16))) char lds[2 * (OA::BYTES + OB::BYTES)];
   const int MT = (p.M + BM - 1) / BM, NT = (p.N + BN - 1) / BN;
-  const int e = blockIdx.x / (MT * NT), mt = blockIdx.x / NT % MT, nt = blockIdx.x % NT;
-  const int r0 = max(p.offsets[e], 0), rows = max(min(p.offsets[e + 1], p.R_cap) - r0, 0);
+  const int s = blockIdx.x / (MT * NT * p.El), b = blockIdx.x % (MT * NT * p.El);
+  const int e = b / (MT * NT), mt = b / NT % MT, nt = b % NT;
+  int r0 = max(p.offsets[e], 0), rows = max(min(p.offsets[e + 1], p.R_cap) - r0, 0);
+  if (p.splits > 1) train::part_of(s, p.splits, r0, rows);
   OA A{};
   A.base = (const T *)p.a;
   A.index = p.a_index;
@@ -281,7 +283,7 @@ __global__ __launch_bounds__(NTHR) void wgrad_kernel(train::WgradArgs p) {
   const int wave = threadIdx.x >> 6, m0 = Wv::m0(wave), n0 = Wv::n0(wave);
   f32x16_t acc[Wv::MB][Wv::NB];
   tile<T, true, true, BM, VA, VB>(A, B, rows, m0, n0, acc, lds);
-  TO *out = (TO *)p.dw + ((size_t)e * p.M + mt * BM) * p.N + nt * BN;
+  TO *out = (TO *)p.dw + (((size_t)s * p.El + e) * p.M + mt * BM) * p.N + nt * BN;
   const int ms = p.M - mt * BM, ns = p.N - nt * BN;
   const bool add = p.add;
   each(acc, m0, n0, [&](int m, int n, float v) {
@@ -290,6 +292,17 @@ __global__ __launch_bounds__(NTHR) void wgrad_kernel(train::WgradArgs p) {
       train::put(o, add ? train::to_f32(*o) + v : v);
     }
   });
+}
+
+// Sums of the parts, in their order.
+template <typename TO>
+__global__ __launch_bounds__(256) void join_kernel(const float *ws, int splits, long long n, int add, TO *dw) {
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+    float v = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < splits; s++) v += ws[s * n + i];
+    train::put(dw + i, add ? train::to_f32(dw[i]) + v : v);
+  }
 }
 
 template <typename T, typename TO, bool KN, int BM>
@@ -316,7 +329,7 @@ hipError_t pick_mm(const train::MmArgs &a, hipStream_t s) {
 template <typename T, typename TO>
 hipError_t launch_wgrad(const train::WgradArgs &a, hipStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const dim3 grid((unsigned)((long long)a.El * ceil_div_i(a.M, kRows<T>) * ceil_div_i(a.N, BN)));
+  const dim3 grid((unsigned)((long long)a.splits * a.El * ceil_div_i(a.M, kRows<T>) * ceil_div_i(a.N, BN)));
   const bool va = a.M % V == 0, vb = a.N % V == 0;
   if (va && vb) hipLaunchKernelGGL((wgrad_kernel<T, TO, true, true>), grid, dim3(NTHR), 0, s, a);
   else if (va) hipLaunchKernelGGL((wgrad_kernel<T, TO, true, false>), grid, dim3(NTHR), 0, s, a);
@@ -328,15 +341,53 @@ hipError_t launch_wgrad(const train::WgradArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t train::launch_grouped_mm(const MmArgs &a, hipStream_t s) {
-  if (mm_dma_fits(a)) return launch_mm_dma(a, s);
+  if (mm_dma_fits(a)) {
+    // Tiles for few rows an expert on average.  128 experts of 1536 x 4096, top 8, us with those and with the large tiles: 64
+    // tokens 231 and 245, 256 247 and 268, 384 263 and 283, 512 363 and 288; transposed 8 tokens 114 and 127, 24 200 and 206, 64
+    // 243 and 234, 512 376 and 259.
+    bool few = a.R_cap <= (a.kn ? 2LL : 24LL) * a.El;
+    // And where the large tiles would leave most of the chip idle: 4 experts x 3000 rows, 64 x 2048, 14 and 44 us; the tiles of
+    // this file where those for few rows would be very many (8 x 375 rows, 1024 x 1024: 20 us, 28 with those, 26 large).
+    const long long large = (long long)a.El * ceil_div_i(ceil_div_i(a.R_cap, a.El), 256) * ceil_div_i(a.N, 256);
+    const long long small = (a.R_cap / 32 + (long long)a.El) * ceil_div_i(a.N, 64);
+    if (large <= 96) few = few || small <= 768;
+    if (few || large > 96) return launch_mm_dma(a, few, s);
+  }
   if (!a.bf16) return pick_mm<float, float>(a, s);
   return a.out_bf16 ? pick_mm<uint16_t, uint16_t>(a, s) : pick_mm<uint16_t, float>(a, s);
 }
 
-size_t train::wgrad_ws_bytes(int El, int R_cap, int M, int N, int bf16) { return 0; }
+// Parts of an expert's rows, each with sums of its own: where the tiles are fewer than half the compute units and an expert has
+// 512 rows or more on average, as many as fill the chip, of 256 rows or more (4 experts of 256 x 256, 3000 rows each: 65 us in
+// one part, 22 in eleven).
+static int wgrad_splits(int El, int R_cap, int M, int N) {
+  const long long tiles = (long long)El * ceil_div_i(M, 128) * ceil_div_i(N, 128), avg = R_cap / El;
+  if (tiles > 128 || avg < 512) return 1;
+  return (int)std::min({256 / tiles, avg / 256, 32LL});
+}
 
-hipError_t train::launch_grouped_wgrad(const WgradArgs &a, hipStream_t s) {
-  if (wgrad_dma_fits(a)) return launch_wgrad_dma(a, s);
-  if (!a.bf16) return a.out_bf16 ? hipErrorInvalidValue : launch_wgrad<float, float>(a, s);
+size_t train::wgrad_ws_bytes(int El, int R_cap, int M, int N, int bf16) {
+  const int splits = wgrad_splits(El, R_cap, M, N);
+  return splits > 1 ? align_up((size_t)splits * El * M * N * sizeof(float), 256) : 0;
+}
+
+static hipError_t wgrad_parts(const train::WgradArgs &a, hipStream_t s) {
+  if (train::wgrad_dma_fits(a)) return train::launch_wgrad_dma(a, s);
+  if (!a.bf16) return launch_wgrad<float, float>(a, s);
   return a.out_bf16 ? launch_wgrad<uint16_t, uint16_t>(a, s) : launch_wgrad<uint16_t, float>(a, s);
+}
+
+hipError_t train::launch_grouped_wgrad(const WgradArgs &args, hipStream_t s) {
+  WgradArgs a = args;
+  a.splits = wgrad_splits(a.El, a.R_cap, a.M, a.N);
+  if (a.splits == 1) return wgrad_parts(a, s);
+  a.dw = a.ws;
+  a.out_bf16 = a.add = 0;
+  const hipError_t err = wgrad_parts(a, s);
+  if (err != hipSuccess) return err;
+  const long long n = (long long)a.El * a.M * a.N;
+  const dim3 grid((unsigned)std::min((n + 255) / 256, 4096LL));
+  if (args.out_bf16) hipLaunchKernelGGL((join_kernel<uint16_t>), grid, dim3(256), 0, s, (const float *)a.ws, a.splits, n, args.add, (uint16_t *)args.dw);
+  else hipLaunchKernelGGL((join_kernel<float>), grid, dim3(256), 0, s, (const float *)a.ws, a.splits, n, args.add, (float *)args.dw);
+  return hipGetLastError();
 }

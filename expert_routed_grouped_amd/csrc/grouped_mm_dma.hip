@@ -565,16 +565,13 @@ hipError_t launch_few(const train::MmArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 template <bool KN, bool GATHER>
-hipError_t by_out(const train::MmArgs &a, hipStream_t s) {
-  // Few rows an expert on average.  128 experts of 1536 x 4096, top 8, us with the tiles for few rows and with the large ones: 64
-  // tokens 231 and 245, 256 247 and 268, 384 263 and 283, 512 363 and 288; transposed 8 tokens 114 and 127, 24 200 and 206, 64
-  // 243 and 234, 512 376 and 259.
-  if (a.R_cap <= (KN ? 2LL : 24LL) * a.El) return a.out_bf16 ? launch_few<KN, GATHER, uint16_t>(a, s) : launch_few<KN, GATHER, float>(a, s);
+hipError_t by_out(const train::MmArgs &a, bool few, hipStream_t s) {
+  if (few) return a.out_bf16 ? launch_few<KN, GATHER, uint16_t>(a, s) : launch_few<KN, GATHER, float>(a, s);
   return a.out_bf16 ? launch<KN, GATHER, uint16_t>(a, s) : launch<KN, GATHER, float>(a, s);
 }
 template <bool KN>
-hipError_t by_index(const train::MmArgs &a, hipStream_t s) {
-  return a.a_index ? by_out<KN, true>(a, s) : by_out<KN, false>(a, s);
+hipError_t by_index(const train::MmArgs &a, bool few, hipStream_t s) {
+  return a.a_index ? by_out<KN, true>(a, few, s) : by_out<KN, false>(a, few, s);
 }
 
 // Two workgroups of four waves on a compute unit, so that one multiplies while the other stores, took 809 us of the weight
@@ -590,7 +587,7 @@ __global__ __launch_bounds__(Wg::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
   using SrcA = std::conditional_t<GA, Gathered<C::NA, C::NW>, Source<C::NA, C::NW>>;
   using SrcB = std::conditional_t<GB, Gathered<C::NBL, C::NW>, Source<C::NBL, C::NW>>;
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS + C::NW * kOutBytes + (GA + GB) * C::NW * 512];
-  const int MT = (p.M + C::BM - 1) / C::BM, NT = (p.N + C::BN - 1) / C::BN, per = MT * NT, total = p.El * per;
+  const int MT = (p.M + C::BM - 1) / C::BM, NT = (p.N + C::BN - 1) / C::BN, per = MT * NT, total = p.El * per * p.splits;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m0 = wave / C::WN * (C::MB * 32), n0 = wave % C::WN * (C::NB * 32);
   // Workgroups go round-robin over the 8 XCDs: 32 neighbouring tiles, which share operands, run on one XCD at a time.
@@ -598,15 +595,18 @@ __global__ __launch_bounds__(Wg::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
   if (t >= total) return;
   const auto *const off = (const __attribute__((address_space(4))) int *)(uintptr_t)p.offsets;  // scalar loads
   struct Tile {
-    int e, mt, nt, r0, rows, KT;
+    int e, mt, nt, s, r0, rows, KT;
   };
   auto tile = [&](int at) __attribute__((always_inline)) {
     Tile d;
+    d.s = at / (p.El * per);
+    at -= d.s * p.El * per;
     d.e = at / per;
     d.mt = (at - d.e * per) / NT;
     d.nt = at - d.e * per - d.mt * NT;
     d.r0 = max(off[d.e], 0);
     d.rows = max(min(off[d.e + 1], p.R_cap) - d.r0, 0);
+    if (p.splits > 1) train::part_of(d.s, p.splits, d.r0, d.rows);
     d.KT = (d.rows + C::BK - 1) / C::BK;
     return d;
   };
@@ -711,7 +711,7 @@ __global__ __launch_bounds__(Wg::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
       place(dn);
       first(dn.KT);
     }
-    TO *out = (TO *)p.dw + ((size_t)d.e * p.M + d.mt * C::BM) * p.N + d.nt * C::BN;
+    TO *out = (TO *)p.dw + (((size_t)d.s * p.El + d.e) * p.M + d.mt * C::BM) * p.N + d.nt * C::BN;
     const int ms = p.M - d.mt * C::BM, ns = p.N - d.nt * C::BN;
     const bool full = ms >= C::BM && ns >= C::BN;
     if (ADD && KT == 0) {
@@ -754,4 +754,6 @@ hipError_t train::launch_wgrad_dma(const WgradArgs &a, hipStream_t s) {
   return a.b_index ? wgrad_by_add<false, true>(a, s) : wgrad_by_add<false, false>(a, s);
 }
 
-hipError_t train::launch_mm_dma(const MmArgs &a, hipStream_t s) { return a.kn ? by_index<true>(a, s) : by_index<false>(a, s); }
+hipError_t train::launch_mm_dma(const MmArgs &a, bool few, hipStream_t s) {
+  return a.kn ? by_index<true>(a, few, s) : by_index<false>(a, few, s);
+}

@@ -18,7 +18,7 @@ struct MmArgs {
 };
 hipError_t launch_grouped_mm(const MmArgs &a, hipStream_t s);
 bool mm_dma_fits(const MmArgs &a);  // grouped_mm_dma.hip
-hipError_t launch_mm_dma(const MmArgs &a, hipStream_t s);
+hipError_t launch_mm_dma(const MmArgs &a, bool few, hipStream_t s);
 
 // dw[e] = sum over e's rows of a_r b_r^T (+ dw[e] with add).
 struct WgradArgs {
@@ -30,7 +30,14 @@ struct WgradArgs {
   void *dw;                   // [El, M, N]
   int bf16, out_bf16, add;
   void *ws;                   // wgrad_ws_bytes
+  int splits;                 // set by the launchers: an expert's rows in so many parts, part s's sums at dw + s El M N
 };
+// Rows of part s of an expert's rows [r0, r0 + rows), whole 64s but for the last.
+__device__ __forceinline__ void part_of(int s, int splits, int &r0, int &rows) {
+  const int per = ((rows + splits - 1) / splits + 63) & ~63, at = min(s * per, rows);
+  r0 += at;
+  rows = min(per, rows - at);
+}
 size_t wgrad_ws_bytes(int El, int R_cap, int M, int N, int bf16);
 hipError_t launch_grouped_wgrad(const WgradArgs &a, hipStream_t s);
 bool wgrad_dma_fits(const WgradArgs &a);  // grouped_mm_dma.hip

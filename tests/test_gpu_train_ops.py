@@ -85,6 +85,39 @@ def test_mm_rows_per_expert(rows, transposed):
     check_mm([rows] * 3, 1024, 256, (BF, F32), False, transposed)
 
 
+# enough experts and rows that every workgroup works through several tiles, of every height, whole and short
+MANY = [0, 1, 63, 64, 65, 127, 128, 129, 0, 191, 192, 193, 255, 256, 257, 300, 511, 512, 513, 700] * 6
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("N,K", [(8, 8), (256, 64), (264, 72), (520, 136), (512, 200), (248, 584), (257, 129)])
+def test_mm_many_tiles(N, K, gather, transposed, types):
+    check_mm(MANY, N, K, types, gather, transposed)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("counts", [[5000] + [3] * 60, [40] * 200, [1] * 500 + [2000], [0] * 300 + [256] * 40 + [0] * 300, [100] * 1024])
+def test_mm_uneven_loads(counts, transposed):
+    check_mm(counts, 264, 128, (BF, BF), True, transposed)
+    check_mm(counts, 512, 72, (BF, F32), False, transposed)
+
+
+def test_mm_many_tiles_and_shorter_buffers():
+    """Offsets that run past the buffers: the rows there are, nothing behind them."""
+    g = gen(66)
+    w = randn(g, len(MANY), 264, 64, dtype=BF)
+    n = 5000
+    a = randn(g, n, 64, dtype=BF)
+    store = torch.full((n + 300, 264), 7.0, device=DEV, dtype=BF)
+    off = R.offsets_of(MANY)
+    moe.moe_grouped_mm(a, w, off, out=store[:n])
+    assert (store[n:] == 7.0).all()
+    want, mag = R.mm(a, w, off.clamp(max=n))
+    R.check(store[:n], want, mag * 66 * R.STEP32 + want.abs() * R.half_step(BF) * 1.01)
+
+
 @pytest.mark.parametrize("types", TYPES)
 @pytest.mark.parametrize("transposed", [False, True])
 def test_mm_non_finite_values_stay_in_their_rows(types, transposed):
@@ -163,6 +196,48 @@ def test_wgrad_long_sums(M, N, types):
     """Few tiles and many rows."""
     check_wgrad([4099, 1, 2500], M, N, types, "none", False)
     check_wgrad([4099, 1, 2500], M, N, types, "a", True)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("gather", ["none", "a", "b", "both"])
+@pytest.mark.parametrize("add", [False, True])
+def test_wgrad_many_tiles(gather, add, types):
+    """Several tiles a workgroup, whole and short, with experts that have none, one, two and more steps of rows."""
+    counts = [0, 1, 31, 32, 33, 64, 65, 0, 0, 96, 97, 128, 300] * 10
+    for M, N in ((264, 520), (512, 256), (136, 64)):
+        if gather != "both":
+            check_wgrad(counts, M, N, types, gather, add)
+            continue
+        g = gen(M)
+        dt, ot = types
+        off = R.offsets_of(counts)
+        a, ai, _ = grouped_rows(g, counts, M, dt, True)
+        b, bi, _ = grouped_rows(g, counts, N, dt, True)
+        out = randn(g, len(counts), M, N, dtype=ot)
+        old = out.double()
+        moe.moe_grouped_wgrad(a, b, off, a_index=ai, b_index=bi, out=out, add=add)
+        want, mag = R.wgrad(a, b, off, ai, bi)
+        if add:
+            want, mag = want + old, mag + old.abs()
+        R.check(out, want, mag * 303 * R.STEP32 + want.abs() * R.half_step(ot) * 1.01)
+
+
+@pytest.mark.parametrize("types", TYPES)
+def test_wgrad_in_parts_whatever_the_loads(types):
+    """Averages that split the rows, with an expert that has all of them, few or none."""
+    for counts in ([4096, 0, 0], [1, 4000, 30], [0, 0, 0, 5000], [600, 700, 800, 1]):
+        check_wgrad(counts, 136, 264, types, "a", True)
+        check_wgrad(counts, 40, 24, types, "none", False)
+
+
+def test_wgrad_and_offsets_past_the_buffers():
+    g = gen(67)
+    counts, n = [40] * 30, 700
+    a, b = randn(g, n, 256, dtype=BF), randn(g, n, 256, dtype=BF)
+    off = R.offsets_of(counts)
+    got = moe.moe_grouped_wgrad(a, b, off, dtype=F32)
+    want, mag = R.wgrad(a, b, off.clamp(max=n))
+    R.check(got, want, mag * 43 * R.STEP32)
 
 
 def test_wgrad_non_finite_rows_stay_with_their_expert():
