@@ -99,9 +99,9 @@ struct Source {
       for (int u = 0; u < COUNT; u++) dma(r, to + (wave + NW * u) * 1024, off[u] | m, so);
     }
   }
-  // k-major tile, BK = 64: segment s holds rows 8s .. 8s + 7.  ``row`` gives the byte offset of
-  // segment u's tile row.
-  template <typename F>
+  // k-major tile of 128 bytes a row and step: segment s holds rows 8s .. 8s + 7.  ``row`` gives the byte offset of segment u's
+  // tile row.  ESZ: bytes of an element.
+  template <int ESZ = 2, typename F>
   __device__ __forceinline__ void k_major(int wave, int lane, int K, F row) {
     static_assert(NW % 2 == 0, "a lane's chunk is the same in all of its segments");
     int chunk = 0;
@@ -112,7 +112,17 @@ struct Source {
       off[u] = row(u, t) + (uint32_t)chunk * 16u;
     }
     step = 128;
-    last = (K & 63) != 0 && chunk * 8 >= (K & 63) ? kNowhere : 0u;
+    const int tail = K & (128 / ESZ - 1);
+    last = tail != 0 && chunk * (16 / ESZ) >= tail ? kNowhere : 0u;
+  }
+  // fp32 k rows of R columns, as they lie in memory (they are read word by word).
+  template <int R, int BK>
+  __device__ __forceinline__ void mn_words(int wave, int lane, uint32_t ld, uint32_t col) {
+#pragma unroll
+    for (int u = 0; u < N; u++)
+      off[u] = (uint32_t)((wave + NW * u) * (256 / R) + lane / (R / 4)) * ld + col + (uint32_t)(lane % (R / 4)) * 16u;
+    step = BK * ld;
+    last = 0;
   }
   // mn-major tile of R columns from byte ``col`` of rows that lie ``ld`` bytes apart, BK k rows a step.
   template <int R, int BK>
@@ -276,7 +286,7 @@ struct MmTile {
   bool once;  // the expert's only tile of rows: its matrix is read once
   const void *w;
 };
-template <typename C>
+template <typename C, int ESZ = 2>
 struct MmTiles {
   const __attribute__((address_space(4))) int *off;
   int El, R_cap, NT, G, upto, total;
@@ -311,7 +321,7 @@ struct MmTiles {
     t.r0 = beg + (rr - t.nt * mtiles) * t.trows;
     t.once = mtiles == 1;
     t.rows = min(t.trows, beg + cnt - t.r0);
-    t.w = (const char *)p.w + (size_t)e * p.N * p.K * 2;
+    t.w = (const char *)p.w + (size_t)e * p.N * p.K * ESZ;
     return t;
   }
 };
@@ -461,39 +471,44 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
 }
 
 // Few rows an expert: the matrices are read once, so what counts is how much of them is under way.  Tiles of up to 32 rows
-// x 64 columns, 64 values of the contraction a step, six steps in LDS (72 KB, two workgroups on a compute unit); each of four
-// waves multiplies a quarter of every step, and the quarters are joined at the end.
+// x 64 columns, 128 bytes of the contraction a step, six steps in LDS (72 KB, two workgroups on a compute unit); each of four
+// waves multiplies a quarter of every step, and the quarters are joined at the end.  64 tokens x 8 of 128 experts, 1536 x 4096:
+// 231 us, 6.9 TB/s.  fp32 operands go through the same tiles, 32 values a step, on v_mfma_f32_32x32x2_f32.
+template <typename T>
 struct Few {
-  static constexpr int BM = 32, BN = 64, BK = 64, NW = 4, NTHR = 256, S = 6;
-  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2, LDS = S * (A_BYTES + B_BYTES);
+  static constexpr int BM = 32, BN = 64, BK = 128 / sizeof(T), NW = 4, NTHR = 256, S = 6;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, LDS = S * (A_BYTES + B_BYTES);
   static constexpr int NA = A_BYTES / 1024 / NW, NBL = B_BYTES / 1024 / NW;
   static constexpr int PITCH = BN * 4 + 16;  // bytes between the rows of a quarter's sums
   static_assert(NW * BM * PITCH <= LDS, "the quarters fit");
 };
 
-template <bool KN, bool GATHER, typename TO>
-__global__ __launch_bounds__(Few::NTHR, 2) void mm_few_kernel(train::MmArgs p) {
+template <typename T, bool KN, bool GATHER, typename TO>
+__global__ __launch_bounds__(Few<T>::NTHR, 2) void mm_few_kernel(train::MmArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
-  using C = Few;
+  using C = Few<T>;
+  constexpr int ESZ = sizeof(T);
+  constexpr bool F32 = ESZ == 4;
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const MmTiles<C> tiles(p, lane);
+  const MmTiles<C, ESZ> tiles(p, lane);
   if ((int)blockIdx.x >= tiles.total) return;
   const int xcd = blockIdx.x & 7, q = tiles.total >> 3, rem = tiles.total & 7;  // runs of tiles to an XCD
   const MmTile t = tiles.at(xcd * q + min(xcd, rem) + (blockIdx.x >> 3), p);
   const int K = p.K, KT = (K + C::BK - 1) / C::BK, rows = t.rows;
-  const uint32_t lda = (uint32_t)K * 2u;
+  const uint32_t lda = (uint32_t)K * ESZ, ldn = (uint32_t)p.N * ESZ, col = (uint32_t)t.nt * C::BN * ESZ;
   Source<C::NA, C::NW> sa;
   Source<C::NBL, C::NW> sb;
   if constexpr (GATHER) sa.r = resource(p.a, (size_t)p.a_rows * lda);
   else sa.r = resource((const char *)p.a + (size_t)t.r0 * lda, (size_t)rows * lda);
-  sa.k_major(wave, lane, K, [&](int, int r) {
+  sa.template k_major<ESZ>(wave, lane, K, [&](int, int r) {
     const int at = min(r, rows - 1);  // rows past the end repeat the last one; nothing of them is stored
     return (uint32_t)(GATHER ? min(max(p.a_index[t.r0 + at], 0), p.a_rows - 1) : at) * lda;
   });
-  sb.r = resource(t.w, (size_t)p.N * K * 2);
-  if constexpr (KN) sb.template mn_major<C::BN, C::BK>(wave, lane, (uint32_t)p.N * 2u, t.nt * C::BN * 2u);
-  else sb.k_major(wave, lane, K, [&](int, int r) { return (uint32_t)min(t.nt * C::BN + r, p.N - 1) * lda; });
+  sb.r = resource(t.w, (size_t)p.N * K * ESZ);
+  if constexpr (KN && F32) sb.template mn_words<C::BN, C::BK>(wave, lane, ldn, col);
+  else if constexpr (KN) sb.template mn_major<C::BN, C::BK>(wave, lane, ldn, col);
+  else sb.template k_major<ESZ>(wave, lane, K, [&](int, int r) { return (uint32_t)min(t.nt * C::BN + r, p.N - 1) * lda; });
   const uint32_t to = lds_at(lds);
   // Step kt into its slot.  Steps past the end load nothing (every lane's offset is nowhere), so that the count below holds.
   int slot = 0;
@@ -511,8 +526,8 @@ __global__ __launch_bounds__(Few::NTHR, 2) void mm_few_kernel(train::MmArgs p) {
     slot = slot + 1 == C::S ? 0 : slot + 1;
   };
   for (int kt = 0; kt < C::S - 1; kt++) load(kt);
-  const Frag<false, C::BM, 1> fa(0, lane);
-  const Frag<KN, C::BN, 2> fb(0, lane);
+  const Frag<false, C::BM, 1> fa(0, lane);  // 16 bytes of a k-major row: eight bf16 or four fp32
+  const Frag<KN && !F32, C::BN, 2> fb(0, lane);
   f32x16_t acc[2];
 #pragma unroll
   for (int j = 0; j < 2; j++)
@@ -523,10 +538,29 @@ __global__ __launch_bounds__(Few::NTHR, 2) void mm_few_kernel(train::MmArgs p) {
     // the step's loads have landed; the slot that is filled next was read a step ago
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((C::NA + C::NBL) * (C::S - 2)) : "memory");
     const char *a = lds + rd * (C::A_BYTES + C::B_BYTES), *b = a + C::A_BYTES;
-    const bf16x8_t af = fa.at(a, wave, 0), b0 = fb.at(b, wave, 0), b1 = fb.at(b, wave, 1);
-    load(kt + C::S - 1);
-    acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b0, af, acc[0], 0, 0, 0);
-    acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b1, af, acc[1], 0, 0, 0);
+    if constexpr (F32) {  // this wave's eight values: instruction e takes 4g + e of lane group g
+      const u32x4_t av = __builtin_bit_cast(u32x4_t, fa.at(a, wave, 0));
+      u32x4_t bv[2];
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        if constexpr (KN) {
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            bv[j][e] = *(const uint32_t *)(b + (8 * wave + 4 * (lane >> 5) + e) * (C::BN * 4) + (32 * j + (lane & 31)) * 4);
+        } else bv[j] = __builtin_bit_cast(u32x4_t, fb.at(b, wave, j));
+      }
+      load(kt + C::S - 1);
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(bv[j][e]), __uint_as_float(av[e]), acc[j], 0, 0, 0);
+    } else {
+      const bf16x8_t af = fa.at(a, wave, 0), b0 = fb.at(b, wave, 0), b1 = fb.at(b, wave, 1);
+      load(kt + C::S - 1);
+      acc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b0, af, acc[0], 0, 0, 0);
+      acc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b1, af, acc[1], 0, 0, 0);
+    }
     rd = rd + 1 == C::S ? 0 : rd + 1;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -558,15 +592,17 @@ hipError_t launch(const train::MmArgs &a, hipStream_t s) {
   hipLaunchKernelGGL((mm_dma_kernel<KN, GATHER, TO>), dim3(kWorkers), dim3(Mm::NTHR), 0, s, a);
   return hipGetLastError();
 }
-template <bool KN, bool GATHER, typename TO>
+template <typename T, bool KN, bool GATHER, typename TO>
 hipError_t launch_few(const train::MmArgs &a, hipStream_t s) {
-  const long long mt = std::min(((long long)a.R_cap + (long long)a.El * (Few::BM - 1)) / Few::BM, (long long)a.R_cap);
-  hipLaunchKernelGGL((mm_few_kernel<KN, GATHER, TO>), dim3((unsigned)(mt * ceil_div_i(a.N, Few::BN))), dim3(Few::NTHR), 0, s, a);
+  using C = Few<T>;
+  const long long mt = std::min(((long long)a.R_cap + (long long)a.El * (C::BM - 1)) / C::BM, (long long)a.R_cap);
+  hipLaunchKernelGGL((mm_few_kernel<T, KN, GATHER, TO>), dim3((unsigned)(mt * ceil_div_i(a.N, C::BN))), dim3(C::NTHR), 0, s, a);
   return hipGetLastError();
 }
 template <bool KN, bool GATHER>
 hipError_t by_out(const train::MmArgs &a, bool few, hipStream_t s) {
-  if (few) return a.out_bf16 ? launch_few<KN, GATHER, uint16_t>(a, s) : launch_few<KN, GATHER, float>(a, s);
+  if (!a.bf16) return launch_few<float, KN, GATHER, float>(a, s);
+  if (few) return a.out_bf16 ? launch_few<uint16_t, KN, GATHER, uint16_t>(a, s) : launch_few<uint16_t, KN, GATHER, float>(a, s);
   return a.out_bf16 ? launch<KN, GATHER, uint16_t>(a, s) : launch<KN, GATHER, float>(a, s);
 }
 template <bool KN>
@@ -727,11 +763,11 @@ __global__ __launch_bounds__(Wg::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
 
 }  // namespace
 
-// bf16 rows of whole 16-byte pieces, every 32-bit byte offset below kNowhere.
+// Rows of whole 16-byte pieces, every 32-bit byte offset below kNowhere.
 bool train::mm_dma_fits(const MmArgs &a) {
-  const long long lim = 1LL << 31;
-  return a.bf16 && a.K % 8 == 0 && a.N % 8 == 0 && (long long)a.N * a.K * 2 < lim &&
-         (a.a_index ? (long long)a.a_rows * a.K * 2 < lim : 256LL * a.K * 2 < lim);
+  const long long lim = 1LL << 31, esz = a.bf16 ? 2 : 4, v = 16 / esz;
+  return a.K % v == 0 && a.N % v == 0 && (long long)a.N * a.K * esz < lim &&
+         (a.a_index ? (long long)a.a_rows * a.K * esz < lim : 256LL * a.K * esz < lim);
 }
 template <bool GA, bool GB, bool ADD>
 static hipError_t wgrad_by_out(const train::WgradArgs &a, hipStream_t s) {

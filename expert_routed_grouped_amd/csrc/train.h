@@ -18,7 +18,7 @@ struct MmArgs {
 };
 hipError_t launch_grouped_mm(const MmArgs &a, hipStream_t s);
 bool mm_dma_fits(const MmArgs &a);  // grouped_mm_dma.hip
-hipError_t launch_mm_dma(const MmArgs &a, bool few, hipStream_t s);
+hipError_t launch_mm_dma(const MmArgs &a, bool few, hipStream_t s);  // fp32: few only
 
 // dw[e] = sum over e's rows of a_r b_r^T (+ dw[e] with add).
 struct WgradArgs {
