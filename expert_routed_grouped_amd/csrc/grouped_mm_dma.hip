@@ -235,6 +235,22 @@ __device__ __forceinline__ void store(const f32x16_t (&acc)[MA][NB], char *lds, 
   for (int i = 0; i < MB; i++)
 #pragma unroll
     for (int j0 = 0; j0 < NB; j0 += JB) {
+      constexpr int U = 32 * LR / 64;
+      const int n = n0 + 32 * j0 + lane % LR * V;
+      // a wave's own address and a lane's offset from it
+      auto place = [&](int u) __attribute__((always_inline)) {
+        return (TO *)((char *)(out + (size_t)(m0 + 32 * i + u * (64 / LR)) * ld + n0 + 32 * j0) + at_lane);
+      };
+      auto inside = [&](int u) __attribute__((always_inline)) {
+        return FULL || (m0 + 32 * i + u * (64 / LR) + lane / LR < rows && n < cols);
+      };
+      // What is added to: all of a pass on its way at once, past the caches as the sums are (6000 tokens' fp32 gradients of 4096 x
+      // 1536: one after the other 1753 us, 1495 at once, 1331 past the caches).
+      u32x4_t old[ADD ? U : 1];
+      if constexpr (ADD) {
+#pragma unroll
+        for (int u = 0; u < U; u++) old[u] = inside(u) ? __builtin_nontemporal_load((const u32x4_t *)place(u)) : u32x4_t{0u, 0u, 0u, 0u};
+      }
 #pragma unroll
       for (int j = 0; j < JB; j++)
 #pragma unroll
@@ -244,25 +260,25 @@ __device__ __forceinline__ void store(const f32x16_t (&acc)[MA][NB], char *lds, 
           train::store_n<4>((TS *)(w + (32 * j + 8 * q) * (int)sizeof(TS)), v);
         }
       asm volatile("" ::: "memory");  // other lanes' values are read: the order of a wave's LDS accesses is the program's
-      const int n = n0 + 32 * j0 + lane % LR * V;
 #pragma unroll
-      for (int u = 0; u < 32 * LR / 64; u++) {
-        const int m = m0 + 32 * i + u * (64 / LR) + lane / LR;
+      for (int u = 0; u < U; u++) {
         const char *const at = rd + u * (64 / LR) * kOutPitch;
-        // a wave's own address and a lane's offset from it
-        TO *const o = (TO *)((char *)(out + (size_t)(m0 + 32 * i + u * (64 / LR)) * ld + n0 + 32 * j0) + at_lane);
-        if (FULL || (m < rows && n < cols)) {
+        if (inside(u)) {
           if constexpr (ADD) {
             float x[V], y[V];
             train::load_n<V>((const float *)at, x);
-            train::load_n<V>(o, y);
+            train::load_n<V>((const TO *)&old[u], y);
 #pragma unroll
             for (int k = 0; k < V; k++) x[k] += y[k];
-            train::store_n<V>(o, x);
+            u32x4_t v;
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+              v[k] = sizeof(TO) == 4 ? __float_as_uint(x[k]) : pack_bf16x2(x[2 * k % V], x[(2 * k + 1) % V]);
+            __builtin_nontemporal_store(v, (u32x4_t *)place(u));
           } else {
             const u32x4_t v = *(const u32x4_t *)at;
-            if constexpr (ONCE) __builtin_nontemporal_store(v, (u32x4_t *)o);
-            else *(u32x4_t *)o = v;
+            if constexpr (ONCE) __builtin_nontemporal_store(v, (u32x4_t *)place(u));
+            else *(u32x4_t *)place(u) = v;
           }
         }
       }
