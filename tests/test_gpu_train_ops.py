@@ -507,3 +507,63 @@ def test_block_norm_backward_parts():
     assert none["dx"].shape == (0, 264) and all((none[n] == 0).all() for n in ("dw_next", "dw_post", "dgate"))
     x, n, r1, r2 = moe.moe_block_norm(s[:0], wn, y=y[:0], stats=True)
     assert x.shape == n.shape == (0, 264) and r1.shape == (0,) and r2 is None
+
+
+# ------------------------------------------------------------------ sizes past 32 bits
+def test_rows_past_four_gigabytes():
+    """Outputs and inputs of more than 2^32 bytes: the first and the last rows."""
+    g, R_, N, K = gen(77), 1_100_000, 2048, 64
+    off = torch.tensor([0, 1000, R_ - 700, R_], dtype=torch.int32, device=DEV)
+    a, w = randn(g, R_, K, dtype=BF), randn(g, 3, N, K, dtype=BF)
+    out = moe.moe_grouped_mm(a, w, off)
+    for i, j, e in ((0, 300, 0), (R_ - 1000, R_ - 700, 1), (R_ - 700, R_, 2)):
+        want = a[i:j].double() @ w[e].double().T
+        mag = a[i:j].double().abs() @ w[e].double().abs().T
+        R.check(out[i:j], want, mag * (K + 2) * R.STEP32 + want.abs() * R.half_step(BF) * 1.01)
+    back = moe.moe_grouped_mm(out, w, off, transposed=True)  # rows of 4 KB each, from 4.5 GB
+    i = R_ - 700
+    want, mag = out[i:].double() @ w[2].double(), out[i:].double().abs() @ w[2].double().abs()
+    R.check(back[i:], want, mag * (N + 2) * R.STEP32 + want.abs() * R.half_step(BF) * 1.01)
+    h = moe.moe_swiglu(out, off)
+    g64 = out[i:].double().chunk(2, 1)[0]
+    want = R.swiglu(out[i:])
+    R.check(h[i:], want, want.abs() * (1.01 * R.half_step(BF) + (20 + 2 * g64.abs()) * R.STEP32) + 1e-30)  # as in test_swiglu
+    last = torch.tensor([0, 0, i, R_], dtype=torch.int32, device=DEV)
+    dw = moe.moe_grouped_wgrad(out, a, last, dtype=F32)
+    want, mag = out[i:].double().T @ a[i:].double(), out[i:].double().abs().T @ a[i:].double().abs()
+    R.check(dw[2], want, mag * 703 * R.STEP32)
+    assert (dw[0] == 0).all()
+
+
+def test_tokens_past_two_gigabytes():
+    """Gathered from a tensor that 31-bit offsets do not reach."""
+    g, T, K = gen(78), 300_000, 4096
+    a, w = torch.zeros((T, K), dtype=BF, device=DEV), randn(g, 2, 96, K, dtype=BF)
+    pick = torch.tensor([0, T - 1, 262_145, T - 2, 5, 270_000], dtype=torch.int32, device=DEV)
+    a[pick.long()] = randn(g, 6, K, dtype=BF)
+    off = R.offsets_of([2, 4])
+    want, mag = R.mm(a, w, off, pick)
+    R.check(moe.moe_grouped_mm(a, w, off, row_index=pick), want, mag * (K + 2) * R.STEP32 + want.abs() * R.half_step(BF) * 1.01)
+    b = randn(g, 6, 136, dtype=BF)
+    want, mag = R.wgrad(b, a, off, None, pick)
+    R.check(moe.moe_grouped_wgrad(b, a, off, b_index=pick, dtype=F32), want, mag * 9 * R.STEP32)
+
+
+def test_norm_past_four_gigabytes():
+    T, H = 530_000, 4096
+    x = torch.ones((T, H), dtype=BF, device=DEV)
+    x[-1] = 3
+    w = torch.full((H,), 2.0, device=DEV)
+    _, n, rn, _ = moe.moe_block_norm(x, w, stats=True)
+    assert (n[0] == 2).all() and (n[-1] == 2).all() and abs(float(rn[-1]) * 3 - 1) < 1e-5
+    # gradients in three rows alone: adding the others' zeros rounds nothing, so three terms a column.  In such a row dn w is
+    # constant, so that dn w - xh mean(dn w xh) is eps-sized and dx is dx_out; half a step of its type.
+    dn = torch.zeros_like(x)
+    for t in (0, T - 2, T - 1):
+        dn[t] = x[t]
+    got = moe.moe_block_norm_backward(x, w, rn, dn, dx_out=x)
+    half = R.half_step(BF)
+    assert (got["dx"][-1] - 3).abs().max() <= 3 * half and (got["dx"][:-1].amax() - 1).abs() <= half
+    assert (got["dx"][:-1].amin() - 1).abs() <= half
+    want = 1 / (1 + 1e-6) ** 0.5 * 2 + 9 / (9 + 1e-6) ** 0.5
+    assert (got["dw_next"].double() - want).abs().max() <= want * (3 + 8) * R.STEP32
