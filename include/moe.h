@@ -716,9 +716,11 @@ int moe_swiglu_backward(const void *gu, const void *dh, int dtype, const int32_t
  *                    rows[rows_at[t, j], :]
  * ``rows`` [R_cap, H] are the input gradients of the experts' rows (rows_dtype), rows_at [T, k] the token_row of the
  * local experts' moe_permute; rows NULL: none.  offsets [E + 1] and row_token [T*k] are those of moe_permute over all
- * E experts (e_begin 0, e_end E), whether this rank holds them or not.  They are read for dw_router and d_bias only.  Outputs that are NULL are not computed.  x [T, H] and w_router [E, H]
- * of type ``dtype``, dx [T, H] of type dx_dtype (MOE_BF16 or MOE_F32).  Sums in fp32, in an order that the routing
- * alone fixes.  Gates that other ranks' experts contribute to must be summed over the ranks first.  T == 0 writes zeros to dw_router and d_bias.
+ * E experts (e_begin 0, e_end E), whether this rank holds them or not.  They are read for dw_router and d_bias only.  Outputs
+ * that are NULL are not computed.  x [T, H] and w_router [E, H] of type ``dtype``, dx [T, H] of type dx_dtype (MOE_BF16 or
+ * MOE_F32).  Sums in fp32, in an order that the routing alone fixes.  topk_ids must hold distinct experts per token, as for
+ * moe_permute.  Gates that other ranks' experts contribute to must be summed over the ranks first.  T == 0 writes zeros to
+ * dw_router and d_bias.
  * Errors: MOE_ERR_SHAPE (E <= 1024, 1 <= k <= min(E, 32), H <= 2^20, T*k < 2^28, overlapping buffers),
  * MOE_ERR_DTYPE, MOE_ERR_NULL, MOE_ERR_ALIGN (16 bytes), MOE_ERR_HIP.
  */

@@ -220,3 +220,21 @@ def test_two_graphs_do_not_share_memory():
         for _, res, want, _ in runs:
             for p, q in zip(res, want):
                 assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("cfg", [CFGS[0], CFGS[1]], ids=["f32", "bf16"])
+def test_a_block_without_tokens(cfg):
+    """A rank that got no tokens: empty results, zero gradients, and what is added to is left as it was."""
+    dev, x, d_out = block(cfg)
+    out, saved = train.block_forward(dev, x[:0])
+    assert out.shape == (0, cfg.H)
+    grads = train.block_backward(dev, saved, d_out[:0])
+    assert grads["dx"].shape == (0, cfg.H)
+    for n, t in grads.items():
+        assert t is not None and (n == "dx" or (t == 0).all()), n
+    _, full = train.block_forward(dev, x)
+    have = train.block_backward(dev, full, d_out)
+    want = {n: have[n].clone() for n in ("w_gate_up", "w_down")}
+    train.block_backward(dev, saved, d_out[:0], grads=have)
+    for n, t in want.items():
+        assert torch.equal(have[n], t), n
