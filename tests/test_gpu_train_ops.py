@@ -240,6 +240,23 @@ def test_wgrad_and_offsets_past_the_buffers():
     R.check(got, want, mag * 43 * R.STEP32)
 
 
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("M,N", [(1, 1), (65, 131), (130, 5), (64, 128), (67, 777)])
+def test_wgrad_of_experts_without_rows_writes_its_matrices_alone(M, N, types):
+    """Zeros in every element of theirs and nowhere else; nothing at all where gradients are added to."""
+    t, ot = types
+    off = R.offsets_of([0, 2, 0, 0])
+    g, n, pad = gen(M), 4 * M * N, 64
+    a, b = randn(g, 2, M, dtype=t), randn(g, 2, N, dtype=t)
+    for add in (False, True):
+        whole = torch.full((n + 2 * pad,), 7.0, dtype=ot, device=DEV)
+        out = whole[pad:pad + n].view(4, M, N)
+        moe.moe_grouped_wgrad(a, b, off, out=out, add=add)
+        assert (whole[:pad] == 7.0).all() and (whole[pad + n:] == 7.0).all()
+        for e in (0, 2, 3):
+            assert (out[e] == (7.0 if add else 0.0)).all(), (add, e)
+
+
 def test_wgrad_non_finite_rows_stay_with_their_expert():
     g, off = gen(8), R.offsets_of([33, 0, 31])
     a, b = randn(g, 64, 64, dtype=BF), randn(g, 64, 128, dtype=BF)
