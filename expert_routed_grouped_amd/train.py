@@ -34,13 +34,15 @@ def experts_forward(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tens
     T, k = perm["token_row"].shape
     R = _rows(perm)
     row_token, row_w = perm["row_token"][:R], perm["row_w"][:R]
-    gu = moe.moe_grouped_mm(x, w_gate_up, perm["offsets"], row_index=row_token, stream=stream)
-    h = moe.moe_swiglu(gu, perm["offsets"], row_w, stream=stream)
-    rows = moe.moe_grouped_mm(h, w_down, perm["offsets"], dtype=torch.float32, stream=stream)
-    ones = moe._new((T, k), torch.float32, x.device, stream)
-    with torch.cuda.stream(moe.torch_stream(stream, x.device)):
-        ones.fill_(1.0)
-    return moe.moe_combine(rows, perm["token_row"], ones, stream=stream), {"x": x, "gu": gu, "perm": perm}
+    with _on(x):
+        gu = moe.moe_grouped_mm(x, w_gate_up, perm["offsets"], row_index=row_token, stream=stream)
+        h = moe.moe_swiglu(gu, perm["offsets"], row_w, stream=stream)
+        rows = moe.moe_grouped_mm(h, w_down, perm["offsets"], dtype=torch.float32, stream=stream)
+        ones = moe._new((T, k), torch.float32, x.device, stream)
+        with torch.cuda.stream(moe.torch_stream(stream, x.device)):
+            ones.fill_(1.0)
+        y = moe.moe_combine(rows, perm["token_row"], ones, stream=stream)
+    return y, {"x": x, "gu": gu, "perm": perm}
 
 
 def experts_backward(saved: dict, dy: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
@@ -54,14 +56,15 @@ def experts_backward(saved: dict, dy: torch.Tensor, w_gate_up: torch.Tensor, w_d
     perm, x, gu = saved["perm"], saved["x"], saved["gu"]
     off, R = perm["offsets"], _rows(perm)
     row_token, row_w, token_row = perm["row_token"][:R], perm["row_w"][:R], perm["token_row"]
-    dh = moe.moe_grouped_mm(dy, w_down, off, row_index=row_token, transposed=True, stream=stream)
-    dgu, h, d_row_w = moe.moe_swiglu_backward(gu, dh, off, row_w, h=dh, stream=stream)
-    dw_down = moe.moe_grouped_wgrad(dy, h, off, a_index=row_token, out=dw_down, add=add, dtype=dtype, stream=stream)
-    dw_gate_up = moe.moe_grouped_wgrad(dgu, x, off, b_index=row_token, out=dw_gate_up, add=add, dtype=dtype, stream=stream)
-    dx_rows = moe.moe_grouped_mm(dgu, w_gate_up, off, transposed=True, stream=stream)
-    with torch.cuda.stream(moe.torch_stream(stream, x.device)):
-        at = token_row.clamp(min=0).long()
-        d_gates = torch.where(token_row >= 0, d_row_w[at], 0.0) if R > 0 else torch.zeros_like(token_row, dtype=torch.float32)
+    with _on(x):
+        dh = moe.moe_grouped_mm(dy, w_down, off, row_index=row_token, transposed=True, stream=stream)
+        dgu, h, d_row_w = moe.moe_swiglu_backward(gu, dh, off, row_w, h=dh, stream=stream)
+        dw_down = moe.moe_grouped_wgrad(dy, h, off, a_index=row_token, out=dw_down, add=add, dtype=dtype, stream=stream)
+        dw_gate_up = moe.moe_grouped_wgrad(dgu, x, off, b_index=row_token, out=dw_gate_up, add=add, dtype=dtype, stream=stream)
+        dx_rows = moe.moe_grouped_mm(dgu, w_gate_up, off, transposed=True, stream=stream)
+        with torch.cuda.stream(moe.torch_stream(stream, x.device)):
+            at = token_row.clamp(min=0).long()
+            d_gates = torch.where(token_row >= 0, d_row_w[at], 0.0) if R > 0 else torch.zeros_like(token_row, dtype=torch.float32)
     return {"dw_gate_up": dw_gate_up, "dw_down": dw_down, "dx_rows": dx_rows, "d_gates": d_gates}
 
 
