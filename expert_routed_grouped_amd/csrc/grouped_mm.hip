@@ -11,14 +11,11 @@
 // LDS read.  What lies outside an expert's rows, N, M or K is stored as zero, in both operands, so that nothing
 // outside can reach a product.  32 experts of 1024 x 2048 in fp32, 12000 rows: 505 us, 100 TFLOP/s, matrix units busy in 0.65 of the
 // cycles, the rest their start and the last, partly idle round; gradients of 8 x 777 x 515 from 602 rows 21 us, latency.
-#include "ffn_common.h"
-#include "train.h"
+#include "grouped_tiles.h"
 
 #include <algorithm>
 
 namespace {
-
-using ffn::TileParams;
 
 constexpr int BN = 128, KB = 128, PITCH = KB + 16;  // bytes of a step; bytes between rows of a k-major tile
 constexpr int NTHR = 256;
@@ -208,18 +205,22 @@ struct Waves {  // BM = 128: 2 x 2 waves of 64 x 64 outputs; 64: 2 x 2 of 32 x 6
 template <typename T>
 constexpr int kRows = sizeof(T) == 4 ? 64 : 128;
 
+template <int BM_>
+struct Shape {
+  static constexpr int BM = BM_, BN = ::BN;
+};
+
 template <typename T, typename TO, bool KN, int BM, bool VA, bool VB>
 __global__ __launch_bounds__(NTHR) void mm_kernel(train::MmArgs p) {
   using OA = Operand<T, false, BM>;
   using OB = Operand<T, KN, BN>;
   using Wv = Waves<BM>;
   __shared__ __attribute__((aligned(16))) char lds[2 * (OA::BYTES + OB::BYTES)];
-  TileParams tp{};
-  tp.offsets = p.offsets;
-  tp.El = p.El;
-  tp.R_cap = p.R_cap;
-  int e, nt, r0, rows;
-  if (!ffn::find_tile<BM>(tp, (p.N + BN - 1) / BN, e, nt, r0, rows) || r0 < 0) return;
+  const train::MmTiles<Shape<BM>, sizeof(T)> tiles(p, threadIdx.x & 63);
+  if ((int)blockIdx.x >= tiles.total) return;
+  const int xcd = blockIdx.x & 7, q = tiles.total >> 3, rem = tiles.total & 7;  // runs of tiles to an XCD
+  const train::MmTile t = tiles.at(xcd * q + min(xcd, rem) + (blockIdx.x >> 3), p);
+  const int nt = t.nt, r0 = t.r0, rows = t.rows;
   OA A{};
   A.base = (const T *)p.a;
   A.index = p.a_index;
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(NTHR) void mm_kernel(train::MmArgs p) {
   A.limit = p.a_rows;
   A.K = p.K;
   OB B{};
-  B.base = (const T *)p.w + (size_t)e * p.N * p.K;
+  B.base = (const T *)t.w;
   if constexpr (KN) {
     B.ld = p.N;
     B.rows = p.K;
