@@ -266,7 +266,8 @@ __global__ __launch_bounds__(NTHR) void wgrad_kernel(train::WgradArgs p) {
   const int at = xcd * each_xcd + min(xcd, more) + (blockIdx.x >> 3);
   const int s = at / (MT * NT * p.El), b = at % (MT * NT * p.El);
   const int e = b / (MT * NT), mt = b / NT % MT, nt = b % NT;
-  int r0 = max(p.offsets[e], 0), rows = max(min(p.offsets[e + 1], p.R_cap) - r0, 0);
+  int r0, rows;
+  train::clip_rows(p.offsets[e], p.offsets[e + 1], p.R_cap, r0, rows);
   if (p.splits > 1) train::part_of(s, p.splits, r0, rows);
   // No rows: nothing to add, or zeros, 16 bytes a lane (6 tokens, 123 experts x 1301 x 1210 fp32: 169 us through the products, 143).
   if (rows == 0) {

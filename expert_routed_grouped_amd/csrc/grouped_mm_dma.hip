@@ -610,8 +610,7 @@ __global__ __launch_bounds__(Wg::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
     d.e = at / per;
     d.mt = (at - d.e * per) / NT;
     d.nt = at - d.e * per - d.mt * NT;
-    d.r0 = max(off[d.e], 0);
-    d.rows = max(min(off[d.e + 1], p.R_cap) - d.r0, 0);
+    train::clip_rows(off[d.e], off[d.e + 1], p.R_cap, d.r0, d.rows);
     if (p.splits > 1) train::part_of(d.s, p.splits, d.r0, d.rows);
     d.KT = (d.rows + C::BK - 1) / C::BK;
     return d;

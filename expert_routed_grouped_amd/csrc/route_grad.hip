@@ -25,7 +25,8 @@ __device__ __forceinline__ void weight_part(const RouteGradArgs &a, int e, int p
   constexpr int kWaves = THR / 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = min((piece * 64 + lane) * N, a.H - N);
-  const int r0 = max(a.offsets[e], 0), cnt = max(min(a.offsets[e + 1], a.T * a.k) - r0, 0);
+  int r0, cnt;
+  train::clip_rows(a.offsets[e], a.offsets[e + 1], a.T * a.k, r0, cnt);
   const int per = (cnt + kWaves - 1) / kWaves, b = r0 + min(wave * per, cnt), end = min(b + per, r0 + cnt);
   float sum[N], bias = 0.0f;
 #pragma unroll

@@ -5,6 +5,13 @@
 
 namespace train {
 
+// The rows [r0, r0 + rows) between an expert's offsets that lie in the buffers.  Both ends are clipped before they are
+// subtracted: whatever the offsets say, the difference fits.
+__device__ __forceinline__ void clip_rows(int begin, int end, int R_cap, int &r0, int &rows) {
+  r0 = min(max(begin, 0), R_cap);
+  rows = max(min(end, R_cap), r0) - r0;
+}
+
 // One product grouped by expert.  Rows r of expert e are offsets[e] .. offsets[e+1] - 1, never past R_cap.
 struct MmArgs {
   const void *a;              // [a_rows, K]; row r of the product reads a[a_index ? a_index[r] : r]

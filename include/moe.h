@@ -630,9 +630,10 @@ int moe_shared_expert(const void *x, int x_dtype, int T, int H, int I_s, const v
  * moe_swiglu, moe_grouped_mm (down, fp32 rows), moe_combine with weights of one (the gates are in h),
  * moe_block_norm; the Python package has both passes in train.py.
  *
- * Rows behind the last expert's, offsets[E_loc] .. R_cap - 1, are neither read nor written, and no row from
- * R_cap on is touched whatever the offsets say.  Buffers that a call writes may not overlap those it reads
- * or each other (MOE_ERR_SHAPE), apart from the exceptions named below.
+ * Rows behind the last expert's, offsets[E_loc] .. R_cap - 1, are neither read nor written.  An expert's rows are those of
+ * offsets[e] .. offsets[e + 1] - 1 that lie in 0 .. R_cap - 1: no row outside the buffers is touched whatever the offsets say.
+ * Offsets that do not ascend leave the rows that they name unspecified.  Buffers that a call writes may not overlap those it
+ * reads or each other (MOE_ERR_SHAPE), apart from the exceptions named below.
  * ------------------------------------------------------------------------------------------------ */
 
 /* moe_grouped_mm flags */
