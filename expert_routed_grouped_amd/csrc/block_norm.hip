@@ -59,7 +59,8 @@ __device__ __forceinline__ float one_w(const void *p, int bf16, size_t i) {
 template <typename TX, typename TY, int W, int NV, int N>
 __global__ __launch_bounds__(W * 64) void block_norm_kernel(NormArgs a) {
   __shared__ float buf[2 * W];
-  const int t = blockIdx.x, H = a.H;
+  const int t = train::block_of(), H = a.H;
+  if (t >= a.T) return;
   const size_t row = (size_t)t * H;
   float x[NV][N], y[NV][N];
 #pragma unroll
@@ -319,7 +320,7 @@ int blocks(int T, int H) {
 template <typename TX, typename TY, typename TD, int W, int NV, int N>
 hipError_t launch(const NormArgs &a, hipStream_t s) {
   if constexpr (std::is_void_v<TD>) {  // T >= 1
-    hipLaunchKernelGGL((block_norm_kernel<TX, TY, W, NV, N>), dim3(a.T), dim3(W * 64), 0, s, a);
+    hipLaunchKernelGGL((block_norm_kernel<TX, TY, W, NV, N>), train::grid_of(a.T, W * 64), dim3(W * 64), 0, s, a);
     return hipGetLastError();
   } else {
     const int G = blocks(a.T, a.H);

@@ -217,9 +217,10 @@ __global__ __launch_bounds__(NTHR) void mm_kernel(train::MmArgs p) {
   using Wv = Waves<BM>;
   __shared__ __attribute__((aligned(16))) char lds[2 * (OA::BYTES + OB::BYTES)];
   const train::MmTiles<Shape<BM>, sizeof(T)> tiles(p, threadIdx.x & 63);
-  if ((int)blockIdx.x >= tiles.total) return;
-  const int xcd = blockIdx.x & 7, q = tiles.total >> 3, rem = tiles.total & 7;  // runs of tiles to an XCD
-  const train::MmTile t = tiles.at(xcd * q + min(xcd, rem) + (blockIdx.x >> 3), p);
+  const int b = train::block_of();
+  if (b >= tiles.total) return;
+  const int xcd = b & 7, q = tiles.total >> 3, rem = tiles.total & 7;  // runs of tiles to an XCD
+  const train::MmTile t = tiles.at(xcd * q + min(xcd, rem) + (b >> 3), p);
   const int nt = t.nt, r0 = t.r0, rows = t.rows;
   OA A{};
   A.base = (const T *)p.a;
@@ -262,8 +263,9 @@ __global__ __launch_bounds__(NTHR) void wgrad_kernel(train::WgradArgs p) {
   const int MT = (p.M + BM - 1) / BM, NT = (p.N + BN - 1) / BN;
   // Workgroups go round-robin over the 8 XCDs: runs of tiles to an XCD, so that the lines that two tiles of an odd row share
   // meet in one L2 (8 x 777 x 515 fp32 from 602 rows 25.3 us in launch order, 20.9 so; bf16 1021 x 1023, 12000 rows 115 and 87).
-  const int G = gridDim.x, each_xcd = G >> 3, more = G & 7, xcd = blockIdx.x & 7;
-  const int at = xcd * each_xcd + min(xcd, more) + (blockIdx.x >> 3);
+  const int G = p.splits * p.El * MT * NT, wg = train::block_of(), each_xcd = G >> 3, more = G & 7, xcd = wg & 7;
+  if (wg >= G) return;
+  const int at = xcd * each_xcd + min(xcd, more) + (wg >> 3);
   const int s = at / (MT * NT * p.El), b = at % (MT * NT * p.El);
   const int e = b / (MT * NT), mt = b / NT % MT, nt = b % NT;
   int r0, rows;
@@ -334,7 +336,7 @@ hipError_t launch_mm(const train::MmArgs &a, hipStream_t s) {
   const bool va = a.K % V == 0, vb = (KN ? a.N : a.K) % V == 0;
   // worst-case tiles: sum of ceil(c / BM) <= (R + El (BM - 1)) / BM
   const long long mt = std::min(((long long)a.R_cap + (long long)a.El * (BM - 1)) / BM, (long long)a.R_cap);
-  const dim3 grid((unsigned)(mt * ceil_div_i(a.N, BN)));
+  const dim3 grid = train::grid_of(mt * ceil_div_i(a.N, BN), NTHR);
   if (va && vb) hipLaunchKernelGGL((mm_kernel<T, TO, KN, BM, true, true>), grid, dim3(NTHR), 0, s, a);
   else if (va) hipLaunchKernelGGL((mm_kernel<T, TO, KN, BM, true, false>), grid, dim3(NTHR), 0, s, a);
   else if (vb) hipLaunchKernelGGL((mm_kernel<T, TO, KN, BM, false, true>), grid, dim3(NTHR), 0, s, a);
@@ -352,7 +354,7 @@ hipError_t pick_mm(const train::MmArgs &a, hipStream_t s) {
 template <typename T, typename TO>
 hipError_t launch_wgrad(const train::WgradArgs &a, hipStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const dim3 grid((unsigned)((long long)a.splits * a.El * ceil_div_i(a.M, kRows<T>) * ceil_div_i(a.N, BN)));
+  const dim3 grid = train::grid_of((long long)a.splits * a.El * ceil_div_i(a.M, kRows<T>) * ceil_div_i(a.N, BN), NTHR);
   const bool va = a.M % V == 0, vb = a.N % V == 0;
   if (va && vb) hipLaunchKernelGGL((wgrad_kernel<T, TO, true, true>), grid, dim3(NTHR), 0, s, a);
   else if (va) hipLaunchKernelGGL((wgrad_kernel<T, TO, true, false>), grid, dim3(NTHR), 0, s, a);

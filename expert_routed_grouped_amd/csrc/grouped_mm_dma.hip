@@ -462,9 +462,10 @@ __global__ __launch_bounds__(Few<T>::NTHR, 2) void mm_few_kernel(train::MmArgs p
   __shared__ __attribute__((aligned(1024))) char lds[C::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const MmTiles<C, ESZ> tiles(p, lane);
-  if ((int)blockIdx.x >= tiles.total) return;
-  const int xcd = blockIdx.x & 7, q = tiles.total >> 3, rem = tiles.total & 7;  // runs of tiles to an XCD
-  const MmTile t = tiles.at(xcd * q + min(xcd, rem) + (blockIdx.x >> 3), p);
+  const int wg = train::block_of();
+  if (wg >= tiles.total) return;
+  const int xcd = wg & 7, q = tiles.total >> 3, rem = tiles.total & 7;  // runs of tiles to an XCD
+  const MmTile t = tiles.at(xcd * q + min(xcd, rem) + (wg >> 3), p);
   const int K = p.K, KT = (K + C::BK - 1) / C::BK, rows = t.rows;
   const uint32_t lda = (uint32_t)K * ESZ, ldn = (uint32_t)p.N * ESZ, col = (uint32_t)t.nt * C::BN * ESZ;
   Source<C::NA, C::NW> sa;
@@ -566,7 +567,7 @@ template <typename T, bool KN, bool GATHER, typename TO>
 hipError_t launch_few(const train::MmArgs &a, hipStream_t s) {
   using C = Few<T>;
   const long long mt = std::min(((long long)a.R_cap + (long long)a.El * (C::BM - 1)) / C::BM, (long long)a.R_cap);
-  hipLaunchKernelGGL((mm_few_kernel<T, KN, GATHER, TO>), dim3((unsigned)(mt * ceil_div_i(a.N, C::BN))), dim3(C::NTHR), 0, s, a);
+  hipLaunchKernelGGL((mm_few_kernel<T, KN, GATHER, TO>), train::grid_of(mt * ceil_div_i(a.N, C::BN), C::NTHR), dim3(C::NTHR), 0, s, a);
   return hipGetLastError();
 }
 template <bool KN, bool GATHER>

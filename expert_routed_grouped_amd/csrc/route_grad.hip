@@ -142,7 +142,7 @@ __device__ __forceinline__ void token_part(const RouteGradArgs &a, int block, fl
 template <typename T, typename TR, typename TO, int N, int THR>
 __global__ __launch_bounds__(THR) void route_grad_kernel(RouteGradArgs a, int pieces) {
   __shared__ float buf[THR * N > THR / 256 * 96 ? THR * N : THR / 256 * 96];
-  const int b = blockIdx.x, weights = a.E * pieces;
+  const int b = train::block_of(), weights = a.E * pieces;
   if (b < weights) weight_part<T, N, THR>(a, b / pieces, b % pieces, buf);
   else token_part<T, TR, TO, N, THR>(a, b - weights, buf);
 }
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(THR) void route_grad_kernel(RouteGradArgs a, int pi
 template <typename T, typename TR, typename TO, int N, int THR>
 hipError_t launch(const RouteGradArgs &a, hipStream_t s) {
   const int pieces = a.dwr ? ceil_div_i(a.H, 64 * N) : (a.dbias ? 1 : 0);
-  const dim3 grid(a.E * pieces + (a.dx ? ceil_div_i(a.T, THR / 256) : 0));
+  const dim3 grid = train::grid_of(a.E * pieces + (a.dx ? ceil_div_i(a.T, THR / 256) : 0), THR);
   hipLaunchKernelGGL((route_grad_kernel<T, TR, TO, N, THR>), grid, dim3(THR), 0, s, a, pieces);
   return hipGetLastError();
 }

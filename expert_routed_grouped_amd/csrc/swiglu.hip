@@ -30,7 +30,7 @@ template <typename T, int N>
 __global__ __launch_bounds__(kWaves * 64) void swiglu_kernel(SwigluArgs a) {
   constexpr bool EXACT = sizeof(T) == 4;
   const int R = a.offsets ? min(a.offsets[a.El], a.R_cap) : a.R_cap, lane = threadIdx.x & 63;
-  const int r = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int r = train::block_of() * kWaves + (threadIdx.x >> 6);
   if (r >= R) return;
   const T *g = (const T *)a.gu + (size_t)r * 2 * a.I, *u = g + a.I;
   T *h = (T *)a.h + (size_t)r * a.I;
@@ -50,7 +50,7 @@ template <typename T, int N>
 __global__ __launch_bounds__(kWaves * 64) void swiglu_backward_kernel(SwigluArgs a) {
   constexpr bool EXACT = sizeof(T) == 4;
   const int R = a.offsets ? min(a.offsets[a.El], a.R_cap) : a.R_cap, lane = threadIdx.x & 63;
-  const int r = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const int r = train::block_of() * kWaves + (threadIdx.x >> 6);
   if (r >= R) return;
   const T *g = (const T *)a.gu + (size_t)r * 2 * a.I, *u = g + a.I, *dh = (const T *)a.dh + (size_t)r * a.I;
   T *dg = (T *)a.dgu + (size_t)r * 2 * a.I, *du = dg + a.I, *h = a.h ? (T *)a.h + (size_t)r * a.I : nullptr;
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(kWaves * 64) void swiglu_backward_kernel(SwigluArgs
 
 template <typename T, int N>
 hipError_t launch(const SwigluArgs &a, bool backward, hipStream_t s) {
-  const dim3 grid(ceil_div_i(a.R_cap, kWaves)), block(kWaves * 64);
+  const dim3 grid = train::grid_of(ceil_div_i(a.R_cap, kWaves), kWaves * 64), block(kWaves * 64);
   if (backward) hipLaunchKernelGGL((swiglu_backward_kernel<T, N>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((swiglu_kernel<T, N>), grid, block, 0, s, a);
   return hipGetLastError();

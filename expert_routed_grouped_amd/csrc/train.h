@@ -5,6 +5,15 @@
 
 namespace train {
 
+// A launch has fewer than 2^32 threads along an axis: more workgroups than that go into rows of 2^21, the last of which may
+// have workgroups too many.  block_of is a workgroup's number, and the same XCD takes it as in one row.
+constexpr int kGridRow = 1 << 21;
+inline dim3 grid_of(long long blocks, int threads) {
+  if (blocks * threads < (1LL << 32)) return dim3((unsigned)blocks);
+  return dim3(kGridRow, (unsigned)((blocks + kGridRow - 1) / kGridRow));
+}
+__device__ __forceinline__ int block_of() { return (int)(blockIdx.y * kGridRow + blockIdx.x); }
+
 // The rows [r0, r0 + rows) between an expert's offsets that lie in the buffers.  Both ends are clipped before they are
 // subtracted: whatever the offsets say, the difference fits.
 __device__ __forceinline__ void clip_rows(int begin, int end, int R_cap, int &r0, int &rows) {
