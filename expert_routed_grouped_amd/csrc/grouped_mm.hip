@@ -368,11 +368,11 @@ hipError_t launch_wgrad(const train::WgradArgs &a, hipStream_t s) {
 hipError_t train::launch_grouped_mm(const MmArgs &a, hipStream_t s) {
   if (mm_dma_fits(a)) {
     // Tiles for few rows an expert on average.  128 experts of 1536 x 4096, top 8, us with those and with the large tiles: 64
-    // tokens 231 and 245, 256 247 and 268, 384 263 and 283, 512 363 and 288; transposed 8 tokens 114 and 127, 24 200 and 206, 64
-    // 243 and 234, 512 376 and 259.  fp32, 32 experts of 1024 x 2048, top 4: 200 tokens 87 and 92, 400 120 and 116.
+    // tokens 230 and 255, 256 243 and 259, 384 248 and 273, 512 296 and 274; transposed 8 tokens 114 and 127, 24 200 and 207, 64
+    // 244 and 233, 512 342 and 259.  fp32, 32 experts of 1024 x 2048, top 4: 200 tokens 73 and 92, 300 84 and 89.
     bool few = a.R_cap <= (a.bf16 ? (a.kn ? 2LL : 24LL) : 40LL) * a.El;
-    // And where the large tiles would leave most of the chip idle: 4 experts x 3000 rows, 64 x 2048, 14 and 44 us; the tiles of
-    // this file where those for few rows would be very many (8 x 375 rows, 1024 x 1024: 20 us, 28 with those, 26 large).
+    // And where the large tiles would leave most of the chip idle: 4 experts x 3000 rows, 64 x 2048, 13 and 44 us; the tiles of
+    // this file where those for few rows would be very many (8 x 375 rows, 1024 x 1024: 18 us, 24 with those, 25 large).
     const int bm = a.bf16 ? 256 : kRows<float>, bn = a.bf16 ? 256 : BN;
     const long long large = (long long)a.El * ceil_div_i(ceil_div_i(a.R_cap, a.El), bm) * ceil_div_i(a.N, bn);
     const long long small = (a.R_cap / 32 + (long long)a.El) * ceil_div_i(a.N, 64);

@@ -197,13 +197,10 @@ struct Frag {
       for (int kk = 0; kk < 4; kk++) base[kk] = (uint32_t)(r0 + n) * 128u + (uint32_t)((2 * kk + g) ^ ((n >> 1) & 7)) * 16u;
     }
   }
-  // The same with kk known at run time only.
+  // The same with kk known at run time only (base[kk] is base[0] ^ 32 kk).
   __device__ __forceinline__ bf16x8_t at(const char *slot, int kk, int b) const {
     if constexpr (MN) return get(slot + kk * 16 * (R * 2), 0, b);
-    else {
-      const uint32_t o = kk == 0 ? base[0] : kk == 1 ? base[1] : kk == 2 ? base[2] : base[3];
-      return *(const bf16x8_t *)(slot + o + b * 4096);
-    }
+    else return *(const bf16x8_t *)(slot + (base[0] ^ (uint32_t)(kk * 32)) + b * 4096);
   }
   __device__ __forceinline__ bf16x8_t get(const char *slot, int kk, int b) const {
     if constexpr (MN) {
@@ -443,7 +440,7 @@ __global__ __launch_bounds__(Mm::NTHR, 1) __attribute__((amdgpu_waves_per_eu(2, 
 // Few rows an expert: the matrices are read once, so what counts is how much of them is under way.  Tiles of up to 32 rows
 // x 64 columns, 128 bytes of the contraction a step, six steps in LDS (72 KB, two workgroups on a compute unit); each of four
 // waves multiplies a quarter of every step, and the quarters are joined at the end.  64 tokens x 8 of 128 experts, 1536 x 4096:
-// 231 us, 6.9 TB/s.  fp32 operands go through the same tiles, 32 values a step, on v_mfma_f32_32x32x2_f32.
+// 230 us, 6.9 TB/s.  fp32 operands go through the same tiles, 32 values a step, on v_mfma_f32_32x32x2_f32.
 template <typename T>
 struct Few {
   static constexpr int BM = 32, BN = 64, BK = 128 / sizeof(T), NW = 4, NTHR = 256, S = 6;
@@ -489,10 +486,12 @@ __global__ __launch_bounds__(Few<T>::NTHR, 2) void mm_few_kernel(train::MmArgs p
     const int k = min(kt, KT - 1);
 #pragma unroll
     for (int u = 0; u < C::NA; u++) dma(sa.r, at + (wave + C::NW * u) * 1024, sa.off[u] | m, (uint32_t)k * sa.step);
+    if (t.once) {
 #pragma unroll
-    for (int u = 0; u < C::NBL; u++) {
-      if (t.once) dma_once(sb.r, at + C::A_BYTES + (wave + C::NW * u) * 1024, sb.off[u] | mb, (uint32_t)k * sb.step);
-      else dma(sb.r, at + C::A_BYTES + (wave + C::NW * u) * 1024, sb.off[u] | mb, (uint32_t)k * sb.step);
+      for (int u = 0; u < C::NBL; u++) dma_once(sb.r, at + C::A_BYTES + (wave + C::NW * u) * 1024, sb.off[u] | mb, (uint32_t)k * sb.step);
+    } else {
+#pragma unroll
+      for (int u = 0; u < C::NBL; u++) dma(sb.r, at + C::A_BYTES + (wave + C::NW * u) * 1024, sb.off[u] | mb, (uint32_t)k * sb.step);
     }
     slot = slot + 1 == C::S ? 0 : slot + 1;
   };
