@@ -101,8 +101,11 @@ def block_forward(dev: dict, x: torch.Tensor, stream=None):
 def block_backward(dev: dict, saved: dict, d_out: torch.Tensor, grads: Optional[dict] = None, dtype=torch.float32,
                    stream=None) -> dict:
     """Gradients of block_forward for ``d_out`` [T, H] -> dict(dx, w_gate_up, w_down, w_router, bias, norm_pre, norm_post,
-    gate), None for what the block has not.  ``grads``: the dict of an earlier call, whose expert gradients (of ``dtype``; by
-    far the largest) are added to in place; the others are new in each call."""
+    gate), None for what the block has not.
+
+    ``grads``: the dict of an earlier call.  Its w_gate_up and w_down (of ``dtype``; by far the largest) are added to in place
+    and come back as the sums.  All other entries are of this call alone, with ``grads`` too: who accumulates over calls
+    adds those up, before the earlier dict is let go."""
     _check(dev)
     scale, act = dev.get("scale", 1.0), saved["x"].dtype
     with _on(d_out):

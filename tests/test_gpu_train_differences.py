@@ -41,3 +41,18 @@ def test_backward_agrees_with_differences_of_64_bits(gate):
             # fp32 gradients: as the block's test has it, relative in the 2-norm; projected on a unit vector the error is at most
             # that of the whole
             assert abs(num - float((grad * v).sum())) < 3 * TOL[torch.float32] * size, (name, along, num)
+
+
+def test_what_is_added_to_and_what_is_of_one_call():
+    """With an earlier call's dict the experts' gradients become sums in place, every other entry is this call's alone."""
+    cfg = LayerConfig("acc", T=12, H=64, E=4, k=2, I=32, act="f32", wdt="f32", seed=42, w_std=0.2)
+    dev, x, d_out = block(cfg)
+    _, saved = train.block_forward(dev, x)
+    first = train.block_backward(dev, saved, d_out)
+    kept = {n: t.clone() for n, t in first.items()}
+    second = train.block_backward(dev, saved, d_out, grads=first)
+    for n in NAMES:
+        if n in ("w_gate_up", "w_down"):
+            assert second[n] is first[n] and torch.equal(second[n], 2 * kept[n])  # the same fp32 sums twice: exact
+        else:
+            assert second[n] is not first[n] and torch.equal(second[n], kept[n]) and torch.equal(first[n], kept[n])
