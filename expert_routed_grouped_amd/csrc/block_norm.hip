@@ -10,9 +10,9 @@
 //   q = sum gate w_post yh (dx' + r dn w_next) - (r c / H) sum gate w_post yh xh.
 //
 // A workgroup holds a row in registers: every array is read once.  The column sums of the backward pass are kept per
-// workgroup over its rows and joined by a second launch, in a fixed order.  Bound by memory: 6000 x 4096, bf16 and an fp32 y, 45 us
-// forward (5.4 TB/s), 79 backward (5.0); rows of more than 8192 values (odd ones: 4096) do not
-// fit in the backward pass's registers and spill.
+// workgroup over its rows and joined by a second launch, in a fixed order.  Bound by memory: 6000 x 4096, bf16 and an fp32 y, 39 to 46 us
+// forward (6.3 to 5.3 TB/s), 79 backward (5.0).  Rows of more than 8192 values (odd ones: 4096) do not fit in the backward pass's registers
+// and spill, odd ones of more than 8192 in the forward pass too: 3000 x 16384 100 and 543 us, 3000 x 16383 3310 and 1730.
 #include "train.h"
 
 #include <type_traits>

@@ -9,8 +9,9 @@
 // are turned (below), so that the four rows of two neighbouring pieces, which half a wave reads at once, meet all 64 banks.
 //
 // Large tiles are 256 x 256 outputs, eight waves of 128 x 64: rows times matrix take 64 values of the contraction a step, weight
-// gradients 32.  Bound by power: 6000 tokens x 8 of 128 experts, 1536 x 4096, run at 1.9 GHz, 639 to 657 us (0.92 to 0.945 PFLOP/s),
-// weight gradients of the same size 740 to 752 us (0.80 to 0.82; 1.6 GB of results).  Few rows an expert take tiles
+// gradients 32.  6000 tokens x 8 of 128 experts, 1536 x 4096, take 639 to 662 us (0.91 to 0.945 PFLOP/s), weight gradients of the same
+// size 716 to 765 (0.79 to 0.84; 1.6 GB of results).  Power holds the clock near 1.9 GHz, as in a dense library product; the matrix units are
+// busy in 0.55 and 0.41 of the cycles (0.70 there), as all waves load, wait, multiply and store in step.  Few rows an expert take tiles
 // of their own (mm_few_kernel; also fp32).
 #include "grouped_tiles.h"
 

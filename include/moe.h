@@ -660,7 +660,8 @@ int moe_grouped_mm(const void *a, const int32_t *row_index, int a_rows, const vo
 /* moe_grouped_wgrad flags */
 #define MOE_WGRAD_ADD 1u /* add to dw instead of overwriting it */
 
-/* Bytes of workspace moe_grouped_wgrad needs (partial sums where few tiles share many rows; else 0). */
+/* Bytes of workspace moe_grouped_wgrad needs (partial sums where few tiles share many rows; else 0).  The type is checked;
+ * the sums are fp32 whatever it is. */
 size_t moe_grouped_wgrad_workspace_size(int E_loc, int R_cap, int M, int N, int dtype);
 
 /*
@@ -671,7 +672,7 @@ size_t moe_grouped_wgrad_workspace_size(int E_loc, int R_cap, int M, int N, int 
  *
  * For a projection out = W a: a is the gradient of its output, b its input.  a [a_rows, M] and b [b_rows, N] of
  * type ``dtype`` (MOE_BF16 or MOE_F32), dw [E_loc, M, N] of type dw_dtype (MOE_BF16 or MOE_F32; MOE_F32 with MOE_F32
- * operands).  Products are summed in fp32, in an order that the sizes alone fix; with MOE_WGRAD_ADD dw is added in
+ * operands).  Products are summed in fp32, in an order that the sizes and the offsets fix; with MOE_WGRAD_ADD dw is added in
  * fp32 and the sum rounded once.  Every matrix is written, those of experts without a row with zeros (or left as
  * they are with MOE_WGRAD_ADD).  Index and size rules as in moe_grouped_mm.  workspace: at least
  * moe_grouped_wgrad_workspace_size(...) bytes, 256-byte aligned, contents free before and after.
@@ -753,7 +754,8 @@ int moe_block_norm(const void *x, int x_dtype, const void *y, int y_dtype, const
                    const void *gate, int w_dtype, int gate_kind, float scale, float eps, int T, int H, void *x_out, void *n,
                    float *rstd_next, float *rstd_post, void *stream);
 
-/* Bytes of workspace moe_block_norm_backward needs for dw_next, dw_post and a channel gate's gradient (0 for few rows). */
+/* Bytes of workspace moe_block_norm_backward needs for dw_next, dw_post and a channel gate's gradient (0 for few rows).
+ * Depends on both. */
 size_t moe_block_norm_backward_workspace_size(int T, int H);
 
 /*
@@ -768,7 +770,7 @@ size_t moe_block_norm_backward_workspace_size(int T, int H);
  * dx of type x_dtype, dy of type dy_dtype (MOE_BF16 or MOE_F32).  Outputs that are NULL are not computed.  dx may be dx_out or dn itself.
  * dx_out and dn are of type x_dtype; not both NULL.  workspace (for dw_next, dw_post and a channel gate): at least
  * moe_block_norm_backward_workspace_size(T, H) bytes, 256-byte aligned, contents free.  The sums over t have an order
- * that T alone fixes.  T == 0 writes zeros to dw_next, dw_post and a channel gate's gradient.
+ * that T and H fix.  T == 0 writes zeros to dw_next, dw_post and a channel gate's gradient.
  */
 int moe_block_norm_backward(const void *x_out, int x_dtype, const void *y, int y_dtype, const void *w_next,
                             const void *w_post, const void *gate, int w_dtype, int gate_kind, float scale,
