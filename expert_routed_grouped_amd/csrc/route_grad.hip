@@ -144,7 +144,7 @@ __global__ __launch_bounds__(THR) void route_grad_kernel(RouteGradArgs a, int pi
   __shared__ float buf[THR * N > THR / 256 * 96 ? THR * N : THR / 256 * 96];
   const int b = train::block_of(), weights = a.E * pieces;
   if (b < weights) weight_part<T, N, THR>(a, b / pieces, b % pieces, buf);
-  else token_part<T, TR, TO, N, THR>(a, b - weights, buf);
+  else if (a.dx) token_part<T, TR, TO, N, THR>(a, b - weights, buf);  // without dx: workgroups too many of a last row
 }
 
 template <typename T, typename TR, typename TO, int N, int THR>

@@ -89,3 +89,24 @@ def test_wgrad_of_many_columns():
     a, b = randn(gen(7), E, 1, dtype=BF), randn(gen(8), E, N, dtype=BF)
     dw = moe.moe_grouped_wgrad(a, b, R.offsets_of([1] * E))
     assert torch.equal(dw.view(E, N), a * b)
+
+
+def test_route_backward_of_the_weight_alone():
+    """More pieces of odd rows than one row of workgroups takes, and no dx: the workgroups too many have nothing to write."""
+    T, E, k, H = 32769, 1024, 32, 64 * 4096 + 1
+    at = torch.arange(T, device=DEV)[:, None]
+    ids = ((at + 32 * torch.arange(k, device=DEV)) % E).int()
+    gates, dg = torch.full((T, k), 1 / 32, device=DEV), torch.zeros((T, k), device=DEV)
+    t = T - 3
+    dg[t, 0] = 32.0  # dl = (32 - 1) / 32, and (0 - 1) / 32 for the token's other experts
+    x = torch.ones((T, H), dtype=BF, device=DEV)
+    perm = moe.moe_permute(ids, gates, E, 0, E)
+    dw, db = torch.full((E, H), 7.0, device=DEV), torch.full((E,), 7.0, device=DEV)
+    p = lambda v: v.data_ptr()  # noqa: E731
+    assert moe.lib().moe_route_backward(p(ids), p(gates), p(dg), T, k, E, H, p(x), None, moe.MOE_BF16, p(perm["offsets"]),
+                                        p(perm["row_token"]), None, 0, None, 0, None, 0, p(dw), p(db),
+                                        torch.cuda.current_stream().cuda_stream) == 0
+    want = torch.zeros(E, device=DEV)
+    want[ids[t].long()] = -1 / 32
+    want[int(ids[t, 0])] = 31 / 32
+    assert torch.equal(db, want) and torch.equal(dw, want[:, None].expand(E, H))
